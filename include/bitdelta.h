@@ -433,6 +433,124 @@ int32_t bitdelta_residency_state(bitdelta_residency* r, int32_t variant);
 /* Bytes held by resident and loading variants, or -1 for a null manager. */
 int64_t bitdelta_residency_used_bytes(bitdelta_residency* r);
 
+/*
+ * ---- Attention over a paged cache -------------------------------------------------------------
+ *
+ * Between the linears of a decoder block each token attends the keys and values of its own
+ * sequence.  Those live in pages: page p holds page_size tokens of kv_heads heads, token t of a
+ * sequence sits in slot t % page_size of page table[t / page_size].  For query head h of a
+ * sequence's query row q and the set J of keys it sees (kv head h / (heads / kv_heads)):
+ *
+ *     s_j = scale * k_scale * (q . k_j)           lse = ln sum_{j in J} exp(s_j)
+ *     out = v_scale * sum_{j in J} exp(s_j - lse) * v_j
+ *
+ * An empty J gives out = 0 and lse = -inf.  Scores, maxima and sums are fp32; the weights enter
+ * the product with the values as bf16; out is rounded to bf16 once.  Results do not depend on
+ * timing: every sum is taken in a fixed order.
+ *
+ * Device tables cannot be checked before a kernel runs, so the kernels check them: a length below
+ * 0 counts as 0 and one beyond its table row as the row's capacity, and a key whose table entry
+ * is not in [0, num_pages) is absent (no query sees it).  What the cache holds outside the keys a
+ * call's queries see (beyond the lengths, before the window) is never used, NaN included.
+ *
+ * Limits (else UNSUPPORTED): head_dim 64 or 128, at most 64 query heads per kv head, 1024
+ * sequences per call, 2^30 tokens per sequence.
+ */
+#define BITDELTA_ATTEND_MAX_SEQS 1024
+#define BITDELTA_ATTEND_MAX_GROUP 64
+
+typedef enum {
+  BITDELTA_KV_BF16 = 0,
+  BITDELTA_KV_FP8 = 1 /* OCP e4m3 */
+} bitdelta_kv_dtype;
+
+typedef struct {
+  const void* k; /* [dev] keys, 16-byte aligned                                                 */
+  const void* v; /* [dev] values, 16-byte aligned                                               */
+  int32_t dtype; /* bitdelta_kv_dtype                                                           */
+  int32_t num_pages;
+  int32_t page_size; /* tokens per page, any number >= 1                                        */
+  int32_t kv_heads;
+  int32_t head_dim;
+  /* strides in elements, each a multiple of 16 bytes; the head_dim values of a row are
+   * contiguous */
+  int64_t k_stride_page, k_stride_token, k_stride_head;
+  int64_t v_stride_page, v_stride_token, v_stride_head;
+  float k_scale, v_scale; /* what a stored value is multiplied by; finite, > 0                  */
+} bitdelta_kv_cache;
+
+/* Query and output rows: token t, head h at t * stride_token + h * stride_head (in elements; q's
+ * multiples of 8, out's of 4), head_dim contiguous values.  q is 16-byte, out 8-byte aligned. */
+typedef struct {
+  const void* q; /* [dev] bf16                                                                  */
+  void* out;     /* [dev] bf16                                                                  */
+  float* lse;    /* [dev] float32 [tokens][heads], or NULL                                      */
+  int64_t tokens;
+  int32_t heads;
+  int64_t q_stride_token, q_stride_head;
+  int64_t out_stride_token, out_stride_head;
+  float scale; /* finite, > 0; usually 1 / sqrt(head_dim)                                       */
+} bitdelta_attend_rows;
+
+/*
+ * bitdelta_attend_shared — decode attention, one new token per sequence, for a batch whose
+ * sequences share prefixes by segment: sequence b of segment g (seg_offsets as in
+ * bitdelta_plan_segments: the requests of one variant share that variant's prompt) sees the
+ * prefix_lens[g] prefix keys of row g of prefix_table, then its own lens[b] keys of row b of
+ * table.  A segment's prefix is read once for all its sequences.
+ *
+ *   rows          q, out: tokens = the number of sequences, in segment order.
+ *   table         [dev] int32 [tokens][table_width];  lens [dev] int32 [tokens].
+ *   prefix_table  [dev] int32 [num_segments][prefix_width];  prefix_lens [dev] int32
+ *                 [num_segments].  prefix_width may be 0 (no prefixes).
+ *   seg_offsets   [host] int32 [num_segments + 1], 0 = first <= ... <= last = tokens;
+ *                 num_segments <= BITDELTA_MAX_SEGMENTS.
+ *   workspace     [dev] at least bitdelta_attend_shared_workspace_bytes(...) bytes, 16-byte
+ *                 aligned (may be NULL when that is 0); as for bitdelta_matmul.
+ * tokens = 0 is a no-op.  Errors: INVALID_ARG, SHAPE, ALIGNMENT, WORKSPACE, UNSUPPORTED, HIP.
+ */
+bitdelta_status bitdelta_attend_shared(const bitdelta_attend_rows* rows,
+                                       const bitdelta_kv_cache* cache, const int32_t* table,
+                                       int32_t table_width, const int32_t* lens,
+                                       const int32_t* prefix_table, int32_t prefix_width,
+                                       const int32_t* prefix_lens, const int32_t* seg_offsets,
+                                       int32_t num_segments, void* workspace,
+                                       size_t workspace_bytes, bitdelta_stream stream);
+/* Workspace of that call (0 for arguments it would refuse). */
+size_t bitdelta_attend_shared_workspace_bytes(int64_t tokens, int32_t heads,
+                                              const bitdelta_kv_cache* cache, int32_t table_width,
+                                              int32_t prefix_width, const int32_t* seg_offsets,
+                                              int32_t num_segments);
+
+/*
+ * bitdelta_attend_window — causal attention of the last tokens of each sequence with a sliding
+ * window and first tokens that stay visible.  Sequence b has lens[b] keys in the cache, its new
+ * tokens among them as the last ones; its query rows are q_offsets[b] .. q_offsets[b + 1] - 1, of
+ * which row q_offsets[b + 1] - 1 is the token at position lens[b] - 1.  The token at position p
+ * sees key j iff j <= p and (p - j < window or j < sinks).  A window of at least lens[b] is plain
+ * causal attention.
+ *
+ *   q_offsets   [dev] int32 [batch + 1], ascending, or NULL: one token per sequence (decode;
+ *               then rows->tokens = batch and max_q_len = 1).
+ *   max_q_len   [host] at least the longest chunk of the call; query rows beyond it, or outside
+ *               [0, tokens), are not computed.
+ *   window      >= 1; sinks >= 0.
+ *   workspace   as above, bitdelta_attend_window_workspace_bytes(...).
+ * batch = 0 or tokens = 0 is a no-op.  Errors as bitdelta_attend_shared.
+ */
+bitdelta_status bitdelta_attend_window(const bitdelta_attend_rows* rows,
+                                       const bitdelta_kv_cache* cache, int32_t batch,
+                                       const int32_t* table, int32_t table_width,
+                                       const int32_t* lens, const int32_t* q_offsets,
+                                       int32_t max_q_len, int32_t window, int32_t sinks,
+                                       void* workspace, size_t workspace_bytes,
+                                       bitdelta_stream stream);
+/* Workspace of that call (0 for arguments it would refuse). */
+size_t bitdelta_attend_window_workspace_bytes(int64_t tokens, int32_t heads,
+                                              const bitdelta_kv_cache* cache, int32_t batch,
+                                              int32_t table_width, int32_t max_q_len,
+                                              int32_t window, int32_t sinks);
+
 #ifdef __cplusplus
 }
 #endif

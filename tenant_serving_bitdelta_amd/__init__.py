@@ -17,7 +17,8 @@ __all__ = [
     "compress_rows", "compress_rows_workspace_bytes", "compress_from_weights",
     "compress", "plan_segments", "matmul", "matmul_grouped", "auto_path", "PATHS",
     "matmul_workspace_bytes", "sign_words_t128", "reconstruct", "upload_variant", "Residency",
-    "matmul_grouped_noalloc", "NOALLOC_SCRATCH_BYTES",
+    "matmul_grouped_noalloc", "NOALLOC_SCRATCH_BYTES", "attend_shared",
+    "attend_shared_workspace_bytes", "attend_window", "attend_window_workspace_bytes",
 ]
 
 ABI_VERSION = 7
@@ -51,6 +52,28 @@ class _Problem(ctypes.Structure):
         ("x", ctypes.c_void_p), ("w_base", ctypes.c_void_p), ("y", ctypes.c_void_p),
         ("d_out", ctypes.c_int64), ("d_in", ctypes.c_int64),
         ("variants", ctypes.POINTER(_Variant)), ("num_variants", ctypes.c_int32),
+    ]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("k_stride_page", ctypes.c_int64), ("k_stride_token", ctypes.c_int64),
+        ("k_stride_head", ctypes.c_int64), ("v_stride_page", ctypes.c_int64),
+        ("v_stride_token", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
+        ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+    ]
+
+
+class _AttendRows(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("tokens", ctypes.c_int64), ("heads", ctypes.c_int32),
+        ("q_stride_token", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+        ("out_stride_token", ctypes.c_int64), ("out_stride_head", ctypes.c_int64),
+        ("scale", ctypes.c_float),
     ]
 
 
@@ -152,6 +175,25 @@ def _lib():
                                                       ctypes.c_int32]
         L.bitdelta_auto_path.restype = ctypes.c_int32
         L.bitdelta_auto_path.argtypes = [ctypes.c_int64, _i32p, _i32p, ctypes.c_int32]
+        rows_p, cache_p = ctypes.POINTER(_AttendRows), ctypes.POINTER(_KvCache)
+        L.bitdelta_attend_shared.restype = ctypes.c_int
+        L.bitdelta_attend_shared.argtypes = [rows_p, cache_p, ctypes.c_void_p, ctypes.c_int32,
+                                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                             ctypes.c_void_p, _i32p, ctypes.c_int32,
+                                             ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        L.bitdelta_attend_shared_workspace_bytes.restype = ctypes.c_size_t
+        L.bitdelta_attend_shared_workspace_bytes.argtypes = [
+            ctypes.c_int64, ctypes.c_int32, cache_p, ctypes.c_int32, ctypes.c_int32, _i32p,
+            ctypes.c_int32]
+        L.bitdelta_attend_window.restype = ctypes.c_int
+        L.bitdelta_attend_window.argtypes = [rows_p, cache_p, ctypes.c_int32, ctypes.c_void_p,
+                                             ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                             ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        L.bitdelta_attend_window_workspace_bytes.restype = ctypes.c_size_t
+        L.bitdelta_attend_window_workspace_bytes.argtypes = [
+            ctypes.c_int64, ctypes.c_int32, cache_p, ctypes.c_int32, ctypes.c_int32,
+            ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]
         _LIB = L
     return _LIB
 
@@ -187,6 +229,13 @@ def _temp(nbytes, device, stream, dtype_name="uint8"):
     if stream is not None and int(stream) != torch.cuda.current_stream(device).cuda_stream:
         t.record_stream(torch.cuda.ExternalStream(int(stream), device=device))
     return t
+
+
+def _on_stream(t, stream):
+    """Record a result made on torch's current stream as in use on the call's own."""
+    import torch
+    if stream is not None and int(stream) != torch.cuda.current_stream(t.device).cuda_stream:
+        t.record_stream(torch.cuda.ExternalStream(int(stream), device=t.device))
 
 
 def _numel_at_least(t, n, what):
@@ -597,3 +646,165 @@ def upload_variant(host_words, host_alpha, d_out: int, d_in: int, words=None, ti
                                           d_in, wptr, tptr, aptr, sptr, sbytes, _stream(stream)),
            "bitdelta_upload_variant")
     return words, tiled, alpha
+
+
+# ---------------------------------------------------------------------------------------------
+# Attention over a paged cache
+# ---------------------------------------------------------------------------------------------
+
+def _kv_cache(k_pages, v_pages, k_scale, v_scale):
+    """bitdelta_kv_cache of two [pages, page_size, kv_heads, head_dim] tensors (bf16 or
+    float8_e4m3fn), any strides but contiguous rows."""
+    import torch
+    dtypes = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+    for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{what} must be a CUDA/HIP torch tensor")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{what} must be torch.bfloat16 or torch.float8_e4m3fn, got {t.dtype}")
+        if t.dim() != 4:
+            raise ValueError(f"{what} must be [pages, page_size, kv_heads, head_dim]")
+        if t.shape[3] > 1 and t.stride(3) != 1:
+            raise ValueError(f"{what} must have contiguous rows")
+    if k_pages.dtype != v_pages.dtype or k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have one shape and type")
+    if k_pages.device != v_pages.device:
+        raise ValueError("k_pages and v_pages must be on one device")
+    c = _KvCache()
+    c.k, c.v, c.dtype = k_pages.data_ptr(), v_pages.data_ptr(), dtypes[k_pages.dtype]
+    c.num_pages, c.page_size, c.kv_heads, c.head_dim = (int(n) for n in k_pages.shape)
+    c.k_stride_page, c.k_stride_token, c.k_stride_head = k_pages.stride()[:3]
+    c.v_stride_page, c.v_stride_token, c.v_stride_head = v_pages.stride()[:3]
+    c.k_scale, c.v_scale = float(k_scale), float(v_scale)
+    return c
+
+
+def _attend_rows(q, cache, out, lse, return_lse, scale, stream):
+    """(bitdelta_attend_rows, out, lse) for q [tokens, heads, head_dim]; out and lse are made here
+    when missing."""
+    import torch
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA/HIP torch tensor")
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be torch.bfloat16, got {q.dtype}")
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [tokens, heads, {cache.head_dim}], not {tuple(q.shape)}")
+    if q.stride(2) != 1:
+        raise ValueError("q must have contiguous rows")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        _on_stream(out, stream)
+    if not out.is_cuda or out.dtype != torch.bfloat16:
+        raise TypeError("out must be a torch.bfloat16 CUDA/HIP tensor")
+    _check_shape(out, q.shape, "out")
+    if out.stride(2) != 1:
+        raise ValueError("out must have contiguous rows")
+    if lse is None and return_lse:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        _on_stream(lse, stream)
+    r = _AttendRows()
+    r.q, r.out = q.data_ptr(), out.data_ptr()
+    if lse is not None:
+        _check_shape(lse, q.shape[:2], "lse")
+        r.lse = _dev(lse, "torch.float32", "lse")
+    r.tokens, r.heads = int(q.shape[0]), int(q.shape[1])
+    r.q_stride_token, r.q_stride_head = q.stride()[:2]
+    r.out_stride_token, r.out_stride_head = out.stride()[:2]
+    r.scale = float(cache.head_dim ** -0.5 if scale is None else scale)
+    return r, out, lse
+
+
+def _table(t, lens, n, what):
+    """(pointer, width, lens pointer) of an int32 page table [n, width] and its lengths [n]."""
+    if t.dim() != 2 or t.shape[0] != n:
+        raise ValueError(f"{what} must be [{n}, pages], not {tuple(t.shape)}")
+    _check_shape(lens, (n,), f"{what}'s lengths")
+    return (_dev(t, "torch.int32", what), int(t.shape[1]),
+            _dev(lens, "torch.int32", f"{what}'s lengths"))
+
+
+def attend_shared_workspace_bytes(k_pages, heads, table, prefix_table, seg_offsets) -> int:
+    """Device workspace an attend_shared call with these tables needs (bytes, 0 if none)."""
+    offs, offs_p = _i32(seg_offsets)
+    c = _kv_cache(k_pages, k_pages, 1.0, 1.0)
+    pwidth = 0 if prefix_table is None else int(prefix_table.shape[1])
+    return int(_lib().bitdelta_attend_shared_workspace_bytes(
+        int(table.shape[0]), heads, ctypes.byref(c), int(table.shape[1]), pwidth, offs_p,
+        offs.size - 1))
+
+
+def attend_shared(q, k_pages, v_pages, table, lens, prefix_table, prefix_lens, seg_offsets,
+                  scale=None, k_scale=1.0, v_scale=1.0, out=None, lse=None, return_lse=False,
+                  workspace=None, stream=None):
+    """Decode attention, one new token per sequence, over a paged cache whose prefixes are shared
+    by segment: sequence b of segment g (``seg_offsets`` as plan_segments returns them) sees the
+    first ``prefix_lens[g]`` tokens of ``prefix_table[g]``, then the first ``lens[b]`` of
+    ``table[b]``.
+
+    ``q``: bf16 [batch, heads, head_dim]; ``k_pages`` / ``v_pages``: [pages, page_size, kv_heads,
+    head_dim] bf16 or float8_e4m3fn (each stored value times ``k_scale`` / ``v_scale``), any
+    strides but contiguous rows; ``table`` int32 [batch, n], ``lens`` int32 [batch],
+    ``prefix_table`` int32 [segments, m] and ``prefix_lens`` int32 [segments] (both None: no
+    prefixes), on the device.  Returns bf16 ``out`` like q, and with ``return_lse`` (or ``lse``
+    given) also the natural log of each row's softmax sum, float32 [batch, heads].  A sequence
+    with no keys gives zeros and -inf."""
+    offs, offs_p = _i32(seg_offsets)
+    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale)
+    rows, out, lse = _attend_rows(q, cache, out, lse, return_lse, scale, stream)
+    tptr, width, lptr = _table(table, lens, rows.tokens, "table")
+    if offs.size < 1:
+        raise ValueError("seg_offsets must hold at least one offset")
+    nseg = offs.size - 1
+    if (prefix_table is None) != (prefix_lens is None):
+        raise ValueError("give prefix_table and prefix_lens, or neither")
+    if prefix_table is None:
+        # no prefixes: the batch is one segment without keys (its length pointer is never read
+        # past a table of width 0, which holds none)
+        pptr, pwidth, plptr = None, 0, lptr
+        offs, offs_p = _i32([0, rows.tokens])
+        nseg = 1
+    else:
+        pptr, pwidth, plptr = _table(prefix_table, prefix_lens, nseg, "prefix_table")
+    need = 0 if workspace is not None else int(_lib().bitdelta_attend_shared_workspace_bytes(
+        rows.tokens, rows.heads, ctypes.byref(cache), width, pwidth, offs_p, nseg))
+    ws_ptr, ws_bytes, ws = _workspace(workspace, need, q.device, stream)
+    _check(_lib().bitdelta_attend_shared(
+        ctypes.byref(rows), ctypes.byref(cache), tptr, width, lptr, pptr, pwidth, plptr, offs_p,
+        nseg, ws_ptr, ws_bytes, _stream(stream)), "bitdelta_attend_shared")
+    return out if lse is None else (out, lse)
+
+
+def attend_window_workspace_bytes(k_pages, heads, table, tokens, max_q_len, window, sinks) -> int:
+    """Device workspace an attend_window call of these sizes needs (bytes, 0 if none)."""
+    c = _kv_cache(k_pages, k_pages, 1.0, 1.0)
+    return int(_lib().bitdelta_attend_window_workspace_bytes(
+        tokens, heads, ctypes.byref(c), int(table.shape[0]), int(table.shape[1]), max_q_len,
+        window, sinks))
+
+
+def attend_window(q, k_pages, v_pages, table, lens, window, sinks=0, q_offsets=None, max_q_len=1,
+                  scale=None, k_scale=1.0, v_scale=1.0, out=None, lse=None, return_lse=False,
+                  workspace=None, stream=None):
+    """Causal attention of each sequence's last tokens over a paged cache, with a sliding window
+    and first tokens that stay visible: the token at position p sees key j iff j <= p and
+    (p - j < ``window`` or j < ``sinks``).  Sequence b holds ``lens[b]`` keys, its new tokens
+    among them as the last ones.
+
+    ``q``: bf16 [tokens, heads, head_dim]; sequence b's rows are q_offsets[b] .. q_offsets[b + 1]
+    (int32 [batch + 1] on the device; None: one token per sequence), none longer than
+    ``max_q_len``.  Cache, tables, scales and results as for attend_shared."""
+    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale)
+    rows, out, lse = _attend_rows(q, cache, out, lse, return_lse, scale, stream)
+    batch = int(lens.shape[0]) if lens.dim() == 1 else -1
+    tptr, width, lptr = _table(table, lens, batch, "table")
+    optr = None
+    if q_offsets is not None:
+        _check_shape(q_offsets, (batch + 1,), "q_offsets")
+        optr = _dev(q_offsets, "torch.int32", "q_offsets")
+    need = 0 if workspace is not None else int(_lib().bitdelta_attend_window_workspace_bytes(
+        rows.tokens, rows.heads, ctypes.byref(cache), batch, width, max_q_len, window, sinks))
+    ws_ptr, ws_bytes, ws = _workspace(workspace, need, q.device, stream)
+    _check(_lib().bitdelta_attend_window(
+        ctypes.byref(rows), ctypes.byref(cache), batch, tptr, width, lptr, optr, max_q_len, window,
+        sinks, ws_ptr, ws_bytes, _stream(stream)), "bitdelta_attend_window")
+    return out if lse is None else (out, lse)

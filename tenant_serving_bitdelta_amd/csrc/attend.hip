@@ -1,0 +1,1117 @@
+// Attention over a paged cache: decode with prefixes shared by the segments of a batch, and causal
+// attention with a sliding window and first tokens that stay visible.
+//
+// Mathematics, per query row q of kv head h and its visible keys j:
+//   s_j = c * (q . k_j),  c = scale * k_scale * log2(e)
+//   m = max_j s_j,  l = sum_j 2^(s_j - m),  o = v_scale / l * sum_j 2^(s_j - m) v_j
+// in one pass: the running maximum m and sum l are kept in fp32 per row, and the fp32 output sums
+// are rescaled when m grows.  Scores are computed transposed, S^T = K Q^T, so that the matrix
+// instruction leaves each lane with scores of ONE query row: the softmax needs no shared memory,
+// and the weights are already the B operand of O^T = V^T P^T.  The order of the keys inside a
+// product is free as long as both operands agree, so the A operand V^T is read from LDS
+// (transposed reads) in the key order the scores came out in.
+#include <type_traits>
+
+#include "attend.h"
+#include "bd_internal.h"
+
+namespace bd {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kLn2 = 0.6931471805599453f;
+// Output sums are rescaled only when a row's maximum grows by more than this many powers of two:
+// weights then stay below 2^8, far from fp32 overflow, and their bf16 rounding is relative.
+constexpr float kRescale = 8.0f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// max over the two halves of a wave, in every lane
+__device__ __forceinline__ float half_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// the same over the lanes l, l ^ 16
+__device__ __forceinline__ float row_max(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float row_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ unsigned pack_bf16(float a, float b) {
+  f32x2 f;
+  f[0] = a;
+  f[1] = b;
+  return __builtin_bit_cast(unsigned, __builtin_convertvector(f, bf16x2));
+}
+
+// 4 e4m3 values -> 4 bf16, exact
+__device__ __forceinline__ u32x2 fp8x4_to_bf16(unsigned v) {
+  u32x2 r;
+  r[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
+  r[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true));
+  return r;
+}
+__device__ __forceinline__ u32x4 fp8x8_to_bf16(unsigned a, unsigned b) {
+  const u32x2 x = fp8x4_to_bf16(a), y = fp8x4_to_bf16(b);
+  return u32x4{x[0], x[1], y[0], y[1]};
+}
+
+// Is any of 8 bf16 (16 e4m3) values infinite or NaN?
+template <bool FP8>
+__device__ __forceinline__ bool not_finite(const u32x4& v) {
+  unsigned bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned x = v[i];
+    if constexpr (FP8) {
+      // e4m3 has no infinity; NaN is all ones below the sign
+      const unsigned y = ~x & 0x7F7F7F7Fu;  // a zero byte marks a NaN
+      bad |= (y - 0x01010101u) & ~y & 0x80808080u;
+    } else {
+      bad |= (unsigned)((x & 0x7F80u) == 0x7F80u) | (unsigned)((x & 0x7F800000u) == 0x7F800000u);
+    }
+  }
+  return bad != 0;
+}
+// v with value k (0 .. 7) cleared where bit k of keep is
+__device__ __forceinline__ u32x4 keep_values(const u32x4& v, unsigned keep) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned m = ((keep >> (2 * i)) & 1u ? 0xFFFFu : 0u) |
+                       ((keep >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
+    const unsigned x = v[i];
+    r[i] = x & m;
+  }
+  return r;
+}
+
+__device__ __forceinline__ u32x2 lds_read_tr(const unsigned char* p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                       (lds_s16x4*)(const_cast<unsigned char*>(p))));
+}
+
+__device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Byte offset of 16-byte unit u of row r in a V tile (D bf16 a row).  A transposed read takes 32
+// bytes of each of 8 consecutive rows at a time; the XOR spreads those over all banks.
+template <int D>
+__device__ __forceinline__ unsigned v_unit(int r, int u) {
+  const int x = D == 128 ? 2 * (r & 7) : 2 * ((r >> 1) & 3);
+  return (unsigned)(r * (D * 2) + ((u ^ x) << 4));
+}
+// The same for a K tile, whose reads take one 16-byte unit of 16 consecutive rows at a time.
+template <int D>
+__device__ __forceinline__ unsigned k_unit(int r, int u) {
+  const int x = D == 128 ? (r & 15) : ((r >> 1) & 7);
+  return (unsigned)(r * (D * 2) + ((u ^ x) << 4));
+}
+
+__device__ __forceinline__ int clamp_len(int len, int width, int page_size) {
+  const int64_t cap = (int64_t)width * page_size;
+  return len < 0 ? 0 : (len > cap ? (int)cap : len);
+}
+
+// Does the token at position pos see key vp of its list?  In vp, the list's second part ends at
+// pos + (na - lo) for this token and begins a window before; the first tokens are the vp below
+// min(sinks, pos + 1) (when lo < sinks the list has no gap, else the token sees all na of them).
+// Written without branches: one compare per bound.
+__device__ __forceinline__ bool sees(const KeyList& l, int pos, int window, int sinks, int vp) {
+  return ((unsigned)(pos + (l.na - l.lo) - vp) < (unsigned)window) | (vp < min(sinks, pos + 1));
+}
+
+// What one unit (sequence, kv head) of the row kernel reads and for which query rows.
+struct RowUnit {
+  KeyList keys;
+  int t0, nq;   // first token row of q, tokens
+  int p0;       // position of the first token (window op)
+};
+__device__ __forceinline__ RowUnit row_unit(const AttendArgs& a, int b) {
+  RowUnit u;
+  const int len = clamp_len(a.lens[b], a.width, a.cache.page_size);
+  const int32_t* row = a.table + (int64_t)b * a.width;
+  if (a.nseg > 0) {
+    u.t0 = b;
+    u.nq = 1;
+    u.p0 = 0;
+    u.keys = KeyList{row, row, a.width, a.width, 0, 0, len};
+    if (a.row_prefix) {
+      int g = 0;
+      while (g + 1 < a.nseg && a.seg_offsets[g + 1] <= b) ++g;
+      const int plen = clamp_len(a.prefix_lens[g], a.pwidth, a.cache.page_size);
+      u.keys.ta = a.prefix_table + (int64_t)g * a.pwidth;
+      u.keys.wa = a.pwidth;
+      u.keys.na = plen;
+      // positions of both parts together stay below 2^31 (checked on the host)
+      u.keys.n = plen + len;
+    }
+  } else {
+    int q0 = b, nq = 1;
+    if (a.q_offsets) {
+      q0 = a.q_offsets[b];
+      nq = a.q_offsets[b + 1] - q0;
+      nq = nq < 0 ? 0 : (nq > a.max_q ? a.max_q : nq);
+      if (q0 < 0 || q0 > a.tokens) nq = 0;
+      else if (nq > a.tokens - q0) nq = a.tokens - q0;
+    }
+    u.t0 = q0;
+    u.nq = nq;
+    u.p0 = len - nq;
+    u.keys = window_keys(row, a.width, len, u.p0, a.window, a.sinks);
+  }
+  return u;
+}
+__device__ __forceinline__ int row_steps(const RowUnit& u) {
+  return u.nq > 0 ? (u.keys.n + kRowStep - 1) / kRowStep : 0;
+}
+
+// Running sums of `count` values (value(i) >= 0) into scan[0 .. count] in LDS, by all threads of
+// the workgroup; scan[0] = 0.
+template <int kThreads, class F>
+__device__ void block_scan(int* scan, int* wave_sum, int count, F value) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (tid == 0) scan[0] = 0;
+  int carry = 0;
+  for (int base = 0; base < count; base += kThreads) {
+    const int i = base + tid;
+    int x = i < count ? value(i) : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(x, d, 64);
+      if (lane >= d) x += y;
+    }
+    if (lane == 63) wave_sum[wave] = x;
+    __syncthreads();
+    int before = carry, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) {
+      if (w < wave) before += wave_sum[w];
+      total += wave_sum[w];
+    }
+    if (i < count) scan[i + 1] = before + x;
+    carry += total;
+    __syncthreads();
+  }
+}
+// largest i with scan[i] <= x, for 0 <= x < scan[count]
+__device__ __forceinline__ int scan_find(const int* scan, int count, int x) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (scan[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Row kernel: up to 16 * NC query rows (the heads of one kv head, for one or a few tokens) against
+// a key list.  Bound by reading the cache: each of a workgroup's 4 waves takes 32 keys of a
+// 128-key step on its own (no barrier in the loop), its K rows straight from memory into operand
+// registers (4 lanes take 64 bytes of a row) and its V rows through 8 KiB of its own LDS.  The
+// waves' sums meet at the end of a piece.
+// ---------------------------------------------------------------------------------------------
+template <int D, bool FP8, int NC>
+struct RowLoop {
+  static constexpr int kLoads = FP8 ? D / 64 : D / 32;  // 16-byte loads of a row per lane
+  static constexpr int kSteps = D / 32;                 // matrix steps over D
+  static constexpr int kTiles = D / 16;                 // 16-row tiles of O^T
+
+  u32x4 q[NC][kSteps];
+  f32x4 o[NC][kTiles];
+  float m[NC], l[NC];
+  int pos[NC];   // the column's token position (window op with several tokens)
+  u32x4 kr[2][kLoads], vr[2][kLoads];
+  int id[2], slot[2], vp[2];
+  bool ok[2];
+
+  __device__ __forceinline__ void lookup(const AttendArgs& a, const KeyList& kl, int base, int j) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int p = base + 16 * r + j;
+      const int kp = key_position(kl, p);
+      const int page = page_quotient(kp < 0 ? 0 : kp, a.cache.div);
+      const int at = key_table_index(kl, p, page);
+      slot[r] = kp - page * a.cache.page_size;
+      // the entry is only checked when it is used: the load stays in flight
+      id[r] = at >= 0 ? (p < kl.na ? kl.ta : kl.tb)[at] : -1;
+    }
+  }
+  __device__ __forceinline__ void fetch(const AttendArgs& a, int h, int g) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      ok[r] = page_id_checked(id[r], a.cache.num_pages) >= 0;
+      if (ok[r]) {
+        const unsigned char* kp = a.cache.k + page_row_bytes(id[r], slot[r], a.cache.k_page, a.cache.k_token) +
+                                  (int64_t)h * a.cache.k_head + 16 * g;
+        const unsigned char* vp_ = a.cache.v + page_row_bytes(id[r], slot[r], a.cache.v_page, a.cache.v_token) +
+                                   (int64_t)h * a.cache.v_head + 16 * g;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) kr[r][i] = *reinterpret_cast<const u32x4*>(kp + 64 * i);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) vr[r][i] = *reinterpret_cast<const u32x4*>(vp_ + 64 * i);
+      } else {
+        // absent rows are zeros, so that what the memory holds there cannot reach the sums
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) kr[r][i] = vr[r][i] = u32x4{0, 0, 0, 0};
+      }
+    }
+  }
+};
+
+template <int D, bool FP8, int NC>
+__global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1))
+void attend_row_kernel(const AttendArgs a) {
+  using Loop = RowLoop<D, FP8, NC>;
+  constexpr int kWaveLds = kRowKeys * D * 2;
+  __shared__ __attribute__((aligned(16))) unsigned char vlds[kRowWaves * kWaveLds];
+  __shared__ float ml[kRowWaves][16][2];
+  __shared__ int scan[kAttendMaxSeqs + 1];
+  __shared__ int wave_sum[kRowWaves];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int j = lane & 15, g = lane >> 4;
+  unsigned char* const vl = vlds + wave * kWaveLds;
+
+  int64_t x, x_end, total = 0;
+  if (a.direct) {
+    x = 0;
+    x_end = 1;
+  } else {
+    block_scan<256>(scan, wave_sum, a.batch, [&](int b) { return row_steps(row_unit(a, b)); });
+    total = (int64_t)scan[a.batch] * a.kv_heads;
+    if (blockIdx.x == 0)
+      for (int i = tid; i <= a.batch; i += 256) a.scan[i] = scan[i];
+    const int workers = split_workers(total, a.workers);
+    if ((int)blockIdx.x >= workers) return;
+    x = split_begin(blockIdx.x, total, workers);
+    x_end = split_begin(blockIdx.x + 1, total, workers);
+  }
+
+  while (x < x_end) {
+    int b, h, s_begin, s_end;
+    RowUnit u;
+    if (a.direct) {
+      b = blockIdx.x / a.kv_heads;
+      h = blockIdx.x - b * a.kv_heads;
+      u = row_unit(a, b);
+      s_begin = 0;
+      s_end = row_steps(u);
+      x = x_end;
+    } else {
+      b = scan_find(scan, a.batch, (int)(x / a.kv_heads));
+      u = row_unit(a, b);
+      const int s = row_steps(u);
+      const int64_t x0 = (int64_t)scan[b] * a.kv_heads;
+      h = (int)((x - x0) / s);
+      s_begin = (int)(x - x0 - (int64_t)h * s);
+      s_end = (int)(x_end - x < s - s_begin ? s_begin + (x_end - x) : s);
+    }
+    const int rows = u.nq * a.group;
+    const KeyList kl = u.keys;
+    // with one token per unit every key of the list is visible to every row
+    const bool masked = u.nq > 1;
+
+    Loop w;
+    // ---- queries: column j of block c is row 16c + j, token (row / group), head (row % group)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int row = 16 * c + j;
+      const int t = row / a.group, hh = row - t * a.group;
+      w.pos[c] = u.p0 + t;
+      w.m[c] = kNegInf;
+      w.l[c] = 0.f;
+#pragma unroll
+      for (int i = 0; i < Loop::kTiles; ++i) w.o[c][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const uint16_t* qp = a.q + (int64_t)(u.t0 + t) * a.q_token + (int64_t)(h * a.group + hh) * a.q_head;
+#pragma unroll
+      for (int s = 0; s < Loop::kSteps; ++s) {
+        // the 8 dims of step s that K's register holds for this lane
+        const int d = FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
+        w.q[c][s] = row < rows ? *reinterpret_cast<const u32x4*>(qp + d) : u32x4{0, 0, 0, 0};
+      }
+    }
+
+    int base = s_begin * kRowStep + wave * kRowKeys;
+    const int end = s_end * kRowStep;
+    if (base < end) {
+      w.lookup(a, kl, base, j);
+      w.fetch(a, h, g);
+      if (base + kRowStep < end) w.lookup(a, kl, base + kRowStep, j);
+    }
+    for (; base < end; base += kRowStep) {
+      const bool ok0 = w.ok[0], ok1 = w.ok[1];
+      // keys of the tile that exist, bit (key): lanes 0..15 speak for keys 0..15 and 16..31
+      const unsigned valid = (unsigned)(__ballot(ok0) & 0xFFFFull) |
+                             ((unsigned)(__ballot(ok1) & 0xFFFFull) << 16);
+      // ---- V into LDS, scores from K
+      bool odd_values = false;
+      if (masked) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < Loop::kLoads; ++i) odd_values |= not_finite<FP8>(w.vr[r][i]);
+        odd_values = __any(odd_values);
+      }
+      f32x4 s[NC][2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int i = 0; i < Loop::kLoads; ++i) {
+          const int row = 16 * r + j;
+          if constexpr (FP8) {
+            const u32x4 v = w.vr[r][i];
+            *reinterpret_cast<u32x4*>(vl + v_unit<D>(row, 8 * i + 2 * g)) = fp8x8_to_bf16(v[0], v[1]);
+            *reinterpret_cast<u32x4*>(vl + v_unit<D>(row, 8 * i + 2 * g + 1)) = fp8x8_to_bf16(v[2], v[3]);
+          } else {
+            *reinterpret_cast<u32x4*>(vl + v_unit<D>(row, 4 * i + g)) = w.vr[r][i];
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) s[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < Loop::kLoads; ++i) {
+          const u32x4 kv = w.kr[r][i];
+          if constexpr (FP8) {
+            const u32x4 k0 = fp8x8_to_bf16(kv[0], kv[1]), k1 = fp8x8_to_bf16(kv[2], kv[3]);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              s[c][r] = mfma16(k0, w.q[c][2 * i], s[c][r]);
+              s[c][r] = mfma16(k1, w.q[c][2 * i + 1], s[c][r]);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) s[c][r] = mfma16(kv, w.q[c][i], s[c][r]);
+          }
+        }
+      }
+      // ---- the next tile's rows are on their way while this one is worked on
+      if (base + kRowStep < end) {
+        w.fetch(a, h, g);
+        if (base + 2 * kRowStep < end) w.lookup(a, kl, base + 2 * kRowStep, j);
+      }
+
+      // ---- mask: lane (j, g) holds keys 4g + i (s[.][0]) and 16 + 4g + i (s[.][1]) of column j
+      u32x4 p[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (valid != 0xFFFFFFFFu || masked) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = 16 * r + 4 * g + i;
+              bool seen = (valid >> key) & 1u;
+              if (masked) seen = seen & sees(kl, w.pos[c], a.window, a.sinks, base + key);
+              const float v = s[c][r][i];
+              s[c][r][i] = seen ? v : kNegInf;
+            }
+        }
+        float t = kNegInf;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = fmaxf(t, fmaxf(s[c][0][i], s[c][1][i]));
+        t = half_max(row_max(t)) * a.c;
+        if (__any(t > w.m[c] + kRescale)) {
+          const float mn = fmaxf(w.m[c], t);
+          const float f = mn == kNegInf ? 1.f : exp2_fast(w.m[c] - mn);
+          w.m[c] = mn;
+          w.l[c] *= f;
+#pragma unroll
+          for (int i = 0; i < Loop::kTiles; ++i) w.o[c][i] *= f;
+        }
+        const float mb = w.m[c] == kNegInf ? 0.f : w.m[c];
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          e[i] = exp2_fast(__builtin_fmaf(s[c][i >> 2][i & 3], a.c, -mb));
+          w.l[c] += e[i];
+        }
+        // weights enter the product as bf16 (relative error 2^-9 each, as the values they weigh);
+        // the sum l keeps them in fp32
+        p[c] = u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
+                     pack_bf16(e[6], e[7])};
+      }
+
+      // ---- O^T += V^T P^T: the lane's 8 keys are 4g .. 4g + 3 and 16 + 4g .. 16 + 4g + 3
+      const int vr0 = 4 * g + (j >> 2), vu = (j & 3) >> 1, vb = 8 * (j & 1);
+      auto read_v = [&](int i) {
+        const u32x2 lo = lds_read_tr(vl + v_unit<D>(vr0, 2 * i + vu) + vb);
+        const u32x2 hi = lds_read_tr(vl + v_unit<D>(16 + vr0, 2 * i + vu) + vb);
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+      };
+      if (!odd_values) {
+#pragma unroll
+        for (int i = 0; i < Loop::kTiles; ++i) {
+          const u32x4 v = read_v(i);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) w.o[c][i] = mfma16(v, p[c], w.o[c][i]);
+        }
+      } else {
+        // a value that is not finite, times the zero weight of a token that does not see it, is
+        // NaN: token by token, without the values that it does not see
+        for (int t = 0; t < u.nq; ++t) {
+          unsigned keep = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int key = 16 * (k >> 2) + 4 * g + (k & 3);
+            keep |= (unsigned)sees(kl, u.p0 + t, a.window, a.sinks, base + key) << k;
+          }
+#pragma unroll
+          for (int i = 0; i < Loop::kTiles; ++i) {
+            const u32x4 v = keep_values(read_v(i), keep);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const f32x4 add = mfma16(v, p[c], f32x4{0.f, 0.f, 0.f, 0.f});
+              const bool mine = w.pos[c] == u.p0 + t;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float x = w.o[c][i][e], y = x + add[e];
+                w.o[c][i][e] = mine ? y : x;
+              }
+            }
+          }
+        }
+      }
+    }
+
+    // ---- the waves' sums, block of columns by block of columns
+    const int64_t slot = a.direct ? 0 : blockIdx.x + (int64_t)b * a.kv_heads + h;
+    for (int c = 0; c < NC; ++c) {
+      if (16 * c >= rows) break;
+      float mc, lc;
+      f32x4 oc[Loop::kTiles];
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc)
+        if (cc == c) {
+          mc = w.m[cc];
+          lc = w.l[cc];
+#pragma unroll
+          for (int i = 0; i < Loop::kTiles; ++i) oc[i] = w.o[cc][i];
+        }
+      lc = half_sum(row_sum(lc));
+      __syncthreads();  // the V tiles, or the last block's sums, are no longer read
+      float* const ow = reinterpret_cast<float*>(vl);  // [16 columns][D]
+#pragma unroll
+      for (int i = 0; i < Loop::kTiles; ++i)
+        *reinterpret_cast<f32x4*>(ow + j * D + 16 * i + 4 * g) = oc[i];
+      if (g == 0) {
+        ml[wave][j][0] = mc;
+        ml[wave][j][1] = lc;
+      }
+      __syncthreads();
+      constexpr int kQuads = 16 * D / 4 / 256;  // f32x4 per thread
+#pragma unroll
+      for (int e = 0; e < kQuads; ++e) {
+        const int idx = tid + 256 * e, col = idx / (D / 4), d4 = idx - col * (D / 4);
+        const int row = 16 * c + col;
+        if (row < rows) {
+          float mx = kNegInf;
+#pragma unroll
+          for (int v = 0; v < kRowWaves; ++v) mx = fmaxf(mx, ml[v][col][0]);
+          const float mb = mx == kNegInf ? 0.f : mx;
+          float lt = 0.f;
+          f32x4 ot = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int v = 0; v < kRowWaves; ++v) {
+            const float f = exp2_fast(ml[v][col][0] - mb);
+            lt += f * ml[v][col][1];
+            ot += f * *reinterpret_cast<const f32x4*>(
+                          reinterpret_cast<const float*>(vlds + v * kWaveLds) + col * D + 4 * d4);
+          }
+          if (a.direct) {
+            const int t = row / a.group, hh = h * a.group + row - t * a.group;
+            const float inv = lt > 0.f ? a.v_scale / lt : (lt == 0.f ? 0.f : lt);
+            u32x2 pk = {pack_bf16(ot[0] * inv, ot[1] * inv), pack_bf16(ot[2] * inv, ot[3] * inv)};
+            *reinterpret_cast<u32x2*>(a.out + (int64_t)(u.t0 + t) * a.o_token +
+                                      (int64_t)hh * a.o_head + 4 * d4) = pk;
+            if (a.lse && d4 == 0)
+              a.lse[(int64_t)(u.t0 + t) * a.heads + hh] = lt == 0.f ? kNegInf : (mb + __builtin_log2f(lt)) * kLn2;
+          } else {
+            *reinterpret_cast<f32x4*>(a.part_o + (slot * a.rows + row) * D + 4 * d4) = ot;
+            if (d4 == 0) {
+              a.part_ml[(slot * a.rows + row) * 2] = mx;
+              a.part_ml[(slot * a.rows + row) * 2 + 1] = lt;
+            }
+          }
+        }
+      }
+    }
+    if (!a.direct) {
+      __syncthreads();  // the sums are read before the next piece's V tiles land
+      x += s_end - s_begin;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Tile kernel: 256 query rows (tokens x the heads of one kv head) against a key list in 64-key
+// steps.  8 waves of 32 rows; K and V tiles in LDS, two of each: while a step is worked on the
+// next one's rows are in registers, on their way to the other buffers.
+// ---------------------------------------------------------------------------------------------
+template <int D, bool FP8>
+struct TileStage {
+  static constexpr int kUnits = FP8 ? D / 16 : D / 8;      // 16-byte units of a row in memory
+  static constexpr int kPer = 2 * kTileKeys * kUnits / 512;  // of K and V, per thread
+  static constexpr int kRows = kPer >= 4 ? kPer / 2 : 1;   // rows a thread serves
+  static constexpr int kKV = kPer >= 2 ? 2 : 1;            // both tensors, or one by thread half
+  static constexpr int kRowStride = 512 / kUnits;          // rows between a thread's rows
+
+  u32x4 r[kPer];
+  int id[kRows], slot[kRows];
+  bool ok[kRows];
+
+  __device__ __forceinline__ int row(int tid, int i) const {
+    return (tid / kUnits + i * kRowStride) & (kTileKeys - 1);
+  }
+  __device__ __forceinline__ void lookup(const AttendArgs& a, const KeyList& kl, int base, int tid) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int p = base + row(tid, i);
+      const int kp = key_position(kl, p);
+      const int page = page_quotient(kp < 0 ? 0 : kp, a.cache.div);
+      const int at = key_table_index(kl, p, page);
+      slot[i] = kp - page * a.cache.page_size;
+      id[i] = at >= 0 ? (p < kl.na ? kl.ta : kl.tb)[at] : -1;  // checked when it is used
+    }
+  }
+  __device__ __forceinline__ void fetch(const AttendArgs& a, int h, int tid) {
+    const int u = tid % kUnits;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      ok[i] = page_id_checked(id[i], a.cache.num_pages) >= 0;
+      const unsigned char* kp = a.cache.k + page_row_bytes(id[i], slot[i], a.cache.k_page, a.cache.k_token) +
+                                (int64_t)h * a.cache.k_head + 16 * u;
+      const unsigned char* vp = a.cache.v + page_row_bytes(id[i], slot[i], a.cache.v_page, a.cache.v_token) +
+                                (int64_t)h * a.cache.v_head + 16 * u;
+      if (ok[i]) {
+        if constexpr (kKV == 2) {
+          r[i] = *reinterpret_cast<const u32x4*>(kp);
+          r[kRows + i] = *reinterpret_cast<const u32x4*>(vp);
+        } else {
+          r[i] = *reinterpret_cast<const u32x4*>(tid < 256 ? kp : vp);
+        }
+      } else {
+        r[i] = u32x4{0, 0, 0, 0};
+        if constexpr (kKV == 2) r[kRows + i] = u32x4{0, 0, 0, 0};
+      }
+    }
+  }
+  template <bool kIsV>
+  __device__ __forceinline__ void put(unsigned char* t, int rw, int u, const u32x4& v) const {
+    auto at = [&](int uu) { return kIsV ? v_unit<D>(rw, uu) : k_unit<D>(rw, uu); };
+    if constexpr (FP8) {
+      *reinterpret_cast<u32x4*>(t + at(2 * u)) = fp8x8_to_bf16(v[0], v[1]);
+      *reinterpret_cast<u32x4*>(t + at(2 * u + 1)) = fp8x8_to_bf16(v[2], v[3]);
+    } else {
+      *reinterpret_cast<u32x4*>(t + at(u)) = v;
+    }
+  }
+  // odd: where the wave notes that its V rows hold values that are not finite (null: not asked)
+  __device__ __forceinline__ void store(unsigned char* kt, unsigned char* vt, int* exists, int* odd,
+                                        int tid) const {
+    const int u = tid % kUnits;
+    if (odd) {
+      bool f = false;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) f |= not_finite<FP8>(r[kKV == 2 ? kRows + i : i]);
+      f = __any(f);
+      if ((tid & 63) == 0) odd[tid >> 6] = f;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int rw = row(tid, i);
+      if constexpr (kKV == 2) {
+        put<false>(kt, rw, u, r[i]);
+        put<true>(vt, rw, u, r[kRows + i]);
+      } else if (tid < 256) {
+        put<false>(kt, rw, u, r[i]);
+      } else {
+        put<true>(vt, rw, u, r[i]);
+      }
+      if (u == 0) exists[rw] = ok[i];
+    }
+  }
+};
+
+template <int D, bool FP8, bool PREFIX>
+__global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a) {
+  constexpr int kTile = kTileKeys * D * 2;
+  constexpr int kSteps = D / 16;   // matrix steps over D of a score tile
+  constexpr int kOut = D / 32;     // 32-row tiles of O^T
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // K, V; K, V
+  __shared__ int exists[2][kTileKeys];
+  __shared__ int odd[2][8];
+  __shared__ int scan[kAttendMaxSeqs + 1];
+  __shared__ int wave_sum[8];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane & 31, hf = lane >> 5;
+  const int tpt = kTileRows / a.group;  // tokens per tile
+
+  // ---- work: prefix: a share of all (segment, row tile, kv head) units' steps; window: one unit
+  int64_t x = 0, x_end = 1, total = 1;
+  int w_id = blockIdx.x;
+  if constexpr (PREFIX) {
+    // workgroups go round robin over the 8 XCDs: give each XCD one run of the work, so that the
+    // row tiles and heads that read the same pages share its L2
+    block_scan<512>(scan, wave_sum, a.nseg, [&](int s) {
+      const int n = a.seg_offsets[s + 1] - a.seg_offsets[s];
+      const int len = clamp_len(a.prefix_lens[s], a.pwidth, a.cache.page_size);
+      return (n + tpt - 1) / tpt * ((len + kTileKeys - 1) / kTileKeys);
+    });
+    total = (int64_t)scan[a.nseg] * a.kv_heads;
+    const int workers = split_workers(total, a.tile_workers);
+    const int per = (workers + 7) / 8;
+    w_id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || w_id >= workers) return;
+    x = split_begin(w_id, total, workers);
+    x_end = split_begin(w_id + 1, total, workers);
+  } else {
+    block_scan<512>(scan, wave_sum, a.batch, [&](int b) {
+      const RowUnit u = row_unit(a, b);
+      return (u.nq + tpt - 1) / tpt;
+    });
+  }
+
+  while (x < x_end) {
+    KeyList kl;
+    int t0, nt, p0 = 0, h, s_begin, s_end;
+    int64_t slot = 0;
+    if constexpr (PREFIX) {
+      const int sg = scan_find(scan, a.nseg, (int)(x / a.kv_heads));
+      const int n0 = a.seg_offsets[sg], n = a.seg_offsets[sg + 1] - n0;
+      const int len = clamp_len(a.prefix_lens[sg], a.pwidth, a.cache.page_size);
+      const int steps = (len + kTileKeys - 1) / kTileKeys;
+      const int tiles = (n + tpt - 1) / tpt;
+      int64_t r = x - (int64_t)scan[sg] * a.kv_heads;  // units: kv head major, then row tile
+      h = (int)(r / ((int64_t)tiles * steps));
+      r -= (int64_t)h * tiles * steps;
+      const int rt = (int)(r / steps);
+      s_begin = (int)(r - (int64_t)rt * steps);
+      s_end = (int)(x_end - x < steps - s_begin ? s_begin + (x_end - x) : steps);
+      t0 = n0 + rt * tpt;
+      nt = n - rt * tpt < tpt ? n - rt * tpt : tpt;
+      int ub = 0;  // units before this segment
+      for (int i = 0; i < sg; ++i) ub += (a.seg_offsets[i + 1] - a.seg_offsets[i] + tpt - 1) / tpt;
+      slot = w_id + (int64_t)ub * a.kv_heads + h * tiles + rt;
+      const int32_t* row = a.prefix_table + (int64_t)sg * a.pwidth;
+      kl = KeyList{row, row, a.pwidth, a.pwidth, 0, 0, len};
+    } else {
+      // heads fastest: with a multiple of 8 kv heads each XCD serves its own heads.  Later tiles
+      // see more keys: they start first.
+      const int tiles = scan[a.batch];
+      const int ti = tiles - 1 - (int)blockIdx.x / a.kv_heads;
+      if (ti < 0) return;
+      h = (int)blockIdx.x % a.kv_heads;
+      const int b = scan_find(scan, a.batch, ti);
+      const RowUnit u = row_unit(a, b);
+      const int rt = ti - scan[b];
+      t0 = u.t0 + rt * tpt;
+      nt = u.nq - rt * tpt < tpt ? u.nq - rt * tpt : tpt;
+      p0 = u.p0 + rt * tpt;
+      // keys up to the tile's last token
+      const int len = p0 + nt < 0 ? 0 : p0 + nt;
+      kl = window_keys(a.table + (int64_t)b * a.width, a.width, len, p0, a.window, a.sinks);
+      s_begin = 0;
+      s_end = (kl.n + kTileKeys - 1) / kTileKeys;
+    }
+
+    // ---- this lane's query row: 32 wave + q of the tile
+    const int row = 32 * wave + q;
+    const int t = row / a.group, hh = h * a.group + row - t * a.group;
+    const bool live = t < nt;
+    const int pq = p0 + t;
+    // positions of the wave's first and last live token
+    const int wt0 = 32 * wave / a.group;
+    const int wt1 = (32 * wave + 31) / a.group < nt ? (32 * wave + 31) / a.group : nt - 1;
+    const bool wave_live = wt0 < nt;
+    u32x4 qf[kSteps];
+    {
+      const uint16_t* qp = a.q + (int64_t)(t0 + t) * a.q_token + (int64_t)hh * a.q_head + 8 * hf;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        qf[s] = live ? *reinterpret_cast<const u32x4*>(qp + 16 * s) : u32x4{0, 0, 0, 0};
+    }
+    f32x16 o[kOut];
+#pragma unroll
+    for (int i = 0; i < kOut; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
+    float m = kNegInf, l = 0.f;
+
+    TileStage<D, FP8> st;
+    st.lookup(a, kl, s_begin * kTileKeys, tid);
+    st.fetch(a, h, tid);
+    st.lookup(a, kl, (s_begin + 1) * kTileKeys, tid);
+    __syncthreads();  // the last unit's tiles are no longer read
+    // Is some key of the step hidden from some row of the tile?  (the same for all waves)
+    auto hides = [&](int base) {
+      if constexpr (PREFIX) return false;
+      const int f = key_position(kl, base), last = key_position(kl, base + kTileKeys - 1);
+      return base < kl.na || last > p0 || p0 + nt - 1 - f >= a.window;
+    };
+    st.store(smem, smem + kTile, exists[0], hides(s_begin * kTileKeys) ? odd[0] : nullptr, tid);
+    st.fetch(a, h, tid);
+    st.lookup(a, kl, (s_begin + 2) * kTileKeys, tid);
+    __syncthreads();
+
+    for (int s = s_begin; s < s_end; ++s) {
+      const int buf = (s - s_begin) & 1;
+      const unsigned char* kt = smem + buf * 2 * kTile;
+      const unsigned char* vt = kt + kTile;
+      const int base = s * kTileKeys;
+      const uint64_t valid = __ballot(exists[buf][lane] != 0);
+      // does the wave see anything, does every row see everything?
+      bool any = wave_live && valid != 0, all = valid == ~0ull;
+      if constexpr (!PREFIX) {
+        const int f = key_position(kl, base), last = key_position(kl, base + kTileKeys - 1);
+        const bool in_main = base >= kl.na;
+        any = any && f <= p0 + wt1 && (f < a.sinks || p0 + wt0 - last < a.window);
+        all = all && in_main && last <= p0 + wt0 && p0 + wt1 - f < a.window;
+      }
+      f32x16 sc[2];
+      if (any) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sc[i][e] = 0.f;
+#pragma unroll
+          for (int d = 0; d < kSteps; ++d) {
+            const u32x4 kf = *reinterpret_cast<const u32x4*>(kt + k_unit<D>(32 * i + q, 2 * d + hf));
+            sc[i] = mfma32(kf, qf[d], sc[i]);
+          }
+        }
+      }
+      // ---- the next step's tiles; the buffers were last read before the barrier that began this
+      // step
+      if (s + 1 < s_end) {
+        unsigned char* kn = smem + (buf ^ 1) * 2 * kTile;
+        st.store(kn, kn + kTile, exists[buf ^ 1], hides(base + kTileKeys) ? odd[buf ^ 1] : nullptr,
+                 tid);
+        st.fetch(a, h, tid);
+        st.lookup(a, kl, base + 3 * kTileKeys, tid);
+      }
+      if (any) {
+        // lane (q, hf) holds keys 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
+        if (!all) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int key = 32 * i + 8 * (e >> 2) + 4 * hf + (e & 3);
+              bool seen = (valid >> key) & 1ull;
+              if constexpr (!PREFIX) seen = seen & sees(kl, pq, a.window, a.sinks, base + key);
+              const float v = sc[i][e];
+              sc[i][e] = seen ? v : kNegInf;
+            }
+        }
+        float tm = kNegInf;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) tm = fmaxf(tm, fmaxf(sc[0][e], sc[1][e]));
+        tm = half_max(tm) * a.c;
+        if (__any(tm > m + kRescale)) {
+          const float mn = fmaxf(m, tm);
+          const float f = mn == kNegInf ? 1.f : exp2_fast(m - mn);
+          m = mn;
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < kOut; ++i) o[i] *= f;
+        }
+        const float mb = m == kNegInf ? 0.f : m;
+        u32x4 p[4];
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          float e[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            e[i] = exp2_fast(__builtin_fmaf(sc[kb >> 1][8 * (kb & 1) + i], a.c, -mb));
+            l += e[i];
+          }
+          // weights enter the product as bf16 (relative error 2^-9 each, as the values they
+          // weigh); the sum l keeps them in fp32
+          p[kb] = u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
+                        pack_bf16(e[6], e[7])};
+        }
+        // ---- O^T += V^T P^T: of 16 keys the lane's 8 are 4 hf .. + 3 and 8 + 4 hf .. + 3
+        const int l16 = lane & 15;
+        const int vr = 4 * hf + (l16 >> 2), vu = 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1);
+        const int vb = 8 * (l16 & 1);
+        auto read_v = [&](int kb, int i) {
+          const u32x2 lo = lds_read_tr(vt + v_unit<D>(16 * kb + vr, 4 * i + vu) + vb);
+          const u32x2 hi = lds_read_tr(vt + v_unit<D>(16 * kb + 8 + vr, 4 * i + vu) + vb);
+          return u32x4{lo[0], lo[1], hi[0], hi[1]};
+        };
+        bool odd_values = false;
+        if constexpr (!PREFIX) odd_values = !all && hides(base) && __any(odd[buf][lane & 7]);
+        if (!odd_values) {
+#pragma unroll
+          for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) o[i] = mfma32(read_v(kb, i), p[kb], o[i]);
+        } else {
+          // a value that is not finite, times the zero weight of a token that does not see it, is
+          // NaN: token by token, without the values that it does not see
+          for (int tt = wt0; tt <= wt1; ++tt) {
+            unsigned keep[4];
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+              keep[kb] = 0;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int key = 16 * kb + 8 * (k >> 2) + 4 * hf + (k & 3);
+                keep[kb] |= (unsigned)sees(kl, p0 + tt, a.window, a.sinks, base + key) << k;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) {
+              f32x16 add;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) add[e] = 0.f;
+#pragma unroll
+              for (int kb = 0; kb < 4; ++kb) add = mfma32(keep_values(read_v(kb, i), keep[kb]), p[kb], add);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float x = o[i][e], y = x + add[e];
+                o[i][e] = t == tt ? y : x;
+              }
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+
+    // ---- epilogue: lane (q, hf) holds dims 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
+    l = half_sum(l);
+    if (live) {
+      if constexpr (PREFIX) {
+        float* op = a.tile_o + (slot * kTileRows + row) * D + 4 * hf;
+#pragma unroll
+        for (int i = 0; i < kOut; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<f32x4*>(op + 32 * i + 8 * e) =
+                f32x4{o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
+        if (hf == 0) {
+          a.tile_ml[(slot * kTileRows + row) * 2] = m;
+          a.tile_ml[(slot * kTileRows + row) * 2 + 1] = l;
+        }
+      } else {
+        const float inv = l > 0.f ? a.v_scale / l : (l == 0.f ? 0.f : l);
+        uint16_t* op = a.out + (int64_t)(t0 + t) * a.o_token + (int64_t)hh * a.o_head + 4 * hf;
+#pragma unroll
+        for (int i = 0; i < kOut; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<u32x2*>(op + 32 * i + 8 * e) =
+                u32x2{pack_bf16(o[i][4 * e] * inv, o[i][4 * e + 1] * inv),
+                      pack_bf16(o[i][4 * e + 2] * inv, o[i][4 * e + 3] * inv)};
+        if (a.lse && hf == 0)
+          a.lse[(int64_t)(t0 + t) * a.heads + hh] =
+              l == 0.f ? kNegInf : (m + __builtin_log2f(l)) * kLn2;
+      }
+    }
+    if constexpr (PREFIX) {
+      x += s_end - s_begin;
+    } else {
+      break;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Combine: one wave per query row adds the row's partials of both kernels, in a fixed order.
+// ---------------------------------------------------------------------------------------------
+template <int D>
+__global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a) {
+  __shared__ int pscan[kAttendMaxSegments + 1];
+  __shared__ int wave_sum[4];
+  const int tpt = kTileRows / a.group;
+  if (a.nseg > 0 && !a.row_prefix)
+    block_scan<256>(pscan, wave_sum, a.nseg, [&](int s) {
+      const int n = a.seg_offsets[s + 1] - a.seg_offsets[s];
+      const int len = clamp_len(a.prefix_lens[s], a.pwidth, a.cache.page_size);
+      return (n + tpt - 1) / tpt * ((len + kTileKeys - 1) / kTileKeys);
+    });
+  constexpr int kQ = D / 4, kWays = 64 / kQ;  // lanes of a row, pieces side by side
+  const int lane = threadIdx.x & 63;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t per = (int64_t)a.max_q * a.heads;
+  if (id >= a.batch * per) return;
+  const int b = (int)(id / per);
+  const int rest = (int)(id - b * per);
+  const int tq = rest / a.heads, hh = rest - tq * a.heads;
+  const int h = hh / a.group;
+  const RowUnit u = row_unit(a, b);
+  if (tq >= u.nq) return;
+  const int d4 = lane % kQ, way = lane / kQ;
+
+  float mx = kNegInf, lt = 0.f;
+  f32x4 ot = {0.f, 0.f, 0.f, 0.f};
+  auto add = [&](const float* ml, const float* o) {
+    const float pm = ml[0], pl = ml[1];
+    const f32x4 po = *reinterpret_cast<const f32x4*>(o + 4 * d4);
+    const float mn = fmaxf(mx, pm);
+    const float mb = mn == kNegInf ? 0.f : mn;
+    const float f0 = exp2_fast(mx - mb), f1 = exp2_fast(pm - mb);
+    lt = lt * f0 + pl * f1;
+    ot = ot * f0 + po * f1;
+    mx = mn;
+  };
+  // own rows
+  {
+    const int row = tq * a.group + hh - h * a.group;
+    const int64_t total = (int64_t)a.scan[a.batch] * a.kv_heads;
+    const int steps = a.scan[b + 1] - a.scan[b];
+    if (steps > 0) {
+      const int64_t x0 = (int64_t)a.scan[b] * a.kv_heads + (int64_t)h * steps;
+      const int workers = split_workers(total, a.workers);
+      const int w0 = split_owner(x0, total, workers);
+      const int w1 = split_owner(x0 + steps - 1, total, workers);
+      const int64_t unit = (int64_t)b * a.kv_heads + h;
+      for (int w = w0 + way; w <= w1; w += kWays) {
+        const int64_t at = (w + unit) * a.rows + row;
+        add(a.part_ml + at * 2, a.part_o + at * D);
+      }
+    }
+  }
+  // the prefix
+  if (a.nseg > 0 && !a.row_prefix) {
+    int sg = 0, ub = 0;
+    while (sg + 1 < a.nseg && a.seg_offsets[sg + 1] <= b) {
+      ub += (a.seg_offsets[sg + 1] - a.seg_offsets[sg] + tpt - 1) / tpt;
+      ++sg;
+    }
+    const int n0 = a.seg_offsets[sg];
+    const int tiles = (a.seg_offsets[sg + 1] - n0 + tpt - 1) / tpt;
+    const int seg_steps = pscan[sg + 1] - pscan[sg];
+    if (seg_steps > 0) {
+      const int64_t total = (int64_t)pscan[a.nseg] * a.kv_heads;
+      const int steps = seg_steps / tiles;
+      const int rt = (b - n0) / tpt;
+      const int row = (b - n0 - rt * tpt) * a.group + hh - h * a.group;
+      const int64_t x0 = (int64_t)pscan[sg] * a.kv_heads + ((int64_t)h * tiles + rt) * steps;
+      const int workers = split_workers(total, a.tile_workers);
+      const int w0 = split_owner(x0, total, workers);
+      const int w1 = split_owner(x0 + steps - 1, total, workers);
+      const int64_t unit = (int64_t)ub * a.kv_heads + h * tiles + rt;
+      for (int w = w0 + way; w <= w1; w += kWays) {
+        const int64_t at = (w + unit) * kTileRows + row;
+        add(a.tile_ml + at * 2, a.tile_o + at * D);
+      }
+    }
+  }
+  // the ways' sums
+#pragma unroll
+  for (int d = kQ; d < 64; d <<= 1) {
+    const float om = __shfl_xor(mx, d, 64), ol = __shfl_xor(lt, d, 64);
+    f32x4 oo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) oo[i] = __shfl_xor(ot[i], d, 64);
+    const float mn = fmaxf(mx, om);
+    const float mb = mn == kNegInf ? 0.f : mn;
+    const float f0 = exp2_fast(mx - mb), f1 = exp2_fast(om - mb);
+    lt = lt * f0 + ol * f1;
+    ot = ot * f0 + oo * f1;
+    mx = mn;
+  }
+  if (way == 0) {
+    const float inv = lt > 0.f ? a.v_scale / lt : (lt == 0.f ? 0.f : lt);
+    const int64_t tok = u.t0 + tq;
+    *reinterpret_cast<u32x2*>(a.out + tok * a.o_token + (int64_t)hh * a.o_head + 4 * d4) =
+        u32x2{pack_bf16(ot[0] * inv, ot[1] * inv), pack_bf16(ot[2] * inv, ot[3] * inv)};
+    if (a.lse && d4 == 0)
+      a.lse[tok * a.heads + hh] = lt == 0.f ? kNegInf : (mx + __builtin_log2f(lt)) * kLn2;
+  }
+}
+
+template <int D, bool FP8>
+hipError_t rows_for(const AttendArgs& a, int columns, int blocks, hipStream_t stream) {
+  clear_stale_error();
+  switch (columns) {
+    case 1: hipLaunchKernelGGL((attend_row_kernel<D, FP8, 1>), dim3(blocks), dim3(256), 0, stream, a); break;
+    case 2: hipLaunchKernelGGL((attend_row_kernel<D, FP8, 2>), dim3(blocks), dim3(256), 0, stream, a); break;
+    case 4: hipLaunchKernelGGL((attend_row_kernel<D, FP8, 4>), dim3(blocks), dim3(256), 0, stream, a); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+template <int D, bool FP8, bool PREFIX>
+hipError_t tiles_for(const AttendArgs& a, int blocks, hipStream_t stream) {
+  constexpr int lds = 4 * kTileKeys * D * 2;
+  static DeviceOnce once;
+  const hipError_t e = set_dynamic_lds_once(
+      once, reinterpret_cast<const void*>(&attend_tile_kernel<D, FP8, PREFIX>), lds);
+  if (e != hipSuccess) return e;
+  clear_stale_error();
+  hipLaunchKernelGGL((attend_tile_kernel<D, FP8, PREFIX>), dim3(blocks), dim3(512), lds, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attend_rows(const AttendArgs& a, int dim, bool fp8, int columns, int blocks,
+                              hipStream_t stream) {
+  if (blocks < 1 || a.batch > kAttendMaxSeqs || a.rows > 16 * columns) return hipErrorInvalidValue;
+  if (dim == 64) return fp8 ? rows_for<64, true>(a, columns, blocks, stream)
+                            : rows_for<64, false>(a, columns, blocks, stream);
+  if (dim == 128) return fp8 ? rows_for<128, true>(a, columns, blocks, stream)
+                             : rows_for<128, false>(a, columns, blocks, stream);
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_attend_tiles(const AttendArgs& a, int dim, bool fp8, bool prefix, int blocks,
+                               hipStream_t stream) {
+  if (blocks < 1 || a.batch > kAttendMaxSeqs || a.nseg > kAttendMaxSegments)
+    return hipErrorInvalidValue;
+  if (dim == 64)
+    return prefix ? (fp8 ? tiles_for<64, true, true>(a, blocks, stream)
+                         : tiles_for<64, false, true>(a, blocks, stream))
+                  : (fp8 ? tiles_for<64, true, false>(a, blocks, stream)
+                         : tiles_for<64, false, false>(a, blocks, stream));
+  if (dim == 128)
+    return prefix ? (fp8 ? tiles_for<128, true, true>(a, blocks, stream)
+                         : tiles_for<128, false, true>(a, blocks, stream))
+                  : (fp8 ? tiles_for<128, true, false>(a, blocks, stream)
+                         : tiles_for<128, false, false>(a, blocks, stream));
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_attend_combine(const AttendArgs& a, int dim, hipStream_t stream) {
+  const int64_t waves = (int64_t)a.batch * a.max_q * a.heads;
+  const int blocks = (int)((waves + 3) / 4);
+  clear_stale_error();
+  if (dim == 64)
+    hipLaunchKernelGGL(attend_combine_kernel<64>, dim3(blocks), dim3(256), 0, stream, a);
+  else if (dim == 128)
+    hipLaunchKernelGGL(attend_combine_kernel<128>, dim3(blocks), dim3(256), 0, stream, a);
+  else
+    return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+}  // namespace bd
