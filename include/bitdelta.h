@@ -551,6 +551,35 @@ size_t bitdelta_attend_window_workspace_bytes(int64_t tokens, int32_t heads,
                                               int32_t table_width, int32_t max_q_len,
                                               int32_t window, int32_t sinks);
 
+/*
+ * bitdelta_sample — the next token of each row of logits from given uniform numbers.
+ *
+ * A row's tokens are ordered by descending logit, ties by ascending index (NaN counts as -inf);
+ * the j-th weighs w_j = exp((logit_j - logit_0) / temperature).  The first n are kept:
+ *   n = min(k, n_p, n_m), at least 1;  k = top_k;
+ *   n_p = the smallest n with sum of the first n weights >= top_p * sum of the first k;
+ *   n_m = the number of tokens with w_j >= min_p.
+ * The token drawn is the first whose running sum of weights exceeds u times the sum of the first
+ * n; logprob = ln(its weight / that sum).  Weights and sums are fp64.
+ *
+ *   logits       [dev] logits_dtype (bitdelta_out_dtype: what bitdelta_matmul writes), row r at
+ *                r * row_stride elements, vocab values; naturally aligned.
+ *   u            [dev] float32 [rows], uniform in [0, 1) (values outside count as the nearest).
+ *   temperature  [dev] float32 [rows] or NULL (1); <= 0 or NaN: the first token of the order.
+ *   top_k        [dev] int32 [rows] or NULL; <= 0: off.
+ *   top_p        [dev] float32 [rows] or NULL; >= 1 or NaN: off.
+ *   min_p        [dev] float32 [rows] or NULL; <= 0 or NaN: off.
+ *   tokens       [dev] out int32 [rows]; -1 where every logit of the row is -inf.
+ *   logprob      [dev] out float32 [rows] or NULL; -inf beside a token of -1.
+ * rows = 0 is a no-op.  No workspace.  Errors: INVALID_ARG, SHAPE (row_stride < vocab),
+ * ALIGNMENT, UNSUPPORTED (vocab or rows beyond 2^30), HIP.
+ */
+bitdelta_status bitdelta_sample(const void* logits, int32_t logits_dtype, int64_t rows,
+                                int64_t vocab, int64_t row_stride, const float* u,
+                                const float* temperature, const int32_t* top_k,
+                                const float* top_p, const float* min_p, int32_t* tokens,
+                                float* logprob, bitdelta_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

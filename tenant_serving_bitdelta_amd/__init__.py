@@ -18,7 +18,7 @@ __all__ = [
     "compress", "plan_segments", "matmul", "matmul_grouped", "auto_path", "PATHS",
     "matmul_workspace_bytes", "sign_words_t128", "reconstruct", "upload_variant", "Residency",
     "matmul_grouped_noalloc", "NOALLOC_SCRATCH_BYTES", "attend_shared",
-    "attend_shared_workspace_bytes", "attend_window", "attend_window_workspace_bytes",
+    "attend_shared_workspace_bytes", "attend_window", "attend_window_workspace_bytes", "sample",
 ]
 
 ABI_VERSION = 7
@@ -194,6 +194,9 @@ def _lib():
         L.bitdelta_attend_window_workspace_bytes.argtypes = [
             ctypes.c_int64, ctypes.c_int32, cache_p, ctypes.c_int32, ctypes.c_int32,
             ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]
+        L.bitdelta_sample.restype = ctypes.c_int
+        L.bitdelta_sample.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
+                                      ctypes.c_int64, ctypes.c_int64, *[ctypes.c_void_p] * 8]
         _LIB = L
     return _LIB
 
@@ -808,3 +811,50 @@ def attend_window(q, k_pages, v_pages, table, lens, window, sinks=0, q_offsets=N
         ctypes.byref(rows), ctypes.byref(cache), batch, tptr, width, lptr, optr, max_q_len, window,
         sinks, ws_ptr, ws_bytes, _stream(stream)), "bitdelta_attend_window")
     return out if lse is None else (out, lse)
+
+
+# ---------------------------------------------------------------------------------------------
+# Sampling
+# ---------------------------------------------------------------------------------------------
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None, logprob=None,
+           return_logprob=False, stream=None):
+    """The next token of each row of ``logits`` ([rows, vocab], bf16 or float32, contiguous rows)
+    from the uniform numbers ``u`` (float32 [rows] in [0, 1)).  Tokens are ordered by descending
+    logit, ties by index; ``top_k`` (int32 [rows], <= 0: off), ``top_p`` and ``min_p`` (float32
+    [rows], >= 1 and <= 0: off) each keep a prefix of that order, weighed by
+    exp((logit - largest) / ``temperature``) (float32 [rows]; 0: the first token); the token drawn
+    is the first whose running weight exceeds u times the kept weight.  Returns int32 [rows] (-1:
+    every logit is -inf), and with ``return_logprob`` (or ``logprob`` given) also the natural log
+    of the token's share of the kept weight, float32 [rows]."""
+    import torch
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA/HIP torch tensor")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    rows, vocab = (int(n) for n in logits.shape)
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must have contiguous rows")
+    stride = int(logits.stride(0)) if rows > 1 else max(int(logits.stride(0)), vocab)
+
+    def arg(t, dtype, what):
+        if t is None:
+            return None
+        _check_shape(t, (rows,), what)
+        return _dev(t, dtype, what)
+
+    if out is None:
+        out = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        _on_stream(out, stream)
+    if logprob is None and return_logprob:
+        logprob = torch.empty(rows, dtype=torch.float32, device=logits.device)
+        _on_stream(logprob, stream)
+    _check(_lib().bitdelta_sample(
+        logits.data_ptr(), 0 if logits.dtype == torch.bfloat16 else 1, rows, vocab, stride,
+        arg(u, "torch.float32", "u"), arg(temperature, "torch.float32", "temperature"),
+        arg(top_k, "torch.int32", "top_k"), arg(top_p, "torch.float32", "top_p"),
+        arg(min_p, "torch.float32", "min_p"), arg(out, "torch.int32", "out"),
+        arg(logprob, "torch.float32", "logprob"), _stream(stream)), "bitdelta_sample")
+    return out if logprob is None else (out, logprob)

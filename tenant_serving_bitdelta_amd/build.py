@@ -19,7 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbitdelta.so")
 
 SOURCES = ["compress.hip", "gemv.hip", "stream.hip", "split.hip", "prefill.hip", "reconstruct.hip",
-           "noalloc.hip", "attend.hip", "split_sched.cpp", "api.cpp", "residency.cpp", "attend_api.cpp"]
+           "noalloc.hip", "attend.hip", "sample.hip", "split_sched.cpp", "api.cpp", "residency.cpp", "attend_api.cpp",
+           "sample_api.cpp"]
 ARCH = "gfx950"
 HIP_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
