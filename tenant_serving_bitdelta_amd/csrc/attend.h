@@ -33,12 +33,12 @@ __host__ __device__ __forceinline__ int page_quotient(int n, PageDiv d) {
   return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift);
 }
 
-// A paged cache: byte strides, row bytes contiguous.
+// A paged cache: strides in 16-byte units, row bytes contiguous.
 struct PagedCache {
   const unsigned char* k;
   const unsigned char* v;
-  int64_t k_page, k_token, k_head;
-  int64_t v_page, v_token, v_head;
+  uint32_t k_page, k_token, v_page, v_token;
+  int64_t k_head, v_head;       // bytes
   int32_t num_pages, page_size;
   PageDiv div;
 };
@@ -47,9 +47,10 @@ struct PagedCache {
 __host__ __device__ __forceinline__ int page_id_checked(int id, int num_pages) {
   return (uint32_t)id < (uint32_t)num_pages ? id : -1;
 }
-__host__ __device__ __forceinline__ int64_t page_row_bytes(int id, int slot, int64_t page_stride,
-                                                           int64_t token_stride) {
-  return (int64_t)id * page_stride + (int64_t)slot * token_stride;
+// Byte offset of a slot's row, from strides in 16-byte units: two 32 x 32 -> 64 bit products.
+__host__ __device__ __forceinline__ int64_t page_row_bytes(int id, int slot, uint32_t page_stride,
+                                                           uint32_t token_stride) {
+  return (int64_t)(((uint64_t)(uint32_t)id * page_stride + (uint64_t)(uint32_t)slot * token_stride) << 4);
 }
 
 // The keys a set of queries reads, as one virtual list of n keys: the first na are positions

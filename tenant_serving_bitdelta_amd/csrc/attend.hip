@@ -70,34 +70,42 @@ __device__ __forceinline__ u32x4 fp8x8_to_bf16(unsigned a, unsigned b) {
   return u32x4{x[0], x[1], y[0], y[1]};
 }
 
-// Is any of 8 bf16 (16 e4m3) values infinite or NaN?
+// Clears the bf16 (e4m3) values of v that are infinite or NaN; true if there were any.
 template <bool FP8>
-__device__ __forceinline__ bool not_finite(const u32x4& v) {
-  unsigned bad = 0;
+__device__ __forceinline__ bool clear_odd(u32x4* v) {
+  unsigned any = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const unsigned x = v[i];
-    if constexpr (FP8) {
-      // e4m3 has no infinity; NaN is all ones below the sign
-      const unsigned y = ~x & 0x7F7F7F7Fu;  // a zero byte marks a NaN
-      bad |= (y - 0x01010101u) & ~y & 0x80808080u;
+    const unsigned x = (*v)[i];
+    unsigned m = 0;
+    if constexpr (FP8) {  // e4m3 has no infinity; NaN is all ones below the sign
+#pragma unroll
+      for (int b = 0; b < 32; b += 8) m |= ((x >> b) & 0x7Fu) == 0x7Fu ? 0xFFu << b : 0u;
     } else {
-      bad |= (unsigned)((x & 0x7F80u) == 0x7F80u) | (unsigned)((x & 0x7F800000u) == 0x7F800000u);
+      m = ((x & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
     }
+    (*v)[i] = x & ~m;
+    any |= m;
   }
-  return bad != 0;
+  return any != 0;
 }
-// v with value k (0 .. 7) cleared where bit k of keep is
-__device__ __forceinline__ u32x4 keep_values(const u32x4& v, unsigned keep) {
-  u32x4 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned m = ((keep >> (2 * i)) & 1u ? 0xFFFFu : 0u) |
-                       ((keep >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
-    const unsigned x = v[i];
-    r[i] = x & m;
-  }
-  return r;
+// Element d of a value row as fp32, if it is infinite or NaN, else 0.
+template <bool FP8>
+__device__ __forceinline__ float odd_value(const unsigned char* row, int d) {
+  if constexpr (FP8) return (row[d] & 0x7F) == 0x7F ? __builtin_nanf("") : 0.f;
+  const unsigned x = reinterpret_cast<const uint16_t*>(row)[d];
+  return (x & 0x7F80u) == 0x7F80u ? __uint_as_float(x << 16) : 0.f;
+}
+// Where the value row of key vp sits, or null when it has none.
+__device__ __forceinline__ const unsigned char* value_row(const PagedCache& c, const KeyList& kl, int vp,
+                                                          int h) {
+  const int kp = key_position(kl, vp);
+  const int page = page_quotient(kp, c.div);
+  const int at = key_table_index(kl, vp, page);
+  if (at < 0) return nullptr;
+  const int id = page_id_checked((vp < kl.na ? kl.ta : kl.tb)[at], c.num_pages);
+  if (id < 0) return nullptr;
+  return c.v + page_row_bytes(id, kp - page * c.page_size, c.v_page, c.v_token) + (int64_t)h * c.v_head;
 }
 
 __device__ __forceinline__ u32x2 lds_read_tr(const unsigned char* p) {
@@ -243,7 +251,7 @@ struct RowLoop {
   float m[NC], l[NC];
   int pos[NC];   // the column's token position (window op with several tokens)
   u32x4 kr[2][kLoads], vr[2][kLoads];
-  int id[2], slot[2], vp[2];
+  int id[2], slot[2];
   bool ok[2];
 
   __device__ __forceinline__ void lookup(const AttendArgs& a, const KeyList& kl, int base, int j) {
@@ -261,26 +269,31 @@ struct RowLoop {
   __device__ __forceinline__ void fetch(const AttendArgs& a, int h, int g) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+      // absent keys read page 0 and are cleared before they are used
       ok[r] = page_id_checked(id[r], a.cache.num_pages) >= 0;
-      if (ok[r]) {
-        const unsigned char* kp = a.cache.k + page_row_bytes(id[r], slot[r], a.cache.k_page, a.cache.k_token) +
-                                  (int64_t)h * a.cache.k_head + 16 * g;
-        const unsigned char* vp_ = a.cache.v + page_row_bytes(id[r], slot[r], a.cache.v_page, a.cache.v_token) +
-                                   (int64_t)h * a.cache.v_head + 16 * g;
+      const int page = ok[r] ? id[r] : 0, at = ok[r] ? slot[r] : 0;
+      const unsigned char* kp = a.cache.k + page_row_bytes(page, at, a.cache.k_page, a.cache.k_token) +
+                                (int64_t)h * a.cache.k_head + 16 * g;
+      const unsigned char* vp = a.cache.v + page_row_bytes(page, at, a.cache.v_page, a.cache.v_token) +
+                                (int64_t)h * a.cache.v_head + 16 * g;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) kr[r][i] = *reinterpret_cast<const u32x4*>(kp + 64 * i);
+      for (int i = 0; i < kLoads; ++i) kr[r][i] = *reinterpret_cast<const u32x4*>(kp + 64 * i);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) vr[r][i] = *reinterpret_cast<const u32x4*>(vp_ + 64 * i);
-      } else {
-        // absent rows are zeros, so that what the memory holds there cannot reach the sums
+      for (int i = 0; i < kLoads; ++i) vr[r][i] = *reinterpret_cast<const u32x4*>(vp + 64 * i);
+    }
+  }
+  // what the memory holds for an absent key must not reach the sums
+  __device__ __forceinline__ void clear_absent() {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if (!ok[r])
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) kr[r][i] = vr[r][i] = u32x4{0, 0, 0, 0};
-      }
-    }
   }
 };
 
-template <int D, bool FP8, int NC>
+// MULTI: units may hold several tokens, which see different keys
+template <int D, bool FP8, int NC, bool MULTI>
 __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1))
 void attend_row_kernel(const AttendArgs a) {
   using Loop = RowLoop<D, FP8, NC>;
@@ -331,9 +344,6 @@ void attend_row_kernel(const AttendArgs a) {
     }
     const int rows = u.nq * a.group;
     const KeyList kl = u.keys;
-    // with one token per unit every key of the list is visible to every row
-    const bool masked = u.nq > 1;
-
     Loop w;
     // ---- queries: column j of block c is row 16c + j, token (row / group), head (row % group)
 #pragma unroll
@@ -366,15 +376,23 @@ void attend_row_kernel(const AttendArgs a) {
       // keys of the tile that exist, bit (key): lanes 0..15 speak for keys 0..15 and 16..31
       const unsigned valid = (unsigned)(__ballot(ok0) & 0xFFFFull) |
                              ((unsigned)(__ballot(ok1) & 0xFFFFull) << 16);
-      // ---- V into LDS, scores from K
-      bool odd_values = false;
-      if (masked) {
+      if (valid != 0xFFFFFFFFu) w.clear_absent();
+      // keys whose values are not all finite: those values are taken out here and added below for
+      // the tokens that see them, since their product with a zero weight would be NaN
+      unsigned odd = 0;
+      if constexpr (MULTI) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < 2; ++r) {
+          bool f = false;
 #pragma unroll
-          for (int i = 0; i < Loop::kLoads; ++i) odd_values |= not_finite<FP8>(w.vr[r][i]);
-        odd_values = __any(odd_values);
+          for (int i = 0; i < Loop::kLoads; ++i) f |= clear_odd<FP8>(&w.vr[r][i]);
+          uint64_t m = __ballot(f);
+          m |= m >> 32;
+          m |= m >> 16;
+          odd |= (unsigned)(m & 0xFFFFull) << (16 * r);
+        }
       }
+      // ---- V into LDS, scores from K
       f32x4 s[NC][2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -417,14 +435,14 @@ void attend_row_kernel(const AttendArgs a) {
       u32x4 p[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        if (valid != 0xFFFFFFFFu || masked) {
+        if (valid != 0xFFFFFFFFu || MULTI) {
 #pragma unroll
           for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int key = 16 * r + 4 * g + i;
               bool seen = (valid >> key) & 1u;
-              if (masked) seen = seen & sees(kl, w.pos[c], a.window, a.sinks, base + key);
+              if constexpr (MULTI) seen = seen & sees(kl, w.pos[c], a.window, a.sinks, base + key);
               const float v = s[c][r][i];
               s[c][r][i] = seen ? v : kNegInf;
             }
@@ -456,41 +474,29 @@ void attend_row_kernel(const AttendArgs a) {
 
       // ---- O^T += V^T P^T: the lane's 8 keys are 4g .. 4g + 3 and 16 + 4g .. 16 + 4g + 3
       const int vr0 = 4 * g + (j >> 2), vu = (j & 3) >> 1, vb = 8 * (j & 1);
-      auto read_v = [&](int i) {
+#pragma unroll
+      for (int i = 0; i < Loop::kTiles; ++i) {
         const u32x2 lo = lds_read_tr(vl + v_unit<D>(vr0, 2 * i + vu) + vb);
         const u32x2 hi = lds_read_tr(vl + v_unit<D>(16 + vr0, 2 * i + vu) + vb);
-        return u32x4{lo[0], lo[1], hi[0], hi[1]};
-      };
-      if (!odd_values) {
+        const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
-        for (int i = 0; i < Loop::kTiles; ++i) {
-          const u32x4 v = read_v(i);
+        for (int c = 0; c < NC; ++c) w.o[c][i] = mfma16(v, p[c], w.o[c][i]);
+      }
+      if constexpr (MULTI) {
+        for (; odd; odd &= odd - 1) {
+          const int vp = base + __builtin_ctz(odd);
+          const unsigned char* row = value_row(a.cache, kl, vp, h);
+          if (!row) continue;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) w.o[c][i] = mfma16(v, p[c], w.o[c][i]);
-        }
-      } else {
-        // a value that is not finite, times the zero weight of a token that does not see it, is
-        // NaN: token by token, without the values that it does not see
-        for (int t = 0; t < u.nq; ++t) {
-          unsigned keep = 0;
+          for (int c = 0; c < NC; ++c) {
+            const bool seen = sees(kl, w.pos[c], a.window, a.sinks, vp);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int key = 16 * (k >> 2) + 4 * g + (k & 3);
-            keep |= (unsigned)sees(kl, u.p0 + t, a.window, a.sinks, base + key) << k;
-          }
-#pragma unroll
-          for (int i = 0; i < Loop::kTiles; ++i) {
-            const u32x4 v = keep_values(read_v(i), keep);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              const f32x4 add = mfma16(v, p[c], f32x4{0.f, 0.f, 0.f, 0.f});
-              const bool mine = w.pos[c] == u.p0 + t;
+            for (int i = 0; i < Loop::kTiles; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float x = w.o[c][i][e], y = x + add[e];
-                w.o[c][i][e] = mine ? y : x;
+                const float x = w.o[c][i][e];
+                w.o[c][i][e] = seen ? x + odd_value<FP8>(row, 16 * i + 4 * g + e) : x;
               }
-            }
           }
         }
       }
@@ -600,21 +606,18 @@ struct TileStage {
     const int u = tid % kUnits;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
+      // absent keys read page 0 and are cleared before they are stored
       ok[i] = page_id_checked(id[i], a.cache.num_pages) >= 0;
-      const unsigned char* kp = a.cache.k + page_row_bytes(id[i], slot[i], a.cache.k_page, a.cache.k_token) +
+      const int page = ok[i] ? id[i] : 0, at = ok[i] ? slot[i] : 0;
+      const unsigned char* kp = a.cache.k + page_row_bytes(page, at, a.cache.k_page, a.cache.k_token) +
                                 (int64_t)h * a.cache.k_head + 16 * u;
-      const unsigned char* vp = a.cache.v + page_row_bytes(id[i], slot[i], a.cache.v_page, a.cache.v_token) +
+      const unsigned char* vp = a.cache.v + page_row_bytes(page, at, a.cache.v_page, a.cache.v_token) +
                                 (int64_t)h * a.cache.v_head + 16 * u;
-      if (ok[i]) {
-        if constexpr (kKV == 2) {
-          r[i] = *reinterpret_cast<const u32x4*>(kp);
-          r[kRows + i] = *reinterpret_cast<const u32x4*>(vp);
-        } else {
-          r[i] = *reinterpret_cast<const u32x4*>(tid < 256 ? kp : vp);
-        }
+      if constexpr (kKV == 2) {
+        r[i] = *reinterpret_cast<const u32x4*>(kp);
+        r[kRows + i] = *reinterpret_cast<const u32x4*>(vp);
       } else {
-        r[i] = u32x4{0, 0, 0, 0};
-        if constexpr (kKV == 2) r[kRows + i] = u32x4{0, 0, 0, 0};
+        r[i] = *reinterpret_cast<const u32x4*>(tid < 256 ? kp : vp);
       }
     }
   }
@@ -628,16 +631,34 @@ struct TileStage {
       *reinterpret_cast<u32x4*>(t + at(u)) = v;
     }
   }
-  // odd: where the wave notes that its V rows hold values that are not finite (null: not asked)
-  __device__ __forceinline__ void store(unsigned char* kt, unsigned char* vt, int* exists, int* odd,
-                                        int tid) const {
+  // state: per key, bit 0: it exists; bit 1 (edge steps, where some row does not see some key):
+  // some of its values are not finite.  Those are stored as zeros, since their product with a zero
+  // weight would be NaN, and added later for the rows that see them.
+  __device__ __forceinline__ void store(unsigned char* kt, unsigned char* vt, int* state, bool edge,
+                                        int tid) {
     const int u = tid % kUnits;
-    if (odd) {
-      bool f = false;
+    bool every = true;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) f |= not_finite<FP8>(r[kKV == 2 ? kRows + i : i]);
-      f = __any(f);
-      if ((tid & 63) == 0) odd[tid >> 6] = f;
+    for (int i = 0; i < kRows; ++i) every &= ok[i];
+    if (!__all(every)) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (!ok[i]) {
+          r[i] = u32x4{0, 0, 0, 0};
+          if constexpr (kKV == 2) r[kRows + i] = u32x4{0, 0, 0, 0};
+        }
+    }
+    int bits[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) bits[i] = ok[i];
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        bool f = false;
+        if (kKV == 2 || tid >= 256) f = clear_odd<FP8>(&r[kKV == 2 ? kRows + i : i]);
+        const uint64_t m = __ballot(f) >> ((tid & 63) & ~(kUnits - 1));  // of this key's units
+        if (m & ((1ull << kUnits) - 1)) bits[i] |= 2;
+      }
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
@@ -650,7 +671,7 @@ struct TileStage {
       } else {
         put<true>(vt, rw, u, r[i]);
       }
-      if (u == 0) exists[rw] = ok[i];
+      if (u == 0 && (kKV == 2 || tid >= 256)) state[rw] = bits[i];
     }
   }
 };
@@ -661,8 +682,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
   constexpr int kSteps = D / 16;   // matrix steps over D of a score tile
   constexpr int kOut = D / 32;     // 32-row tiles of O^T
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // K, V; K, V
-  __shared__ int exists[2][kTileKeys];
-  __shared__ int odd[2][8];
+  __shared__ int state[2][kTileKeys];
   __shared__ int scan[kAttendMaxSeqs + 1];
   __shared__ int wave_sum[8];
 
@@ -767,13 +787,13 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
     st.fetch(a, h, tid);
     st.lookup(a, kl, (s_begin + 1) * kTileKeys, tid);
     __syncthreads();  // the last unit's tiles are no longer read
-    // Is some key of the step hidden from some row of the tile?  (the same for all waves)
+    // edge step: some row of the tile does not see some key of it (the same for all waves)
     auto hides = [&](int base) {
       if constexpr (PREFIX) return false;
       const int f = key_position(kl, base), last = key_position(kl, base + kTileKeys - 1);
       return base < kl.na || last > p0 || p0 + nt - 1 - f >= a.window;
     };
-    st.store(smem, smem + kTile, exists[0], hides(s_begin * kTileKeys) ? odd[0] : nullptr, tid);
+    st.store(smem, smem + kTile, state[0], hides(s_begin * kTileKeys), tid);
     st.fetch(a, h, tid);
     st.lookup(a, kl, (s_begin + 2) * kTileKeys, tid);
     __syncthreads();
@@ -783,7 +803,8 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       const unsigned char* kt = smem + buf * 2 * kTile;
       const unsigned char* vt = kt + kTile;
       const int base = s * kTileKeys;
-      const uint64_t valid = __ballot(exists[buf][lane] != 0);
+      const int key_state = state[buf][lane];
+      const uint64_t valid = __ballot(key_state & 1);
       // does the wave see anything, does every row see everything?
       bool any = wave_live && valid != 0, all = valid == ~0ull;
       if constexpr (!PREFIX) {
@@ -809,8 +830,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       // step
       if (s + 1 < s_end) {
         unsigned char* kn = smem + (buf ^ 1) * 2 * kTile;
-        st.store(kn, kn + kTile, exists[buf ^ 1], hides(base + kTileKeys) ? odd[buf ^ 1] : nullptr,
-                 tid);
+        st.store(kn, kn + kTile, state[buf ^ 1], hides(base + kTileKeys), tid);
         st.fetch(a, h, tid);
         st.lookup(a, kl, base + 3 * kTileKeys, tid);
       }
@@ -859,44 +879,28 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
         const int l16 = lane & 15;
         const int vr = 4 * hf + (l16 >> 2), vu = 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1);
         const int vb = 8 * (l16 & 1);
-        auto read_v = [&](int kb, int i) {
-          const u32x2 lo = lds_read_tr(vt + v_unit<D>(16 * kb + vr, 4 * i + vu) + vb);
-          const u32x2 hi = lds_read_tr(vt + v_unit<D>(16 * kb + 8 + vr, 4 * i + vu) + vb);
-          return u32x4{lo[0], lo[1], hi[0], hi[1]};
-        };
-        bool odd_values = false;
-        if constexpr (!PREFIX) odd_values = !all && hides(base) && __any(odd[buf][lane & 7]);
-        if (!odd_values) {
 #pragma unroll
-          for (int kb = 0; kb < 4; ++kb)
+        for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
-            for (int i = 0; i < kOut; ++i) o[i] = mfma32(read_v(kb, i), p[kb], o[i]);
-        } else {
-          // a value that is not finite, times the zero weight of a token that does not see it, is
-          // NaN: token by token, without the values that it does not see
-          for (int tt = wt0; tt <= wt1; ++tt) {
-            unsigned keep[4];
+          for (int i = 0; i < kOut; ++i) {
+            const u32x2 lo = lds_read_tr(vt + v_unit<D>(16 * kb + vr, 4 * i + vu) + vb);
+            const u32x2 hi = lds_read_tr(vt + v_unit<D>(16 * kb + 8 + vr, 4 * i + vu) + vb);
+            o[i] = mfma32(u32x4{lo[0], lo[1], hi[0], hi[1]}, p[kb], o[i]);
+          }
+        if constexpr (!PREFIX) {
+          if (!all) {
+            for (uint64_t odd = __ballot(key_state & 2); odd; odd &= odd - 1) {
+              const int vp = base + __builtin_ctzll(odd);
+              const unsigned char* row_v = value_row(a.cache, kl, vp, h);
+              if (!row_v) continue;
+              const bool seen = sees(kl, pq, a.window, a.sinks, vp);
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-              keep[kb] = 0;
+              for (int i = 0; i < kOut; ++i)
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int key = 16 * kb + 8 * (k >> 2) + 4 * hf + (k & 3);
-                keep[kb] |= (unsigned)sees(kl, p0 + tt, a.window, a.sinks, base + key) << k;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < kOut; ++i) {
-              f32x16 add;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) add[e] = 0.f;
-#pragma unroll
-              for (int kb = 0; kb < 4; ++kb) add = mfma32(keep_values(read_v(kb, i), keep[kb]), p[kb], add);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float x = o[i][e], y = x + add[e];
-                o[i][e] = t == tt ? y : x;
-              }
+                for (int e = 0; e < 16; ++e) {
+                  const float x = o[i][e];
+                  o[i][e] = seen ? x + odd_value<FP8>(row_v, 32 * i + 8 * (e >> 2) + 4 * hf + (e & 3)) : x;
+                }
             }
           }
         }
@@ -1051,12 +1055,15 @@ __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a)
 template <int D, bool FP8>
 hipError_t rows_for(const AttendArgs& a, int columns, int blocks, hipStream_t stream) {
   clear_stale_error();
-  switch (columns) {
-    case 1: hipLaunchKernelGGL((attend_row_kernel<D, FP8, 1>), dim3(blocks), dim3(256), 0, stream, a); break;
-    case 2: hipLaunchKernelGGL((attend_row_kernel<D, FP8, 2>), dim3(blocks), dim3(256), 0, stream, a); break;
-    case 4: hipLaunchKernelGGL((attend_row_kernel<D, FP8, 4>), dim3(blocks), dim3(256), 0, stream, a); break;
-    default: return hipErrorInvalidValue;
-  }
+  const dim3 grid(blocks), block(256);
+  const bool multi = a.max_q > 1;
+  if (columns == 1 && !multi) hipLaunchKernelGGL((attend_row_kernel<D, FP8, 1, false>), grid, block, 0, stream, a);
+  else if (columns == 2 && !multi) hipLaunchKernelGGL((attend_row_kernel<D, FP8, 2, false>), grid, block, 0, stream, a);
+  else if (columns == 4 && !multi) hipLaunchKernelGGL((attend_row_kernel<D, FP8, 4, false>), grid, block, 0, stream, a);
+  else if (columns == 1) hipLaunchKernelGGL((attend_row_kernel<D, FP8, 1, true>), grid, block, 0, stream, a);
+  else if (columns == 2) hipLaunchKernelGGL((attend_row_kernel<D, FP8, 2, true>), grid, block, 0, stream, a);
+  else if (columns == 4) hipLaunchKernelGGL((attend_row_kernel<D, FP8, 4, true>), grid, block, 0, stream, a);
+  else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 

@@ -71,6 +71,7 @@ bitdelta_status check_cache(const bitdelta_kv_cache* c, int32_t heads) {
                     c->v_stride_token, c->v_stride_head}) {
     if (s < 0) return BITDELTA_ERR_INVALID_ARG;
     if (s % unit != 0) return BITDELTA_ERR_ALIGNMENT;
+    if (s / unit > 0xFFFFFFFFll) return BITDELTA_ERR_UNSUPPORTED;
   }
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return BITDELTA_ERR_ALIGNMENT;
   return BITDELTA_OK;
@@ -163,11 +164,11 @@ void fill(bd::AttendArgs* a, const bitdelta_attend_rows& r, const bitdelta_kv_ca
   a->lse = r.lse;
   a->cache.k = static_cast<const unsigned char*>(c.k);
   a->cache.v = static_cast<const unsigned char*>(c.v);
-  a->cache.k_page = c.k_stride_page * es;
-  a->cache.k_token = c.k_stride_token * es;
+  a->cache.k_page = (uint32_t)(c.k_stride_page * es / 16);
+  a->cache.k_token = (uint32_t)(c.k_stride_token * es / 16);
   a->cache.k_head = c.k_stride_head * es;
-  a->cache.v_page = c.v_stride_page * es;
-  a->cache.v_token = c.v_stride_token * es;
+  a->cache.v_page = (uint32_t)(c.v_stride_page * es / 16);
+  a->cache.v_token = (uint32_t)(c.v_stride_token * es / 16);
   a->cache.v_head = c.v_stride_head * es;
   a->cache.num_pages = c.num_pages;
   a->cache.page_size = c.page_size;

@@ -99,7 +99,8 @@ static int check_bad_tables() {
     }
   }
   // offsets past 32 bits
-  CHECK(page_row_bytes(70000, 15, 65536, 256) == 70000ll * 65536 + 15 * 256, "64-bit offset");
+  CHECK(page_row_bytes(70000, 15, 65536, 16) == 70000ll * 65536 * 16 + 15 * 256, "64-bit offset");
+  CHECK(page_row_bytes(3, 5, 0xFFFFFFFFu, 1) == 3ll * 0xFFFFFFFFll * 16 + 80, "widest stride");
   return 0;
 }
 
