@@ -294,7 +294,7 @@ struct RowLoop {
 
 // MULTI: units may hold several tokens, which see different keys
 template <int D, bool FP8, int NC, bool MULTI>
-__global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1))
+__global__ __launch_bounds__(256, NC <= 2 ? 2 : 1)
 void attend_row_kernel(const AttendArgs a) {
   using Loop = RowLoop<D, FP8, NC>;
   constexpr int kWaveLds = kRowKeys * D * 2;
