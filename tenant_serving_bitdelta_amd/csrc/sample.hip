@@ -13,14 +13,12 @@
 // are fp64, so that a draw next to a border between two tokens falls on the side where the
 // definition puts it.
 //
-// When the answer lies outside the collected tokens (a flat distribution and no top-k), a second
-// reading counts and weighs the tokens in bins of 1/128 in (l_0 - l) / T, which confines each
-// border (top-k, top-p, min-p, the draw) to a bin or few; a third reading collects the tokens of
-// those bins, and the borders are resolved as before.  Where even that collects
-// too many (thousands of equal logits), the borders are found by bisection over (logit, index), one
-// reading per step.
-#include <limits.h>
-
+// Where no top-k says how many tokens to collect (top-p alone, or no filter at all), the reading
+// instead counts and weighs the tokens in bins of 1/64 in (l_0 - l) / T, which gives the row's
+// weight and confines each border (top-p, min-p, the draw) to a bin or few; the tokens of those bins
+// are collected, and the borders are resolved as before.  Where even that collects too many
+// (thousands of equal logits), the borders are found by bisection over (logit, index), one reading
+// per step.
 #include "bd_internal.h"
 #include "sample.h"
 
@@ -28,15 +26,36 @@ namespace bd {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kParts = 8;       // a thread's vectors i, i + 8, ... make its part i
+constexpr int kParts = 4;       // a thread's vectors i, i + 4, ... make its part i
 constexpr int kCap = 4096;      // collected tokens at most
-constexpr int kBins = 4096;     // of 1/kBinScale each in (l_0 - l) / T; the last takes the rest
-constexpr int kBinScale = 128;
-constexpr int kMaxK = 1024;     // top-k up to this goes by the threads' maxima (one per thread)
-constexpr int kGuess = 128;     // tokens to collect when no top-k says how many
+constexpr int kPer = kCap / kThreads;  // of them per thread: kPer t .. kPer t + kPer - 1
+constexpr int kMaxK = 2048;     // top-k up to this goes by the maxima of the threads' parts
 constexpr int kFewK = 128;      // up to this many go by one maximum per thread, more by kParts
+constexpr int kBins = 4096;     // of 1/kBinScale each in logit / T; the last takes the rest
+constexpr int kBinScale = 64;
+constexpr int kMaxBinVocab = 1 << 20;
 
 constexpr float kNegInf = -__builtin_inff();
+
+// The workgroup's shared memory, at file scope so that functions that are not inlined address it
+// directly: the kernel's time is largely latency, and much code run once costs fetches.
+struct Shared {
+  uint64_t cand[kCap];
+  union {
+    double cum[kCap];
+    unsigned long long bins[kBins];
+  };
+  uint16_t hits[kParts * kThreads];  // parts to read again: thread + kThreads * part
+  int bucket[kThreads];
+  double wave_d[kWaves];
+  float wave_f[kWaves], wave_g[kWaves];
+  int wave_i[kWaves], wave_n[2][kWaves];
+  int count, nhits, best, most;
+  int found;
+  double found_mass;
+  int found_count;
+};
+__shared__ Shared sh;
 
 // Order-preserving map of floats to unsigned; -0 and +0 are one value, NaN counts as -inf.
 __device__ __forceinline__ float clean(float x) { return x == x ? x + 0.0f : kNegInf; }
@@ -47,21 +66,26 @@ __device__ __forceinline__ unsigned to_key(float x) {
 __device__ __forceinline__ float from_key(unsigned k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
+// A token in the order: larger logits first, then smaller indices.
+__device__ __forceinline__ uint64_t composite(float l, int idx) {
+  return ((uint64_t)to_key(l) << 32) | (0xFFFFFFFFu - (unsigned)idx);
+}
+__device__ __forceinline__ float logit_of(uint64_t c) { return from_key((unsigned)(c >> 32)); }
 
 template <bool F32>
 struct Row {
   static constexpr int kE = F32 ? 4 : 8;  // elements of a 16-byte vector
   const unsigned char* p;                 // first element
-  int vocab;
   int head, nv, extra;  // elements before the first aligned vector, vectors, head + tail elements
+  int iters;            // vectors per thread, at most
 
   __device__ __forceinline__ Row(const SampleArgs& a, int row) {
     p = static_cast<const unsigned char*>(a.logits) + (int64_t)row * a.row_stride * (F32 ? 4 : 2);
-    vocab = a.vocab;
     const int mis = (int)(reinterpret_cast<uintptr_t>(p) & 15);
-    head = min(vocab, mis ? (16 - mis) / (F32 ? 4 : 2) : 0);
-    nv = (vocab - head) / kE;
-    extra = vocab - nv * kE;
+    head = min(a.vocab, mis ? (16 - mis) / (F32 ? 4 : 2) : 0);
+    nv = (a.vocab - head) / kE;
+    extra = a.vocab - nv * kE;
+    iters = (nv + kThreads - 1) / kThreads;
   }
   __device__ __forceinline__ int extra_index(int i) const { return i < head ? i : nv * kE + i; }
   __device__ __forceinline__ float one(int i) const {
@@ -76,15 +100,16 @@ struct Row {
     const unsigned x = r[e >> 1];
     return clean((e & 1) ? bf16hi_to_f32(x) : bf16lo_to_f32(x));
   }
+  __device__ __forceinline__ static float plain(const u32x4& r, int e) {  // NaN and -0 as they are
+    if constexpr (F32) return __uint_as_float(r[e]);
+    const unsigned x = r[e >> 1];
+    return (e & 1) ? bf16hi_to_f32(x) : bf16lo_to_f32(x);
+  }
 };
 
-// ln w and w; the largest logit weighs 1, also where it is infinite
-__device__ __forceinline__ double log_weight(float l, float top, double inv_t) {
-  return l == top ? 0.0 : ((double)l - (double)top) * inv_t;
-}
 // e^x for x <= 0 in fp64: x = n ln 2 + r with |r| <= ln 2 / 2, and the Taylor series of e^r to
-// r^12 (the next term is below 2e-16).  About 20 fp64 instructions.
-__device__ __forceinline__ double exp_f64(double x) {
+// r^12 (the next term is below 2e-16).
+__device__ __noinline__ double exp_f64(double x) {
   x = fmax(x, -745.0);
   const double n = __builtin_rint(x * 1.4426950408889634074);
   double r = __builtin_fma(n, -0.693147180369123816490, x);  // ln 2 in two parts, the first short
@@ -104,127 +129,68 @@ __device__ __forceinline__ double exp_f64(double x) {
   e = __builtin_fma(e, r, 1.0);
   return __builtin_ldexp(e, (int)n);
 }
+// ln w and w; the largest logit weighs 1, also where it is infinite
+__device__ __forceinline__ double log_weight(float l, float top, double inv_t) {
+  return l == top ? 0.0 : ((double)l - (double)top) * inv_t;
+}
 __device__ __forceinline__ double weight(float l, float top, double inv_t) {
   return l == kNegInf ? 0.0 : exp_f64(log_weight(l, top, inv_t));
 }
-// Where a logit falls among the bins, in fp64 (bin = its whole part): never less for a smaller
-// logit.  scale: kBinScale / T; what lies beyond the bins counts as the last one's lower end.
-__device__ __forceinline__ double bin_place(float l, double top, double scale) {
-  return fmin((top - (double)l) * scale, (double)(kBins - 1));
-}
 
-// One reading of the row by the workgroup, kParts vectors a thread in flight ahead of the ones that
-// are worked on: each(vectors, i0) gets the vectors tid + (i0 + q) * kThreads, q < kParts (past the
-// row's end: its last one); one(l, idx) the elements before and after the vectors.
-template <bool F32, class Each, class One>
-__device__ __forceinline__ void read_batches(const Row<F32>& row, Each each, One one) {
-  const int tid = threadIdx.x;
-  const int iters = (row.nv + kThreads - 1) / kThreads;
-  u32x4 r[kParts], nx[kParts];
-  auto fetch = [&](int i0, u32x4* v) {
-#pragma unroll
-    for (int q = 0; q < kParts; ++q) v[q] = row.raw(min(tid + (i0 + q) * kThreads, row.nv - 1));
-  };
-  if (iters > 0) fetch(0, r);
-  if (tid < row.extra) {
-    const int idx = row.extra_index(tid);
-    one(row.one(idx), idx);
+// The bins.  A logit's place is (ref - l) * 64 / T, kept as a fixed-point number: 12 bits of bin, 28
+// of the place within it.  Never less for a smaller logit; what lies beyond the bins counts as the
+// last one's.  One fused product and sum with an offset of 1.5 * 2^24 leaves place * 2^28 in the
+// low bits.
+//
+// A token at place b + 64 x of bin b weighs e^(-b / 64) (1 - y), y = 1 - e^-x < 2^-6.  A bin's
+// tally is one 64-bit integer, count * 2^low + sum of y in units: additions of integers do not
+// depend on their order.  y is computed in fp32, so a weight is off by about 1e-9 of itself at
+// most; these errors average out over a sum.
+struct Bins {
+  double offset, scale;  // of the place
+  int low;               // bits below the count
+  float units;           // units of y in 1
+  float c1, c2, c3, c4;  // y in units as a polynomial of the 28 bits
+  // false: places do not fit (T is so small that only the largest logit counts)
+  __device__ __forceinline__ bool begin_at(double ref) {
+    offset = ref * scale + 25165824.0;
+    return fabs(ref * scale) < 4194304.0;
   }
-  for (int i0 = 0; i0 < iters; i0 += kParts) {
-    if (i0 + kParts < iters) fetch(i0 + kParts, nx);
-    each(r, i0);
-#pragma unroll
-    for (int q = 0; q < kParts; ++q) r[q] = nx[q];
+  __device__ __forceinline__ Bins(int vocab, double inv_t) {
+    scale = inv_t * kBinScale;
+    offset = 0;
+    const int cb = 32 - __builtin_clz((unsigned)vocab);  // a count takes up to cb bits
+    low = 63 - cb;
+    units = __builtin_ldexpf(1.0f, min(low - cb + 6, 36));
+    const float x1 = 1.0f / (kBinScale * 268435456.0f);  // 2^-34
+    c1 = x1 * units;
+    c2 = -0.5f * x1 * c1;
+    c3 = (-1.0f / 3.0f) * x1 * c2;
+    c4 = -0.25f * x1 * c3;
   }
-}
-// The same, element by element: one(l, idx).
-template <bool F32, class One>
-__device__ __forceinline__ void read_row(const Row<F32>& row, One one) {
-  constexpr int kE = Row<F32>::kE;
-  read_batches<F32>(
-      row,
-      [&](const u32x4* r, int i0) {
-#pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-          const int v = (int)threadIdx.x + (i0 + q) * kThreads;
-          if (v < row.nv)
-#pragma unroll
-            for (int e = 0; e < kE; ++e) one(row.part(r[q], e), row.head + v * kE + e);
-        }
-      },
-      one);
-}
-
-// Sums of e^((l - top) / T) over many tokens: with y the exponent in powers of two, y = n + r, |r| <= 1/2, and the series of 2^r to r^11 (the next term is below 1e-14).  n comes
-// out of the low bits of y + 1.5 * 2^52.  Weights below 2^-1000 (0 among them) count as 2^-1000,
-// which does not reach the sums.
-struct Exp2 {
-  double a, top;
-  __device__ __forceinline__ Exp2(float l0, double inv_t) {
-    a = inv_t * 1.4426950408889634074;
-    top = l0;
+  __device__ __forceinline__ uint64_t place(float l) const {
+    const double end = 25165824.0 + kBins - 0.0625;
+    return (uint64_t)__double_as_longlong(fmin(__builtin_fma(-(double)l, scale, offset), end));
   }
-  __device__ __forceinline__ double operator()(float l) const {
-    const double kMagic = 6755399441055744.0;
-    const double y = fmax(((double)l - top) * a, -1000.0);
-    const double t = y + kMagic;
-    const double r = y - (t - kMagic);
-    double e = 4.446e-10;                           // ln2^11 / 11! and so on
-    e = __builtin_fma(e, r, 7.0549116208011233e-9);
-    e = __builtin_fma(e, r, 1.0178086009239699e-7);
-    e = __builtin_fma(e, r, 1.3215486790144309e-6);
-    e = __builtin_fma(e, r, 1.5252733804059841e-5);
-    e = __builtin_fma(e, r, 1.5403530393381610e-4);
-    e = __builtin_fma(e, r, 1.3333558146428443e-3);
-    e = __builtin_fma(e, r, 9.6181291076284772e-3);
-    e = __builtin_fma(e, r, 5.5504108664821580e-2);
-    e = __builtin_fma(e, r, 0.24022650695910071);
-    e = __builtin_fma(e, r, 0.69314718055994531);
-    e = __builtin_fma(e, r, 1.0);
-    return __builtin_ldexp(e, (int)__double_as_longlong(t));
+  __device__ __forceinline__ static int bin(uint64_t place) {
+    return (int)((unsigned)(place >> 28) & (kBins - 1));
+  }
+  __device__ __forceinline__ unsigned long long tally(uint64_t place) const {
+    const float f = (float)((unsigned)place & 0xFFFFFFFu);
+    const float y = f * __builtin_fmaf(f, __builtin_fmaf(f, __builtin_fmaf(f, c4, c3), c2), c1);
+    return (1ull << low) + (unsigned)(y + 0.5f);
+  }
+  __device__ __forceinline__ int count(unsigned long long t) const { return (int)(t >> low); }
+  // of a bin whose upper logit weighs 1
+  __device__ __forceinline__ double weight(unsigned long long t) const {
+    return (double)count(t) - (double)(t & ((1ull << low) - 1)) / (double)units;
   }
 };
 
-__device__ __forceinline__ uint64_t composite(float l, int idx) {
-  return ((uint64_t)to_key(l) << 32) | (0xFFFFFFFFu - (unsigned)idx);
-}
-
-__device__ __forceinline__ double shfl_xor_f64(double x, int d) { return __shfl_xor(x, d, 64); }
-
-// A stretch of the order whose tokens are collected: bins lo .. hi (none: hi < 0), the count and
-// weight of all tokens before it, and its tokens first .. first + size - 1 of the collected ones.
-struct Interval {
-  int lo, hi, count0, first, size;
-  double mass0;
-};
-
-struct Shared {
-  uint64_t cand[kCap];
-  union {
-    double cum[kCap];
-    struct {
-      unsigned long long mass[kBins];
-      int bins[kBins];
-    };
-    uint16_t hits[kParts * kThreads];  // parts to read again: thread + kThreads * part
-  };
-  int rank[256];
-  int wave_n[2][kWaves];
-  float wave_g[kWaves];
-  double wave_d[kWaves];
-  float wave_f[kWaves];
-  int wave_i[kWaves];
-  Interval iv[4];
-  int count, nhits;
-  int best;
-  int solved;
-  int found[4];
-  double found_d;
-};
-
-__device__ double block_sum(Shared& sh, double x) {
+// ---- sums over the workgroup, in a fixed order, to all threads
+__device__ __noinline__ double block_sum(double x) {
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x += shfl_xor_f64(x, d);
+  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) sh.wave_d[threadIdx.x >> 6] = x;
   __syncthreads();
@@ -233,7 +199,7 @@ __device__ double block_sum(Shared& sh, double x) {
   for (int w = 0; w < kWaves; ++w) t += sh.wave_d[w];
   return t;
 }
-__device__ int block_count(Shared& sh, int x) {
+__device__ __noinline__ int block_count(int x) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
   __syncthreads();
@@ -244,8 +210,10 @@ __device__ int block_count(Shared& sh, int x) {
   for (int w = 0; w < kWaves; ++w) t += sh.wave_i[w];
   return t;
 }
-// the largest x, and the smallest in *least
-__device__ float block_max(Shared& sh, float x, float* least) {
+struct Range {
+  float most, least;
+};
+__device__ __noinline__ Range block_range(float x) {
   float y = x;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -258,74 +226,221 @@ __device__ float block_max(Shared& sh, float x, float* least) {
     sh.wave_g[threadIdx.x >> 6] = y;
   }
   __syncthreads();
-  float t = sh.wave_f[0], u = sh.wave_g[0];
+  Range r = {sh.wave_f[0], sh.wave_g[0]};
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) {
-    t = fmaxf(t, sh.wave_f[w]);
-    u = fminf(u, sh.wave_g[w]);
+    r.most = fmaxf(r.most, sh.wave_f[w]);
+    r.least = fminf(r.least, sh.wave_g[w]);
   }
-  *least = u;
-  return t;
+  return r;
+}
+// Running sums of one count and one weight per thread, without its own.
+struct Before {
+  int count;
+  double mass;
+};
+__device__ __noinline__ Before block_prefix(int n, double m) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int y = n;
+  double z = m;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int a = __shfl_up(y, d, 64);
+    const double b = __shfl_up(z, d, 64);
+    if (lane >= d) {
+      y += a;
+      z += b;
+    }
+  }
+  __syncthreads();
+  if (lane == 63) {
+    sh.wave_i[wave] = y;
+    sh.wave_d[wave] = z;
+  }
+  __syncthreads();
+  Before r = {0, 0.0};
+#pragma unroll
+  for (int w = 0; w < kWaves - 1; ++w) {
+    const bool in = w < wave;
+    r.count += in ? sh.wave_i[w] : 0;
+    r.mass += in ? sh.wave_d[w] : 0.0;
+  }
+  r.count += y - n;
+  r.mass += z - m;
+  return r;
 }
 
-// Count and weight of the row's tokens at or above a composite.
-template <bool F32>
-__device__ void above(Shared& sh, const Row<F32>& row, uint64_t c, float top, double inv_t,
-                      int* count, double* mass) {
-  int n = 0;
-  double s = 0;
-  auto one = [&](float l, int idx) {
-    if (composite(l, idx) >= c) {
-      ++n;
-      s += weight(l, top, inv_t);
+// One reading of the row by the workgroup, kParts vectors a thread in flight ahead of the ones that
+// are worked on: each(vectors, i0) gets the vectors tid + (i0 + q) * kThreads, q < kParts (past the
+// row's end: its last one); one(l, idx) the elements before and after the vectors.
+template <bool F32, class Each, class One>
+__device__ __forceinline__ void read_batches(const Row<F32>& row, Each each, One one) {
+  const int tid = threadIdx.x;
+  u32x4 r[kParts], nx[kParts];
+  auto fetch = [&](int i0, u32x4* v) {
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) v[q] = row.raw(min(tid + (i0 + q) * kThreads, row.nv - 1));
+  };
+  if (row.iters > 0) fetch(0, r);
+  if (tid < row.extra) {
+    const int idx = row.extra_index(tid);
+    one(row.one(idx), idx);
+  }
+  for (int i0 = 0; i0 < row.iters; i0 += kParts) {
+    if (i0 + kParts < row.iters) fetch(i0 + kParts, nx);
+    each(r, i0);
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) r[q] = nx[q];
+  }
+}
+
+// Puts the tokens with lo <= logit <= hi that `keep` confirms into sh.cand (sh.count counts them,
+// also beyond kCap), the row read in full: a mask of a batch's elements first, so that the many that
+// fail cost two comparisons each.
+template <bool F32, class Keep>
+__device__ __forceinline__ void collect_row(const Row<F32>& row, float lo, float hi, Keep keep) {
+  constexpr int kE = Row<F32>::kE;
+  auto take = [&](float l, int idx) {
+    if (l >= lo && l <= hi && l > kNegInf && keep(l)) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kCap) sh.cand[at] = composite(l, idx);
     }
   };
-  read_row<F32>(row, one);
-  *count = block_count(sh, n);
-  *mass = block_sum(sh, s);
+  read_batches<F32>(
+      row,
+      [&](const u32x4* r, int i0) {
+        unsigned mask = 0;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+          unsigned m = 0;
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
+            const float l = row.part(r[q], e);
+            m |= (unsigned)((l >= lo) & (l <= hi)) << e;
+          }
+          if ((int)threadIdx.x + (i0 + q) * kThreads < row.nv) mask |= m << (kE * q);
+        }
+        while (mask) {
+          const int bit = __builtin_ctz(mask);
+          mask &= mask - 1;
+          const int v = (int)threadIdx.x + (i0 + bit / kE) * kThreads;
+          const int idx = row.head + v * kE + bit % kE;
+          take(row.one(idx), idx);
+        }
+      },
+      take);
 }
-
-// The largest composite c for which reached(count above c, weight above c) holds; it does for 0.
-template <bool F32, class Reached>
-__device__ uint64_t bisect(Shared& sh, const Row<F32>& row, float top, double inv_t, Reached reached) {
-  uint64_t lo = 0, hi = ((uint64_t)to_key(top) << 32) | 0xFFFFFFFFull;
-  while (lo < hi) {
-    const uint64_t mid = lo + (hi - lo) / 2 + 1;
-    int n;
-    double s;
-    above<F32>(sh, row, mid, top, inv_t, &n, &s);
-    if (reached(n, s)) lo = mid;
-    else hi = mid - 1;
+// The same, reading only the parts listed in sh.hits (by all threads alike) and this thread's own
+// element ev at ei.
+template <bool F32, class Keep>
+__device__ __forceinline__ void collect_hits(const Row<F32>& row, float ev, int ei, float lo, float hi,
+                                             Keep keep) {
+  constexpr int kE = Row<F32>::kE;
+  auto take = [&](float l, int idx) {
+    if (l >= lo && l <= hi && l > kNegInf && keep(l)) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kCap) sh.cand[at] = composite(l, idx);
+    }
+  };
+  take(ev, ei);
+  const int per = (row.iters + kParts - 1) / kParts, total = sh.nhits * per;
+  for (int e0 = threadIdx.x; e0 < total; e0 += kThreads) {
+    const int item = e0 / per, hit = sh.hits[item];
+    const int v = (hit & (kThreads - 1)) + (hit / kThreads + kParts * (e0 - item * per)) * kThreads;
+    if (v < row.nv) {
+      const u32x4 r = row.raw(v);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) take(row.part(r, e), row.head + v * kE + e);
+    }
   }
-  return lo;
+}
+// Lists the parts whose maximum is at least lo.
+__device__ __forceinline__ void list_hits(const float* part, float lo) {
+#pragma unroll
+  for (int q = 0; q < kParts; ++q)
+    if (part[q] >= lo && part[q] > kNegInf)
+      sh.hits[atomicAdd(&sh.nhits, 1)] = (uint16_t)(threadIdx.x + kThreads * q);
 }
 
 // Sorts sh.cand[0 .. n) in descending order (all threads).  Up to 256 tokens by rank, the number of
-// greater ones, which all waves count (each a slice of the comparisons); more by a bitonic network,
-// whose steps of up to 64 stay within 128 tokens of one wave and need no barrier.
-__device__ void sort_candidates(Shared& sh, int n) {
+// greater ones, which all waves count (each a slice of the comparisons).  More: kThreads buckets of
+// equal width from the largest logit down to the least, and the rank within the bucket; a bitonic
+// network where a bucket gets too many for that.
+__device__ __noinline__ void sort_candidates(int n) {
   const int tid = threadIdx.x;
+  sh.bucket[tid] = 0;
+  if (tid == 0) sh.most = 0;
+  __syncthreads();
   if (n <= 256) {
     const int width = n <= 64 ? 64 : (n <= 128 ? 128 : 256);
-    if (tid < width) sh.rank[tid] = 0;
-    __syncthreads();
     const int i = tid & (width - 1), slices = kThreads / width, s = tid / width;
     const uint64_t c = i < n ? sh.cand[i] : 0;
     int rank = 0;
     for (int j = n * s / slices; j < n * (s + 1) / slices; ++j) rank += sh.cand[j] > c;
-    if (i < n && rank) atomicAdd(&sh.rank[i], rank);
+    if (i < n && rank) atomicAdd(&sh.bucket[i], rank);
     __syncthreads();
-    if (tid < n) sh.cand[sh.rank[tid]] = c;
+    if (tid < n) sh.cand[sh.bucket[tid]] = c;
     __syncthreads();
     return;
   }
-  int size = 512;
-  while (size < n) size <<= 1;
-  for (int i = n + tid; i < size; i += kThreads) sh.cand[i] = 0;
+  float least = __builtin_inff(), most = kNegInf;
+  for (int j = tid; j < n; j += kThreads) {
+    const float l = logit_of(sh.cand[j]);
+    least = fminf(least, l);
+    most = fmaxf(most, l);
+  }
+  most = block_range(most).most;
+  least = block_range(least).least;
+  const float width = (most - least) * (1.0f / kThreads);
+  const float inv = width > 0.f && width < __FLT_MAX__ ? 1.0f / width : 0.f;
+  uint64_t c[kPer];
+  int place[kPer];  // bucket * 2^16 + slot
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int j = tid + kThreads * i;
+    c[i] = 0;
+    place[i] = 0;
+    if (j < n) {
+      c[i] = sh.cand[j];
+      const int b = (int)fminf((most - logit_of(c[i])) * inv, (float)(kThreads - 1));
+      place[i] = (b << 16) + atomicAdd(&sh.bucket[b], 1);
+    }
+  }
   __syncthreads();
-  for (int len = 2; len <= size; len <<= 1)
+  const int size = sh.bucket[tid];
+  if (size > 256) sh.most = 1;
+  const int begin = block_prefix(size, 0.0).count;
+  if (sh.most == 0) {
+    sh.bucket[tid] = begin;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (tid + kThreads * i < n) sh.cand[sh.bucket[place[i] >> 16] + (place[i] & 0xFFFF)] = c[i];
+    __syncthreads();
+    int rank[kPer];
+    for (int i = 0; i < kPer; ++i) {
+      rank[i] = 0;
+      if (tid + kThreads * i < n) {
+        const int b = place[i] >> 16;
+        const int first = sh.bucket[b], last = b + 1 < kThreads ? sh.bucket[b + 1] : n;
+        rank[i] = first;
+        for (int j = first; j < last; ++j) rank[i] += sh.cand[j] > c[i];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (tid + kThreads * i < n) sh.cand[rank[i]] = c[i];
+    __syncthreads();
+    return;
+  }
+  int pow2 = 512;
+  while (pow2 < n) pow2 <<= 1;
+  for (int i = n + tid; i < pow2; i += kThreads) sh.cand[i] = 0;
+  __syncthreads();
+  for (int len = 2; len <= pow2; len <<= 1)
     for (int step = len >> 1; step > 0; step >>= 1) {
-      for (int i = tid; i < size / 2; i += kThreads) {
+      for (int i = tid; i < pow2 / 2; i += kThreads) {
         const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
         const uint64_t x = sh.cand[lo], y = sh.cand[hi];
         const bool down = (lo & len) == 0;
@@ -334,57 +449,75 @@ __device__ void sort_candidates(Shared& sh, int n) {
           sh.cand[hi] = x;
         }
       }
-      // the next step (step / 2, or the first of the next length) crosses waves?
-      const int next = step > 1 ? step >> 1 : len;
-      if (next > 64 || step > 64) __syncthreads();
-      else __builtin_amdgcn_wave_barrier();
+      __syncthreads();
     }
-  __syncthreads();
 }
 
-constexpr int kPer = kCap / kThreads;  // sorted tokens per thread: kPer t .. kPer t + kPer - 1
-
-// Weights of the sorted tokens and their running sums (c, sh.cum).
-__device__ void weigh(Shared& sh, int n, float top, double inv_t, double* w, double* c) {
-  const int tid = threadIdx.x, lane = tid & 63;
+// Running sums of the sorted tokens' weights into sh.cum.
+__device__ __noinline__ void weigh(int n, float top, double inv_t) {
+  const int first = kPer * (int)threadIdx.x;
   double x = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int j = kPer * tid + i;
-    w[i] = j < n ? weight(from_key((unsigned)(sh.cand[j] >> 32)), top, inv_t) : 0.0;
-    x += w[i];
-    c[i] = x;
+#pragma unroll 1
+  for (int j = first; j < min(first + kPer, n); ++j) {
+    const double w = weight(logit_of(sh.cand[j]), top, inv_t);
+    sh.cum[j] = w;
+    x += w;
   }
-  double y = x;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double z = __shfl_up(y, d, 64);
-    if (lane >= d) y += z;
-  }
-  if (lane == 63) sh.wave_d[tid >> 6] = y;
-  __syncthreads();
-  double before = y - x;
-#pragma unroll
-  for (int v = 0; v < kWaves; ++v)
-    if (v < (tid >> 6)) before += sh.wave_d[v];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    c[i] += before;
-    sh.cum[kPer * tid + i] = c[i];
+  x = block_prefix(0, x).mass;
+#pragma unroll 1
+  for (int j = first; j < min(first + kPer, n); ++j) {
+    x += sh.cum[j];
+    sh.cum[j] = x;
   }
   __syncthreads();
 }
-
-// How many of this thread's sorted tokens from `from` up to `to` satisfy f(i), summed over all.
-template <class F>
-__device__ int count_tokens(Shared& sh, int from, int to, F f) {
+// How many of the first n running sums are below t (or equal, too).
+__device__ __noinline__ int count_below(int n, double t, bool or_equal) {
   int x = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int j = kPer * (int)threadIdx.x + i;
-    x += j >= from && j < to && f(i);
+#pragma unroll 1
+  for (int j = threadIdx.x; j < n; j += kThreads) x += or_equal ? sh.cum[j] <= t : sh.cum[j] < t;
+  return block_count(x);
+}
+// How many of the first n sorted tokens weigh at least m.
+__device__ __noinline__ int count_heavy(int n, double m, float top, double inv_t) {
+  int x = 0;
+#pragma unroll 1
+  for (int j = threadIdx.x; j < n; j += kThreads) x += weight(logit_of(sh.cand[j]), top, inv_t) >= m;
+  return block_count(x);
+}
+
+// ---- bisection: the last resort
+// Count and weight of the row's tokens at or above a composite.
+template <bool F32>
+__device__ __noinline__ Before above(const Row<F32> row, uint64_t c, float top, double inv_t) {
+  int n = 0;
+  double s = 0;
+  auto one = [&](float l, int idx) {
+    if (composite(l, idx) >= c) {
+      ++n;
+      s += weight(l, top, inv_t);
+    }
+  };
+  if ((int)threadIdx.x < row.extra) one(row.one(row.extra_index(threadIdx.x)), row.extra_index(threadIdx.x));
+#pragma unroll 1
+  for (int i = threadIdx.x; i < row.nv * Row<F32>::kE; i += kThreads) one(row.one(row.head + i), row.head + i);
+  const Before r = {block_count(n), block_sum(s)};
+  return r;
+}
+// The largest composite c at or above which there are `count` tokens, a weight of `mass`, or (strict)
+// a weight of more than `mass`; 0 if there is none.
+template <bool F32>
+__device__ __noinline__ uint64_t bisect(const Row<F32> row, float top, double inv_t, int count, double mass,
+                                        bool strict) {
+  uint64_t lo = 0, hi = ((uint64_t)to_key(top) << 32) | 0xFFFFFFFFull;
+  while (lo < hi) {
+    const uint64_t mid = lo + (hi - lo) / 2 + 1;
+    const Before x = above<F32>(row, mid, top, inv_t);
+    const bool reached = count > 0 ? x.count >= count : (strict ? x.mass > mass : x.mass >= mass);
+    if (reached) lo = mid;
+    else hi = mid - 1;
   }
-  return block_count(sh, x);
+  return lo;
 }
 
 // A row's settings.
@@ -393,266 +526,147 @@ struct Filters {
   double p, minp, u;   // p >= 1, minp = 0: off
   double inv_t;
 };
+struct Answer {
+  uint64_t token;
+  double kept;  // the weight of the tokens kept
+  bool found;
+};
 
-// Second way: bins, then the tokens of the bins that hold a border.  False: too many of those.
 template <bool F32>
-__device__ bool by_bins(Shared& sh, const Row<F32>& row, const Filters& f, float top,
-                        uint64_t* token, double* kept) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  const double scale = f.inv_t * kBinScale;
-  const bool open = top == __builtin_inff();  // only infinite logits weigh anything
-  const double dtop = open ? (double)__FLT_MAX__ : (double)top;
+__device__ __noinline__ Answer by_bisection(const Row<F32> row, const Filters f, float top) {
+  uint64_t border = 0;
+  if (f.k < f.vocab) border = bisect<F32>(row, top, f.inv_t, f.k, 0.0, false);
+  if (f.p < 1.0) {
+    const double zk = above<F32>(row, border, top, f.inv_t).mass;
+    const uint64_t c = bisect<F32>(row, top, f.inv_t, 0, f.p * zk, false);
+    border = c > border ? c : border;
+  }
+  if (f.minp > 0.0) {
+    unsigned lo = 0, hi = to_key(top);  // the smallest key with w >= min_p
+    while (lo < hi) {
+      const unsigned mid = lo + (hi - lo) / 2;
+      if (weight(clean(from_key(mid)), top, f.inv_t) >= f.minp) hi = mid;
+      else lo = mid + 1;
+    }
+    const uint64_t c = (uint64_t)lo << 32;
+    border = c > border ? c : border;
+  }
+  const double zn = above<F32>(row, border, top, f.inv_t).mass;
+  uint64_t hit = bisect<F32>(row, top, f.inv_t, 0, f.u * zn, true);
+  // u * zn rounded up to zn: the last token kept that weighs something
+  if (hit < border || hit == 0) hit = bisect<F32>(row, top, f.inv_t, 0, zn, false);
+  return Answer{hit, zn, true};
+}
+
+// The answer from the tallied bins: each border in turn (top-k,
+// top-p, min-p, the draw) lies in one bin, whose tokens are collected and sorted.  part: this
+// thread's maxima; ev, ei: its single element.  Not found: too many tokens in a bin.
+template <bool F32>
+__device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f, float top,
+                                          const Bins& bins, const float* part, float ev, int ei) {
   constexpr int kOwn = kBins / kThreads;
-  __syncthreads();
-  for (int i = tid; i < kBins; i += kThreads) {
-    sh.bins[i] = 0;
-    sh.mass[i] = 0;
-  }
-  if (tid == 0) sh.count = 0;
-  if (tid < 4) {
-    sh.found[tid] = kBins - 1;
-    sh.iv[tid].lo = kBins;
-    sh.iv[tid].hi = -1;
-    sh.iv[tid].size = 0;
-  }
-  __syncthreads();
-  // A token at place b + x of bin b weighs e^(-b / 128) (1 - y), y = 1 - e^(-x / 128) < 2^-7.  The
-  // bins sum the y, as integers in units of 2^-38 (so that the sums do not depend on the order of
-  // the additions), from fp32: y is off by at most about 2^-31.
-  read_row<F32>(row, [&](float l, int) {
-    if (l > kNegInf && !open) {
-      const double place = bin_place(l, dtop, scale);
-      const int b = (int)place;
-      const float x = (float)(place - (double)b) * (1.0f / kBinScale);
-      const float y = x * __builtin_fmaf(x, __builtin_fmaf(x, 1.0f / 6.0f, -0.5f), 1.0f);
-      atomicAdd(&sh.bins[b], 1);
-      atomicAdd(&sh.mass[b], (unsigned long long)(unsigned)(y * 274877906944.0f));
-    } else if (l > kNegInf) {
-      atomicAdd(&sh.bins[l == top ? 0 : kBins - 1], 1);
-    }
-  });
-  __syncthreads();
-
-  // ---- running counts and weights at the end of each of this thread's bins
-  int cnt[kOwn];
-  double mass[kOwn];
+  const int tid = threadIdx.x;
+  const double inv_scale = 1.0 / bins.scale, ref = (bins.offset - 25165824.0) * inv_scale;
+  const double lead = (double)(bins.place(top) & 0xFFFFFFFFFFull) * (1.0 / 268435456.0);  // of the largest
+  // running counts and weights (of the largest logit: 1) at the end of this thread's bins
+  int cnt[kOwn], cnt0 = 0;
+  double mass[kOwn], mass0 = 0;
   {
-    int cn = 0;
-    double m = 0;
+    // bins far above the largest logit are empty
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-      const int b = kOwn * tid + i, n = sh.bins[b];
-      cn += n;
-      const double e = open ? (b == 0 ? 1.0 : 0.0) : exp_f64(-(double)b / kBinScale);
-      m += e * ((double)n - (double)sh.mass[b] * 3.637978807091713e-12);
-      cnt[i] = cn;
-      mass[i] = m;
+      const int b = kOwn * tid + i;
+      const unsigned long long t = sh.bins[b];
+      const double e = (lead - (double)b) * (1.0 / kBinScale);
+      cnt0 += bins.count(t);
+      if (t) mass0 += exp_f64(e - 1.0) * 2.718281828459045235 * bins.weight(t);
+      cnt[i] = cnt0;
+      mass[i] = mass0;
     }
-    int xc = cn;
-    double xm = m;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int yc = __shfl_up(xc, d, 64);
-      const double ym = __shfl_up(xm, d, 64);
-      if (lane >= d) {
-        xc += yc;
-        xm += ym;
-      }
-    }
-    if (lane == 63) {
-      sh.wave_i[tid >> 6] = xc;
-      sh.wave_d[tid >> 6] = xm;
-    }
-    __syncthreads();
-    xc -= cn;
-    xm -= m;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w)
-      if (w < (tid >> 6)) {
-        xc += sh.wave_i[w];
-        xm += sh.wave_d[w];
-      }
+    const Before b = block_prefix(cnt0, mass0);
+    cnt0 = b.count;
+    mass0 = b.mass;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-      cnt[i] += xc;
-      mass[i] += xm;
+      cnt[i] += cnt0;
+      mass[i] += mass0;
     }
   }
-  // the first bin that passes, the last bin if none does
-  auto first_bin = [&](int slot, auto passes) {
+  if (tid == kThreads - 1) sh.found_mass = mass[kOwn - 1];
+  __syncthreads();
+  int keep = f.vocab;                  // tokens kept
+  double zk = sh.found_mass, zn = zk;  // weight of the first k, of the tokens kept
+  Answer r = {0, 0.0, false};
+  __syncthreads();
+#pragma unroll 1
+  for (int stage = 0; stage < 4; ++stage) {
+    if (stage == 0 ? f.k == f.vocab : (stage == 1 ? f.p >= 1.0 : (stage == 2 && f.minp == 0.0))) continue;
+    // the border's bin: the first whose value passes the target, the last bin if none does
+    const double target = stage == 0   ? (double)f.k
+                          : stage == 1 ? f.p * zk
+                          : stage == 2 ? floor(lead - log(f.minp) * kBinScale)
+                                       : f.u * zn;
+    bool earlier = false;
 #pragma unroll
-    for (int i = kOwn - 1; i >= 0; --i)
-      if (passes(i)) atomicMin(&sh.found[slot], kOwn * tid + i);
-    __syncthreads();
-    const int b = sh.found[slot];
-    __syncthreads();
-    if (tid == 0) sh.found[slot] = kBins - 1;
-    return b;
-  };
-  auto mass_to = [&](int bin) {  // the weight up to and including a bin, to all threads
-    if (bin >= 0 && bin / kOwn == tid) {
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i)
-        if (bin % kOwn == i) sh.found_d = mass[i];
-    }
-    __syncthreads();
-    const double r = bin < 0 ? 0.0 : sh.found_d;
-    __syncthreads();
-    return r;
-  };
-  // ---- the bins of each border: top-k, top-p, min-p, the draw.  Bounds of what a border depends
-  // on (the weight of the first k, of the kept tokens) may spread it over several.
-  constexpr double kSlack = 1e-10;
-  int blo[4], bhi[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    blo[i] = kBins;
-    bhi[i] = -1;
-  }
-  const double z = mass_to(kBins - 1);
-  double zk_lo = z, zk_hi = z;
-  if (f.k < f.vocab) {
-    blo[0] = bhi[0] = first_bin(0, [&](int i) { return cnt[i] >= f.k; });
-    zk_lo = mass_to(blo[0] - 1);
-    zk_hi = mass_to(bhi[0]);
-  }
-  double zn_lo = zk_lo, zn_hi = zk_hi;
-  if (f.p < 1.0) {
-    const double t0 = f.p * zk_lo * (1.0 - kSlack), t1 = f.p * zk_hi * (1.0 + kSlack);
-    blo[1] = first_bin(1, [&](int i) { return mass[i] >= t0; });
-    bhi[1] = first_bin(1, [&](int i) { return mass[i] >= t1; });
-    zn_lo = fmin(zn_lo, fmax(t0, mass_to(blo[1] - 1)));
-    zn_hi = fmin(zn_hi, mass_to(bhi[1]));
-  }
-  if (f.minp > 0.0) {
-    const double d = -log(f.minp) * kBinScale;
-    blo[2] = (int)fmin(fmax(d * (1.0 - 1e-5) - 0.01, 0.0), (double)(kBins - 1));
-    bhi[2] = (int)fmin(d * (1.0 + 1e-5) + 0.01, (double)(kBins - 1));
-    zn_lo = fmin(zn_lo, mass_to(blo[2] - 1));
-    zn_hi = fmin(zn_hi, mass_to(bhi[2]));
-  }
-  {
-    const double t0 = f.u * zn_lo * (1.0 - kSlack), t1 = f.u * zn_hi * (1.0 + kSlack);
-    blo[3] = first_bin(3, [&](int i) { return mass[i] > t0; });
-    bhi[3] = first_bin(3, [&](int i) { return mass[i] > t1; });
-  }
-  // ---- as disjoint intervals, in order: sort by lo, join those that touch
-  if (tid == 0) {
-    int ilo[4], ihi[4], m = 0;
-    for (int i = 0; i < 4; ++i)
-      if (bhi[i] >= 0) {
-        int j = m++;
-        for (; j > 0 && ilo[j - 1] > blo[i]; --j) {
-          ilo[j] = ilo[j - 1];
-          ihi[j] = ihi[j - 1];
-        }
-        ilo[j] = blo[i];
-        ihi[j] = bhi[i];
+    for (int i = -1; i < kOwn; ++i) {
+      const int b = kOwn * tid + i, c = i < 0 ? cnt0 : cnt[i < 0 ? 0 : i];
+      const double m = i < 0 ? mass0 : mass[i < 0 ? 0 : i];
+      const double x = stage == 0 ? (double)c : (stage == 2 ? (double)b : m);
+      const bool here = b >= 0 && (stage == 3 ? x > target : x >= target);
+      if (i >= 0 && !earlier && (here || b == kBins - 1)) {
+        sh.found = b;
+        sh.found_count = i == 0 ? cnt0 : cnt[i > 0 ? i - 1 : 0];
+        sh.found_mass = i == 0 ? mass0 : mass[i > 0 ? i - 1 : 0];
+        sh.best = c;
       }
-    int n = 0;
-    for (int i = 0; i < m; ++i) {
-      if (n > 0 && ilo[i] <= sh.iv[n - 1].hi + 1) {
-        if (ihi[i] > sh.iv[n - 1].hi) sh.iv[n - 1].hi = ihi[i];
-      } else {
-        sh.iv[n].lo = ilo[i];
-        sh.iv[n].hi = ihi[i];
-        sh.iv[n].count0 = 0;
-        sh.iv[n].mass0 = 0.0;
-        ++n;
+      earlier = here;
+    }
+    if (tid == 0) sh.count = sh.nhits = 0;
+    __syncthreads();
+    const int bin = sh.found, before = sh.found_count, n = sh.best - before;
+    const double mass_before = sh.found_mass;
+    if (n > kCap) return r;
+    // the bin's tokens; bounds in logits, with a margin for their rounding, pass over most others
+    const double up = ref - (double)bin * inv_scale, down = up - inv_scale;
+    const double slack = 1e-6 * (fabs(up) + fabs(down)) + 1e-3 * inv_scale;
+    const float hi = (float)(up + slack), lo = bin == kBins - 1 ? kNegInf : (float)(down - slack);
+    auto keep_it = [&](float l) { return Bins::bin(bins.place(l)) == bin; };
+    list_hits(part, lo);
+    __syncthreads();
+    if (sh.nhits > kParts * kThreads / 4) collect_row<F32>(row, lo, hi, keep_it);
+    else collect_hits<F32>(row, ev, ei, lo, hi, keep_it);
+    __syncthreads();
+    sort_candidates(n);
+    weigh(n, top, f.inv_t);
+    if (stage == 0) {
+      const int j = f.k - before;
+      if (j <= n) {  // (else fewer than k tokens are not masked: all of them)
+        keep = f.k;
+        zk = zn = mass_before + sh.cum[j - 1];
       }
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    const int b = kOwn * tid + i;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if (b == sh.iv[v].lo - 1) {
-        sh.iv[v].count0 = cnt[i];
-        sh.iv[v].mass0 = mass[i];
+    } else if (stage == 1) {
+      const int m = min(count_below(n, target - mass_before, false), n - 1);
+      if (before + m + 1 < keep) {
+        keep = before + m + 1;
+        zn = mass_before + (m >= 0 ? sh.cum[m] : 0.0);
       }
-      if (b == sh.iv[v].hi) sh.iv[v].size = cnt[i];
-    }
-  }
-  __syncthreads();
-  if (tid == 0) {
-    int first = 0;
-    for (int v = 0; v < 4; ++v) {
-      Interval& I = sh.iv[v];
-      if (I.hi >= 0) I.size -= I.count0;
-      I.first = first;
-      first += I.size;
-    }
-    sh.found[0] = first;
-  }
-  __syncthreads();
-  const int n = sh.found[0];
-  if (n > kCap || n == 0) return false;
-
-  // ---- third reading: collect the intervals' tokens
-  const int lo0 = sh.iv[0].lo, hi0 = sh.iv[0].hi, lo1 = sh.iv[1].lo, hi1 = sh.iv[1].hi;
-  const int lo2 = sh.iv[2].lo, hi2 = sh.iv[2].hi, lo3 = sh.iv[3].lo, hi3 = sh.iv[3].hi;
-  const int nint = hi3 >= 0 ? 4 : (hi2 >= 0 ? 3 : (hi1 >= 0 ? 2 : 1));
-  read_row<F32>(row, [&](float l, int idx) {
-    const int b = open ? (l == top ? 0 : kBins - 1) : (int)bin_place(l, dtop, scale);
-    bool in = b >= lo0 && b <= hi0;
-    if (nint > 1) in |= b >= lo1 && b <= hi1;
-    if (nint > 2) in |= (b >= lo2 && b <= hi2) || (b >= lo3 && b <= hi3);
-    if (in && l > kNegInf) sh.cand[atomicAdd(&sh.count, 1)] = composite(l, idx);
-  });
-  __syncthreads();
-  sort_candidates(sh, n);
-  double w[kPer], c[kPer];
-  weigh(sh, n, top, f.inv_t, w, c);
-  // the interval that holds a border's bins, and what its running sums lack
-  auto home = [&](int bin) { return bin <= hi0 ? 0 : (bin <= hi1 ? 1 : (bin <= hi2 ? 2 : 3)); };
-  auto lacks = [&](const Interval& I) { return I.mass0 - (I.first > 0 ? sh.cum[I.first - 1] : 0.0); };
-  // ---- the filters' prefixes: counts and weights
-  int keep = f.vocab;
-  double zk = z, zn = z;
-  if (f.k < f.vocab) {
-    const Interval& I = sh.iv[home(blo[0])];
-    const int j = I.first + f.k - I.count0 - 1;
-    if (j < I.first || j >= I.first + I.size) {
-      if (f.k <= I.count0) return false;
-      // fewer than k tokens are not masked: all of them
+    } else if (stage == 2) {
+      const int m = count_heavy(n, f.minp, top, f.inv_t);
+      if (before + m < keep) {
+        keep = max(before + m, 1);
+        zn = fmax(mass_before + (m > 0 ? sh.cum[m - 1] : 0.0), 1.0);
+      }
     } else {
-      zk = zn = sh.cum[j] + lacks(I);
-      keep = f.k;
+      const int m = min(min(count_below(n, target - mass_before, true), n - 1), keep - 1 - before);
+      if (m >= 0) r = Answer{sh.cand[m], zn, true};
     }
+    __syncthreads();
   }
-  if (f.p < 1.0) {
-    const Interval& I = sh.iv[home(blo[1])];
-    const double t = f.p * zk - lacks(I);
-    int m = count_tokens(sh, I.first, I.first + I.size, [&](int i) { return c[i] < t; });
-    m = min(m, I.size - 1);  // (running sums rounded below the bin's)
-    if (I.count0 + m + 1 < keep) {
-      keep = I.count0 + m + 1;
-      zn = sh.cum[I.first + m] + lacks(I);
-    }
-  }
-  if (f.minp > 0.0) {
-    const Interval& I = sh.iv[home(blo[2])];
-    const int m = count_tokens(sh, I.first, I.first + I.size, [&](int i) { return w[i] >= f.minp; });
-    if (I.count0 + m < keep) {
-      keep = I.count0 + m;
-      zn = m > 0 ? sh.cum[I.first + m - 1] + lacks(I) : I.mass0;
-    }
-  }
-  const Interval& I = sh.iv[home(blo[3])];
-  const double t = f.u * zn - lacks(I);
-  int m = count_tokens(sh, I.first, I.first + I.size, [&](int i) { return c[i] <= t; });
-  m = min(min(m, I.size - 1), keep - 1 - I.count0);
-  if (m < 0) return false;
-  *token = sh.cand[I.first + m];
-  *kept = zn;
-  return true;
+  return r;
 }
 
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
-  __shared__ Shared sh;
   constexpr int kE = Row<F32>::kE;
   const int tid = threadIdx.x, lane = tid & 63;
   const int b = blockIdx.x;
@@ -672,63 +686,63 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
   const bool greedy = !(temp > 0.0f) || k == 1 || p <= 0.0 || minp > 1.0;
   const double inv_t = greedy ? 1.0 : 1.0 / (double)temp;
   const bool known_k = k <= kMaxK;
-  const bool need_z = !greedy && k == vocab && !known_k && (p < 1.0 || minp == 0.0);
+  // no filter says how many tokens to collect: tally the bins while reading
+  const bool binned = !greedy && !known_k && (k < vocab || p < 1.0 || minp == 0.0) &&
+                      vocab <= kMaxBinVocab;
+  Bins bins(vocab, inv_t);
 
-  // ---- one reading: maxima of the parts, and the row's weight where the filters need it
-  float part[kParts], ev = kNegInf, mt = kNegInf;
-  double st = 0;
-  const int iters = (row.nv + kThreads - 1) / kThreads;
+  // ---- one reading: maxima of the parts
+  float part[kParts], ev = kNegInf;
 #pragma unroll
   for (int q = 0; q < kParts; ++q) part[q] = kNegInf;
+  auto maxima = [&](const u32x4* r, int i0) {
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) {
+      // a vector past the end repeats the row's last one, which must not become this part's maximum
+      const bool in = tid + (i0 + q) * kThreads < row.nv;
+      float m4 = row.part(r[q], 0);
+#pragma unroll
+      for (int e = 1; e < kE; ++e) m4 = fmaxf(m4, row.part(r[q], e));
+      part[q] = fmaxf(part[q], in ? m4 : kNegInf);
+    }
+  };
+  // a logit beyond the bins (many, if T is small) is counted by its thread and added at the end
+  int beyond = 0;
+  auto tally_one = [&](float l) {  // (not for -inf and NaN)
+    const uint64_t at = bins.place(l);
+    const int bin = Bins::bin(at);
+    if (bin < kBins - 1) atomicAdd(&sh.bins[bin], bins.tally(at));
+    else if (l > kNegInf) ++beyond;
+  };
+  auto tally_batch = [&](const u32x4* r, int i0) {
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+      if (tid + (i0 + q) * kThreads < row.nv)
+#pragma unroll
+        for (int e = 0; e < kE; ++e) tally_one(row.plain(r[q], e));
+  };
+  bool bins_ready = binned;
+  if (binned)
+    for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = 0;
   read_batches<F32>(
       row,
       [&](const u32x4* r, int i0) {
-        float vm = mt;
+        maxima(r, i0);
+        if (binned) {
+          if (i0 == 0) {
+            // the bins (64 T of logits) begin a margin above the largest logit of the first batch
+            float m = ev;
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-          // a vector past the end repeats the row's last one: it adds no weight, and must not
-          // become this part's maximum
-          const bool in = tid + (i0 + q) * kThreads < row.nv;
-          float m4 = row.part(r[q], 0);
-#pragma unroll
-          for (int e = 1; e < kE; ++e) m4 = fmaxf(m4, row.part(r[q], e));
-          m4 = in ? m4 : kNegInf;
-          part[q] = fmaxf(part[q], m4);
-          vm = fmaxf(vm, m4);
-        }
-        if (need_z && vm > kNegInf) {
-          // weights relative to the thread's largest logit so far
-          if (vm > mt) {
-            st *= weight(mt, vm, inv_t);
-            mt = vm;
+            for (int q = 0; q < kParts; ++q) m = fmaxf(m, part[q]);
+            m = block_range(m).most;
+            bins_ready = m > kNegInf && bins.begin_at((double)m + fmin(12.0, 24.0 / inv_t));
           }
-          if (mt < __builtin_inff()) {
-            const Exp2 w(mt, inv_t);
-#pragma unroll
-            for (int q = 0; q < kParts; ++q) {
-              double v = 0;
-#pragma unroll
-              for (int e = 0; e < kE; ++e) v += w(row.part(r[q], e));
-              st += tid + (i0 + q) * kThreads < row.nv ? v : 0.0;
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < kParts; ++q)
-#pragma unroll
-              for (int e = 0; e < kE; ++e)
-                st += tid + (i0 + q) * kThreads < row.nv && row.part(r[q], e) == mt ? 1.0 : 0.0;
-          }
+          if (bins_ready) tally_batch(r, i0);
         }
       },
       [&](float l, int) { ev = l; });
+  if (binned && bins_ready && ev > kNegInf) tally_one(ev);
   const int ei = tid < row.extra ? row.extra_index(tid) : 0;
-  if (need_z && ev > kNegInf) {
-    if (ev > mt) {
-      st *= weight(mt, ev, inv_t);
-      mt = ev;
-    }
-    st += weight(ev, mt, inv_t);
-  }
   float mine = ev;
 #pragma unroll
   for (int s = 0; s < kParts; ++s) mine = fmaxf(mine, part[s]);
@@ -737,8 +751,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
     sh.nhits = 0;
     sh.best = vocab;
   }
-  float least;  // of the threads' maxima
-  const float top = block_max(sh, mine, &least);
+  const Range range = block_range(mine);
+  const float top = range.most;
   if (top == kNegInf) {  // every token is masked
     if (tid == 0) {
       a.tokens[b] = -1;
@@ -746,171 +760,93 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
     }
     return;
   }
-  double z = 0;
-  if (need_z) z = block_sum(sh, mt == kNegInf ? 0.0 : st * weight(mt, top, inv_t));
-
-  // ---- the bound: at least `want` tokens reach it
-  float tau;
-  bool all_min_p = false;  // the collected tokens include every one with w >= min_p
-  if (greedy) {
-    tau = top;
-  } else {
-    const int want = known_k ? k : min(kGuess, vocab);
-    // the want-th largest of the maxima, by bisection over their keys: every wave counts its own.
-    // A bound that a few more reach will do.  All kThreads >= want threads reach the least.
-    const bool few = want <= kFewK;
-    unsigned key[kParts];
+  Answer r = {0, 0.0, false};
+  if (!binned) {
+    // ---- a bound that at least k tokens reach
+    float tau = top;
+    if (!greedy && known_k) {
+      // the k-th largest of the maxima, by bisection over their keys: every wave counts its own.  A
+      // bound that a few more reach will do.  All threads reach the least of their maxima.
+      const bool few = k <= kFewK;
+      unsigned key[kParts];
 #pragma unroll
-    for (int q = 0; q < kParts; ++q) key[q] = to_key(q == 0 && few ? mine : part[q]);
-    unsigned lo = to_key(least), hi = to_key(top);
-    for (int turn = 0; lo < hi; turn ^= 1) {
-      const unsigned mid = lo + (hi - lo) / 2 + 1;
-      int n = __popcll(__ballot(key[0] >= mid));
-      if (!few)
+      for (int q = 0; q < kParts; ++q) key[q] = to_key(q == 0 && few ? mine : part[q]);
+      unsigned lo = k <= kThreads ? to_key(range.least) : 0, hi = to_key(top);
+#pragma unroll 1
+      for (int turn = 0; lo < hi; turn ^= 1) {
+        const unsigned mid = lo + (hi - lo) / 2 + 1;
+        int n = __popcll(__ballot(key[0] >= mid));
+        if (!few)
 #pragma unroll
-        for (int q = 1; q < kParts; ++q) n += __popcll(__ballot(key[q] >= mid));
-      if (lane == 0) sh.wave_n[turn][tid >> 6] = n;
-      __syncthreads();
-      n = 0;
+          for (int q = 1; q < kParts; ++q) n += __popcll(__ballot(key[q] >= mid));
+        if (lane == 0) sh.wave_n[turn][tid >> 6] = n;
+        __syncthreads();
+        n = 0;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) n += sh.wave_n[turn][w];
-      if (n >= want) lo = mid;
-      else hi = mid - 1;
-      if (n >= want && n <= want + (want >> 3)) break;
+        for (int w = 0; w < kWaves; ++w) n += sh.wave_n[turn][w];
+        if (n >= k) lo = mid;
+        else hi = mid - 1;
+        if (n >= k && n <= k + (k >> 3)) break;
+      }
+      // fewer maxima than k (a short row, or masked tokens): every token
+      tau = lo <= to_key(kNegInf) ? kNegInf : from_key(lo);
+    } else if (!greedy) {
+      tau = kNegInf;
+      if (p >= 1.0 && minp > 0.0) {
+        // every token that min_p keeps (and a margin for the rounding of this bound)
+        const float t = (float)((double)top + log(minp) / inv_t);
+        tau = top < __builtin_inff() ? t - fabsf(t) * 1e-5f - 1e-30f : top;
+      }
     }
-    // fewer maxima than wanted (a short row, or masked tokens): every token
-    tau = lo <= to_key(kNegInf) ? kNegInf : from_key(lo);
-    if (!known_k && minp > 0.0) {
-      // every token that min_p keeps (and a margin for the rounding of this bound)
-      const float t2 = (float)((double)top + log(minp) / inv_t);
-      tau = t2 - fabsf(t2) * 1e-5f - 1e-30f;
-      all_min_p = true;
-    }
+    // ---- the tokens that reach it: the first k, every token with w >= min_p, or every token that
+    // is not masked
+    list_hits(part, tau);
     __syncthreads();
-  }
-
-  // ---- collect the tokens at or above the bound: the parts that reach it, read again by all
-  // threads alike
-  auto collect = [&](float l, int idx) {
-    if (l >= tau && l > kNegInf) {
+    collect_hits<F32>(row, ev, ei, tau, top, [](float) { return true; });
+    __syncthreads();
+    const int n = sh.count;
+    if (n <= kCap) {
       if (greedy) {
-        atomicMin(&sh.best, idx);
+        // the first of the tokens at the top
+        for (int j = tid; j < n; j += kThreads)
+          atomicMin(&sh.best, (int)(0xFFFFFFFFu - (unsigned)sh.cand[j]));
+        __syncthreads();
+        r = Answer{composite(top, sh.best), 1.0, true};
       } else {
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < kCap) sh.cand[at] = composite(l, idx);
-      }
-    }
-  };
-#pragma unroll
-  for (int q = 0; q < kParts; ++q)
-    if (part[q] >= tau && part[q] > kNegInf)
-      sh.hits[atomicAdd(&sh.nhits, 1)] = (uint16_t)(tid + kThreads * q);
-  collect(ev, ei);
-  __syncthreads();
-  {
-    const int per = (iters + kParts - 1) / kParts, total = sh.nhits * per;
-    for (int e0 = tid; e0 < total; e0 += kThreads) {
-      const int hit = sh.hits[e0 / per];
-      const int v = (hit & (kThreads - 1)) + (hit / kThreads + kParts * (e0 % per)) * kThreads;
-      if (v < row.nv) {
-        const u32x4 r = row.raw(v);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) collect(row.part(r, e), row.head + v * kE + e);
+        sort_candidates(n);
+        weigh(n, top, inv_t);
+        const int kk = min(k, n);
+        int keep = kk;
+        if (p < 1.0) keep = min(count_below(kk, p * sh.cum[kk - 1], false) + 1, kk);
+        if (minp > 0.0) keep = min(keep, count_heavy(n, minp, top, inv_t));
+        keep = max(keep, 1);
+        const double zn = sh.cum[keep - 1];
+        const int j = count_below(keep, u * zn, true);
+        r = Answer{sh.cand[min(j, keep - 1)], zn, true};
       }
     }
   }
-  __syncthreads();
-  if (greedy) {
-    if (tid == 0) {
-      a.tokens[b] = sh.best;
-      if (a.logprob) a.logprob[b] = 0.0f;
+  const Filters f = {greedy ? 1 : k, vocab, greedy ? 2.0 : p, greedy ? 0.0 : minp, u, inv_t};
+  if (!r.found && vocab <= kMaxBinVocab && top < __builtin_inff()) {
+    if (!bins_ready || __builtin_fma(-(double)top, bins.scale, bins.offset) < 25165824.0) {
+      // too many tokens for the first way, or bins that began too low: tally from the top
+      __syncthreads();
+      for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = 0;
+      beyond = 0;
+      __syncthreads();
+      bins_ready = bins.begin_at((double)top);
+      if (bins_ready) read_batches<F32>(row, tally_batch, [&](float l, int) { if (l > kNegInf) tally_one(l); });
     }
-    return;
+    if (beyond) atomicAdd(&sh.bins[kBins - 1], (unsigned long long)beyond << bins.low);
+    __syncthreads();
+    if (bins_ready) r = by_bins<F32>(row, f, top, bins, part, ev, ei);
   }
-  auto answer = [&](uint64_t token, double kept) {
-    if (tid == 0) {
-      a.tokens[b] = (int)(0xFFFFFFFFu - (unsigned)token);
-      if (a.logprob)
-        a.logprob[b] = (float)(log_weight(from_key((unsigned)(token >> 32)), top, inv_t) - log(kept));
-    }
-  };
-  const int n = sh.count;
-  if (n <= kCap) {
-    sort_candidates(sh, n);
-    double w[kPer], c[kPer];
-    weigh(sh, n, top, inv_t, w, c);
-    // everything collected, or the tokens beyond weigh nothing (they are masked)?
-    const bool complete = tau == kNegInf;
-    const int full = complete ? n : vocab;      // tokens of the order that count
-    const int kk = min(k, full);
-    // shortest of the prefixes; one that ends beyond the collected tokens only counts as "beyond"
-    bool ok = true;
-    int keep = kk;
-    if (p < 1.0) {
-      // the weight of the first k: collected, or the row's when k is off
-      ok = kk <= n || k == vocab;
-      const double t = p * (kk <= n ? sh.cum[kk - 1] : z);
-      const int lim = min(kk, n);
-      const int np = count_tokens(sh, 0, lim, [&](int i) { return c[i] < t; });
-      keep = np < lim ? np + 1 : (kk <= n ? kk : INT_MAX);
-    }
-    if (minp > 0.0) {
-      const int nm = count_tokens(sh, 0, n, [&](int i) { return w[i] >= minp; });
-      if (nm < n || complete || all_min_p) keep = min(keep, nm);
-      else if (keep > n) keep = INT_MAX;
-    }
-    keep = max(keep, 1);
-    if (keep > n && (keep != vocab || p < 1.0 || minp > 0.0)) ok = false;
-    if (ok) {
-      const double zn = keep <= n ? sh.cum[keep - 1] : z;
-      const double t = u * zn;
-      const int lim = min(keep, n);
-      const int j = count_tokens(sh, 0, lim, [&](int i) { return c[i] <= t; });
-      if (j < lim || keep <= n) {
-        answer(sh.cand[min(j, keep - 1)], zn);
-        return;
-      }
-    }
+  if (!r.found) r = by_bisection<F32>(row, f, top);
+  if (tid == 0) {
+    a.tokens[b] = (int)(0xFFFFFFFFu - (unsigned)r.token);
+    if (a.logprob)
+      a.logprob[b] = greedy ? 0.0f : (float)(log_weight(logit_of(r.token), top, inv_t) - log(r.kept));
   }
-  {
-    const Filters f = {k, vocab, p, minp, u, inv_t};
-    uint64_t token;
-    double kept;
-    if (by_bins<F32>(sh, row, f, top, &token, &kept)) {
-      answer(token, kept);
-      return;
-    }
-  }
-
-  // ---- outside the collected tokens: borders by bisection over the whole row
-  uint64_t border = 0;
-  if (k < vocab)
-    border = bisect<F32>(sh, row, top, inv_t, [&](int c, double) { return c >= k; });
-  if (p < 1.0) {
-    int c;
-    double zk;
-    above<F32>(sh, row, border, top, inv_t, &c, &zk);
-    const uint64_t bp = bisect<F32>(sh, row, top, inv_t, [&](int, double s) { return s >= p * zk; });
-    border = max(border, bp);
-  }
-  if (minp > 0.0) {
-    unsigned lo = 0, hi = to_key(top);  // the smallest key with w >= min_p
-    while (lo < hi) {
-      const unsigned mid = lo + (hi - lo) / 2;
-      if (weight(clean(from_key(mid)), top, inv_t) >= minp) hi = mid;
-      else lo = mid + 1;
-    }
-    border = max(border, (uint64_t)lo << 32);
-  }
-  int c;
-  double zn;
-  above<F32>(sh, row, border, top, inv_t, &c, &zn);
-  uint64_t hit = bisect<F32>(sh, row, top, inv_t, [&](int, double s) { return s > u * zn; });
-  if (hit < border || hit == 0) {
-    // u * zn rounded up to zn: the last token kept that weighs something
-    hit = bisect<F32>(sh, row, top, inv_t, [&](int, double s) { return s >= zn; });
-  }
-  answer(hit, zn);
 }
 
 }  // namespace
