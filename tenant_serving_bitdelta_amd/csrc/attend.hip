@@ -144,9 +144,19 @@ __device__ __forceinline__ int clamp_len(int len, int width, int page_size) {
 // Does the token at position pos see key vp of its list?  In vp, the list's second part ends at
 // pos + (na - lo) for this token and begins a window before; the first tokens are the vp below
 // min(sinks, pos + 1) (when lo < sinks the list has no gap, else the token sees all na of them).
-// Written without branches: one compare per bound.
+// Sight holds both relative to a vp, so that a tile's keys are constants beyond it: one subtraction
+// and one comparison per bound, no branches.
+struct Sight {
+  int end, first;
+  __device__ __forceinline__ bool sees(int k, int window) const {
+    return ((unsigned)(end - k) < (unsigned)window) | (k < first);
+  }
+};
+__device__ __forceinline__ Sight sight(const KeyList& l, int pos, int sinks, int vp) {
+  return Sight{pos + (l.na - l.lo) - vp, min(sinks, pos + 1) - vp};
+}
 __device__ __forceinline__ bool sees(const KeyList& l, int pos, int window, int sinks, int vp) {
-  return ((unsigned)(pos + (l.na - l.lo) - vp) < (unsigned)window) | (vp < min(sinks, pos + 1));
+  return sight(l, pos, sinks, vp).sees(0, window);
 }
 
 // What one unit (sequence, kv head) of the row kernel reads and for which query rows.
@@ -436,20 +446,23 @@ void attend_row_kernel(const AttendArgs a) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         if (valid != 0xFFFFFFFFu || MULTI) {
+          const unsigned mine = valid >> (4 * g);
+          const Sight at = sight(kl, w.pos[c], a.sinks, base + 4 * g);
 #pragma unroll
           for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int key = 16 * r + 4 * g + i;
-              bool seen = (valid >> key) & 1u;
-              if constexpr (MULTI) seen = seen & sees(kl, w.pos[c], a.window, a.sinks, base + key);
+              const int key = 16 * r + i;  // + 4 g
+              bool seen = (mine >> key) & 1u;
+              if constexpr (MULTI) seen = seen & at.sees(key, a.window);
               const float v = s[c][r][i];
               s[c][r][i] = seen ? v : kNegInf;
             }
         }
         float t = kNegInf;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t = fmaxf(t, fmaxf(s[c][0][i], s[c][1][i]));
+        for (int i = 0; i < 4; ++i)
+          t = __builtin_elementwise_maximum(t, __builtin_elementwise_maximum((float)s[c][0][i], (float)s[c][1][i]));
         t = half_max(row_max(t)) * a.c;
         if (__any(t > w.m[c] + kRescale)) {
           const float mn = fmaxf(w.m[c], t);
@@ -573,8 +586,11 @@ void attend_row_kernel(const AttendArgs a) {
 
 // ---------------------------------------------------------------------------------------------
 // Tile kernel: 256 query rows (tokens x the heads of one kv head) against a key list in 64-key
-// steps.  8 waves of 32 rows; K and V tiles in LDS, two of each: while a step is worked on the
-// next one's rows are in registers, on their way to the other buffers.
+// steps.  8 waves of 32 rows; K and V tiles in LDS: while a step is worked on the next one's rows
+// are in registers, on their way to the other buffers.  A SIMD holds waves w and w + 4.  The second
+// of them is late by a third of a step: it multiplies a step's weights with the values at the
+// beginning of the next one, so that one wave's matrix instructions run beside the other's softmax
+// (three V tiles, since the late product still reads the last step's).
 // ---------------------------------------------------------------------------------------------
 template <int D, bool FP8>
 struct TileStage {
@@ -681,7 +697,8 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
   constexpr int kTile = kTileKeys * D * 2;
   constexpr int kSteps = D / 16;   // matrix steps over D of a score tile
   constexpr int kOut = D / 32;     // 32-row tiles of O^T
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // K, V; K, V
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // 2 K tiles, 3 V tiles
+  unsigned char* const vbuf = smem + 2 * kTile;
   __shared__ int state[2][kTileKeys];
   __shared__ int scan[kAttendMaxSeqs + 1];
   __shared__ int wave_sum[8];
@@ -690,6 +707,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane & 31, hf = lane >> 5;
   const int tpt = kTileRows / a.group;  // tokens per tile
+  const bool late = wave >= 4;
 
   // ---- work: prefix: a share of all (segment, row tile, kv head) units' steps; window: one unit
   int64_t x = 0, x_end = 1, total = 1;
@@ -793,16 +811,33 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       const int f = key_position(kl, base), last = key_position(kl, base + kTileKeys - 1);
       return base < kl.na || last > p0 || p0 + nt - 1 - f >= a.window;
     };
-    st.store(smem, smem + kTile, state[0], hides(s_begin * kTileKeys), tid);
+    st.store(smem, vbuf, state[0], hides(s_begin * kTileKeys), tid);
     st.fetch(a, h, tid);
     st.lookup(a, kl, (s_begin + 2) * kTileKeys, tid);
     __syncthreads();
 
+    // O^T += V^T P^T of step s: of 16 keys the lane's 8 are 4 hf .. + 3 and 8 + 4 hf .. + 3
+    u32x4 p[4];
+    const int l16 = lane & 15;
+    const int v_row = 4 * hf + (l16 >> 2), v_un = 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1);
+    const int v_b = 8 * (l16 & 1);
+    auto add_values = [&](int s) {
+      const unsigned char* vt = vbuf + (s - s_begin) % 3 * kTile;
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) {
+          const u32x2 lo = lds_read_tr(vt + v_unit<D>(16 * kb + v_row, 4 * i + v_un) + v_b);
+          const u32x2 hi = lds_read_tr(vt + v_unit<D>(16 * kb + 8 + v_row, 4 * i + v_un) + v_b);
+          o[i] = mfma32(u32x4{lo[0], lo[1], hi[0], hi[1]}, p[kb], o[i]);
+        }
+    };
+    bool pending = false;  // the last step's weights wait in p
     for (int s = s_begin; s < s_end; ++s) {
       const int buf = (s - s_begin) & 1;
-      const unsigned char* kt = smem + buf * 2 * kTile;
-      const unsigned char* vt = kt + kTile;
+      const unsigned char* kt = smem + buf * kTile;
       const int base = s * kTileKeys;
+      if (late && pending) add_values(s - 1);
       const int key_state = state[buf][lane];
       const uint64_t valid = __ballot(key_state & 1);
       // does the wave see anything, does every row see everything?
@@ -816,41 +851,49 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       f32x16 sc[2];
       if (any) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e) sc[i][e] = 0.f;
 #pragma unroll
-          for (int d = 0; d < kSteps; ++d) {
+        for (int d = 0; d < kSteps; ++d)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
             const u32x4 kf = *reinterpret_cast<const u32x4*>(kt + k_unit<D>(32 * i + q, 2 * d + hf));
             sc[i] = mfma32(kf, qf[d], sc[i]);
           }
-        }
       }
-      // ---- the next step's tiles; the buffers were last read before the barrier that began this
+      // ---- the next step's tiles; these buffers were last read before the barrier that began this
       // step
       if (s + 1 < s_end) {
-        unsigned char* kn = smem + (buf ^ 1) * 2 * kTile;
-        st.store(kn, kn + kTile, state[buf ^ 1], hides(base + kTileKeys), tid);
+        st.store(smem + (buf ^ 1) * kTile, vbuf + (s + 1 - s_begin) % 3 * kTile, state[buf ^ 1],
+                 hides(base + kTileKeys), tid);
         st.fetch(a, h, tid);
         st.lookup(a, kl, base + 3 * kTileKeys, tid);
       }
+      pending = any;
       if (any) {
         // lane (q, hf) holds keys 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
         if (!all) {
+          const uint64_t mine = valid >> (4 * hf);
+          const Sight at = sight(kl, pq, a.sinks, base + 4 * hf);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i) {
+            const unsigned bits = (unsigned)(mine >> (32 * i));
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int key = 32 * i + 8 * (e >> 2) + 4 * hf + (e & 3);
-              bool seen = (valid >> key) & 1ull;
-              if constexpr (!PREFIX) seen = seen & sees(kl, pq, a.window, a.sinks, base + key);
+              const int key = 8 * (e >> 2) + (e & 3);  // + 32 i + 4 hf
+              bool seen = (bits >> key) & 1u;
+              if constexpr (!PREFIX) seen = seen & at.sees(32 * i + key, a.window);
               const float v = sc[i][e];
               sc[i][e] = seen ? v : kNegInf;
             }
+          }
         }
+        // (elementwise maximum: a NaN among a row's scores passes, the row is NaN then)
         float tm = kNegInf;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) tm = fmaxf(tm, fmaxf(sc[0][e], sc[1][e]));
+        for (int e = 0; e < 16; ++e)
+          tm = __builtin_elementwise_maximum(tm, __builtin_elementwise_maximum((float)sc[0][e], (float)sc[1][e]));
         tm = half_max(tm) * a.c;
         if (__any(tm > m + kRescale)) {
           const float mn = fmaxf(m, tm);
@@ -861,7 +904,6 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
           for (int i = 0; i < kOut; ++i) o[i] *= f;
         }
         const float mb = m == kNegInf ? 0.f : m;
-        u32x4 p[4];
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
           float e[8];
@@ -875,18 +917,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
           p[kb] = u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
                         pack_bf16(e[6], e[7])};
         }
-        // ---- O^T += V^T P^T: of 16 keys the lane's 8 are 4 hf .. + 3 and 8 + 4 hf .. + 3
-        const int l16 = lane & 15;
-        const int vr = 4 * hf + (l16 >> 2), vu = 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1);
-        const int vb = 8 * (l16 & 1);
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb)
-#pragma unroll
-          for (int i = 0; i < kOut; ++i) {
-            const u32x2 lo = lds_read_tr(vt + v_unit<D>(16 * kb + vr, 4 * i + vu) + vb);
-            const u32x2 hi = lds_read_tr(vt + v_unit<D>(16 * kb + 8 + vr, 4 * i + vu) + vb);
-            o[i] = mfma32(u32x4{lo[0], lo[1], hi[0], hi[1]}, p[kb], o[i]);
-          }
+        if (!late) add_values(s);
         if constexpr (!PREFIX) {
           if (!all) {
             for (uint64_t odd = __ballot(key_state & 2); odd; odd &= odd - 1) {
@@ -907,6 +938,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       }
       __syncthreads();
     }
+    if (late && pending) add_values(s_end - 1);
 
     // ---- epilogue: lane (q, hf) holds dims 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
     l = half_sum(l);
@@ -1069,7 +1101,7 @@ hipError_t rows_for(const AttendArgs& a, int columns, int blocks, hipStream_t st
 
 template <int D, bool FP8, bool PREFIX>
 hipError_t tiles_for(const AttendArgs& a, int blocks, hipStream_t stream) {
-  constexpr int lds = 4 * kTileKeys * D * 2;
+  constexpr int lds = 5 * kTileKeys * D * 2;
   static DeviceOnce once;
   const hipError_t e = set_dynamic_lds_once(
       once, reinterpret_cast<const void*>(&attend_tile_kernel<D, FP8, PREFIX>), lds);
