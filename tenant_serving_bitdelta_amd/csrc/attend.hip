@@ -587,11 +587,32 @@ void attend_row_kernel(const AttendArgs a) {
 // ---------------------------------------------------------------------------------------------
 // Tile kernel: 256 query rows (tokens x the heads of one kv head) against a key list in 64-key
 // steps.  8 waves of 32 rows; K and V tiles in LDS: while a step is worked on the next one's rows
-// are in registers, on their way to the other buffers.  A SIMD holds waves w and w + 4.  The second
-// of them is late by a third of a step: it multiplies a step's weights with the values at the
-// beginning of the next one, so that one wave's matrix instructions run beside the other's softmax
-// (three V tiles, since the late product still reads the last step's).
+// are in registers, on their way to the other buffers.  (Letting the second wave of each SIMD run a
+// third of a step late, its product with the values put off to the next step, measured 4% slower.)
 // ---------------------------------------------------------------------------------------------
+// Byte offsets of a key's rows; bit 0 of k: there is no such key (offsets 0).
+struct RowPlace {
+  int64_t k, v;
+};
+// Where the lane's key of a step sits: its table entry, loaded a step before the rows' offsets are
+// worked out from it.
+struct KeyLookup {
+  int id, slot;
+  __device__ __forceinline__ void begin(const PagedCache& c, const KeyList& kl, int vp) {
+    const int kp = key_position(kl, vp);
+    const int page = page_quotient(kp < 0 ? 0 : kp, c.div);
+    const int at = key_table_index(kl, vp, page);
+    slot = kp - page * c.page_size;
+    id = at >= 0 ? (vp < kl.na ? kl.ta : kl.tb)[at] : -1;
+  }
+  __device__ __forceinline__ RowPlace end(const PagedCache& c) const {
+    const bool ok = page_id_checked(id, c.num_pages) >= 0;
+    const int p = ok ? id : 0, t = ok ? slot : 0;
+    return RowPlace{page_row_bytes(p, t, c.k_page, c.k_token) | (ok ? 0 : 1),
+                    page_row_bytes(p, t, c.v_page, c.v_token)};
+  }
+};
+
 template <int D, bool FP8>
 struct TileStage {
   static constexpr int kUnits = FP8 ? D / 16 : D / 8;      // 16-byte units of a row in memory
@@ -601,39 +622,24 @@ struct TileStage {
   static constexpr int kRowStride = 512 / kUnits;          // rows between a thread's rows
 
   u32x4 r[kPer];
-  int id[kRows], slot[kRows];
   bool ok[kRows];
 
   __device__ __forceinline__ int row(int tid, int i) const {
     return (tid / kUnits + i * kRowStride) & (kTileKeys - 1);
   }
-  __device__ __forceinline__ void lookup(const AttendArgs& a, const KeyList& kl, int base, int tid) {
+  // k, v: this thread's unit of the head's first row; places: RowPlace of each of the step's keys
+  __device__ __forceinline__ void fetch(const unsigned char* k, const unsigned char* v,
+                                        const RowPlace* places, int tid) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int p = base + row(tid, i);
-      const int kp = key_position(kl, p);
-      const int page = page_quotient(kp < 0 ? 0 : kp, a.cache.div);
-      const int at = key_table_index(kl, p, page);
-      slot[i] = kp - page * a.cache.page_size;
-      id[i] = at >= 0 ? (p < kl.na ? kl.ta : kl.tb)[at] : -1;  // checked when it is used
-    }
-  }
-  __device__ __forceinline__ void fetch(const AttendArgs& a, int h, int tid) {
-    const int u = tid % kUnits;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+      const RowPlace at = places[row(tid, i)];
       // absent keys read page 0 and are cleared before they are stored
-      ok[i] = page_id_checked(id[i], a.cache.num_pages) >= 0;
-      const int page = ok[i] ? id[i] : 0, at = ok[i] ? slot[i] : 0;
-      const unsigned char* kp = a.cache.k + page_row_bytes(page, at, a.cache.k_page, a.cache.k_token) +
-                                (int64_t)h * a.cache.k_head + 16 * u;
-      const unsigned char* vp = a.cache.v + page_row_bytes(page, at, a.cache.v_page, a.cache.v_token) +
-                                (int64_t)h * a.cache.v_head + 16 * u;
+      ok[i] = (at.k & 1) == 0;
       if constexpr (kKV == 2) {
-        r[i] = *reinterpret_cast<const u32x4*>(kp);
-        r[kRows + i] = *reinterpret_cast<const u32x4*>(vp);
+        r[i] = *reinterpret_cast<const u32x4*>(k + (at.k & ~15ll));
+        r[kRows + i] = *reinterpret_cast<const u32x4*>(v + at.v);
       } else {
-        r[i] = *reinterpret_cast<const u32x4*>(tid < 256 ? kp : vp);
+        r[i] = *reinterpret_cast<const u32x4*>(tid < 256 ? k + (at.k & ~15ll) : v + at.v);
       }
     }
   }
@@ -697,9 +703,10 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
   constexpr int kTile = kTileKeys * D * 2;
   constexpr int kSteps = D / 16;   // matrix steps over D of a score tile
   constexpr int kOut = D / 32;     // 32-row tiles of O^T
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // 2 K tiles, 3 V tiles
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // 2 K tiles, 2 V tiles
   unsigned char* const vbuf = smem + 2 * kTile;
   __shared__ int state[2][kTileKeys];
+  __shared__ RowPlace places[2][kTileKeys];
   __shared__ int scan[kAttendMaxSeqs + 1];
   __shared__ int wave_sum[8];
 
@@ -707,7 +714,6 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane & 31, hf = lane >> 5;
   const int tpt = kTileRows / a.group;  // tokens per tile
-  const bool late = wave >= 4;
 
   // ---- work: prefix: a share of all (segment, row tile, kv head) units' steps; window: one unit
   int64_t x = 0, x_end = 1, total = 1;
@@ -800,20 +806,38 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
     float m = kNegInf, l = 0.f;
 
+    // The pipeline: the keys of step t are looked up by one wave (wave t mod 8, one lane a key): table
+    // entries loaded in step t - 4, rows' offsets written to LDS in step t - 3; all threads load the
+    // rows in step t - 2 and write them to LDS in step t - 1.
     TileStage<D, FP8> st;
-    st.lookup(a, kl, s_begin * kTileKeys, tid);
-    st.fetch(a, h, tid);
-    st.lookup(a, kl, (s_begin + 1) * kTileKeys, tid);
-    __syncthreads();  // the last unit's tiles are no longer read
+    KeyLookup look;
+    const int my_unit = 16 * (tid % TileStage<D, FP8>::kUnits);
+    const unsigned char* const kh = a.cache.k + (int64_t)h * a.cache.k_head + my_unit;
+    const unsigned char* const vh = a.cache.v + (int64_t)h * a.cache.v_head + my_unit;
+    auto look_begin = [&](int s) {
+      if (((s - s_begin) & 7) == wave) look.begin(a.cache, kl, s * kTileKeys + lane);
+    };
+    auto look_end = [&](int s) {
+      if (((s - s_begin) & 7) == wave) places[(s - s_begin) & 1][lane] = look.end(a.cache);
+    };
     // edge step: some row of the tile does not see some key of it (the same for all waves)
     auto hides = [&](int base) {
       if constexpr (PREFIX) return false;
       const int f = key_position(kl, base), last = key_position(kl, base + kTileKeys - 1);
       return base < kl.na || last > p0 || p0 + nt - 1 - f >= a.window;
     };
+    look_begin(s_begin);
+    look_begin(s_begin + 1);
+    look_begin(s_begin + 2);
+    look_begin(s_begin + 3);
+    look_end(s_begin);
+    look_end(s_begin + 1);
+    __syncthreads();  // (also: the last unit's tiles are no longer read)
+    st.fetch(kh, vh, places[0], tid);
     st.store(smem, vbuf, state[0], hides(s_begin * kTileKeys), tid);
-    st.fetch(a, h, tid);
-    st.lookup(a, kl, (s_begin + 2) * kTileKeys, tid);
+    st.fetch(kh, vh, places[1], tid);
+    __syncthreads();
+    look_end(s_begin + 2);
     __syncthreads();
 
     // O^T += V^T P^T of step s: of 16 keys the lane's 8 are 4 hf .. + 3 and 8 + 4 hf .. + 3
@@ -821,8 +845,8 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
     const int l16 = lane & 15;
     const int v_row = 4 * hf + (l16 >> 2), v_un = 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1);
     const int v_b = 8 * (l16 & 1);
-    auto add_values = [&](int s) {
-      const unsigned char* vt = vbuf + (s - s_begin) % 3 * kTile;
+    auto add_values = [&](int buf) {
+      const unsigned char* vt = vbuf + buf * kTile;
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
@@ -832,12 +856,10 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
           o[i] = mfma32(u32x4{lo[0], lo[1], hi[0], hi[1]}, p[kb], o[i]);
         }
     };
-    bool pending = false;  // the last step's weights wait in p
     for (int s = s_begin; s < s_end; ++s) {
       const int buf = (s - s_begin) & 1;
       const unsigned char* kt = smem + buf * kTile;
       const int base = s * kTileKeys;
-      if (late && pending) add_values(s - 1);
       const int key_state = state[buf][lane];
       const uint64_t valid = __ballot(key_state & 1);
       // does the wave see anything, does every row see everything?
@@ -854,23 +876,41 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e) sc[i][e] = 0.f;
+        // kDeep pairs of operand reads in flight ahead of the matrix instructions (left to itself
+        // the compiler sinks each read to its use)
+        constexpr int kDeep = kSteps < 4 ? kSteps : 4;
+        u32x4 kf[kDeep][2];
+        auto read_k = [&](int d) {
 #pragma unroll
-        for (int d = 0; d < kSteps; ++d)
+          for (int i = 0; i < 2; ++i)
+            kf[d % kDeep][i] = *reinterpret_cast<const u32x4*>(kt + k_unit<D>(32 * i + q, 2 * d + hf));
+        };
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const u32x4 kf = *reinterpret_cast<const u32x4*>(kt + k_unit<D>(32 * i + q, 2 * d + hf));
-            sc[i] = mfma32(kf, qf[d], sc[i]);
-          }
+        for (int d = 0; d < kDeep; ++d) read_k(d);
+#pragma unroll
+        for (int d = 0; d < kSteps; ++d) {
+          const u32x4 k0 = kf[d % kDeep][0], k1 = kf[d % kDeep][1];
+          if (d + kDeep < kSteps) read_k(d + kDeep);
+          sc[0] = mfma32(k0, qf[d], sc[0]);
+          sc[1] = mfma32(k1, qf[d], sc[1]);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * kDeep, 0);
+#pragma unroll
+        for (int d = 0; d < kSteps - kDeep; ++d) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 2 * kDeep, 0);
       }
       // ---- the next step's tiles; these buffers were last read before the barrier that began this
       // step
       if (s + 1 < s_end) {
-        st.store(smem + (buf ^ 1) * kTile, vbuf + (s + 1 - s_begin) % 3 * kTile, state[buf ^ 1],
+        st.store(smem + (buf ^ 1) * kTile, vbuf + (buf ^ 1) * kTile, state[buf ^ 1],
                  hides(base + kTileKeys), tid);
-        st.fetch(a, h, tid);
-        st.lookup(a, kl, base + 3 * kTileKeys, tid);
+        st.fetch(kh, vh, places[buf], tid);
+        look_end(s + 3);
+        look_begin(s + 4);
       }
-      pending = any;
       if (any) {
         // lane (q, hf) holds keys 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
         if (!all) {
@@ -917,7 +957,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
           p[kb] = u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
                         pack_bf16(e[6], e[7])};
         }
-        if (!late) add_values(s);
+        add_values(buf);
         if constexpr (!PREFIX) {
           if (!all) {
             for (uint64_t odd = __ballot(key_state & 2); odd; odd &= odd - 1) {
@@ -938,7 +978,6 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       }
       __syncthreads();
     }
-    if (late && pending) add_values(s_end - 1);
 
     // ---- epilogue: lane (q, hf) holds dims 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
     l = half_sum(l);
@@ -1101,7 +1140,7 @@ hipError_t rows_for(const AttendArgs& a, int columns, int blocks, hipStream_t st
 
 template <int D, bool FP8, bool PREFIX>
 hipError_t tiles_for(const AttendArgs& a, int blocks, hipStream_t stream) {
-  constexpr int lds = 5 * kTileKeys * D * 2;
+  constexpr int lds = 4 * kTileKeys * D * 2;
   static DeviceOnce once;
   const hipError_t e = set_dynamic_lds_once(
       once, reinterpret_cast<const void*>(&attend_tile_kernel<D, FP8, PREFIX>), lds);
