@@ -179,11 +179,11 @@ def _lib():
         L.bitdelta_attend_shared.restype = ctypes.c_int
         L.bitdelta_attend_shared.argtypes = [rows_p, cache_p, ctypes.c_void_p, ctypes.c_int32,
                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
-                                             ctypes.c_void_p, _i32p, ctypes.c_int32,
+                                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                              ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
         L.bitdelta_attend_shared_workspace_bytes.restype = ctypes.c_size_t
         L.bitdelta_attend_shared_workspace_bytes.argtypes = [
-            ctypes.c_int64, ctypes.c_int32, cache_p, ctypes.c_int32, ctypes.c_int32, _i32p,
+            ctypes.c_int64, ctypes.c_int32, cache_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
             ctypes.c_int32]
         L.bitdelta_attend_window.restype = ctypes.c_int
         L.bitdelta_attend_window.argtypes = [rows_p, cache_p, ctypes.c_int32, ctypes.c_void_p,
@@ -219,6 +219,14 @@ def _stream(stream):
         return ctypes.c_void_p(int(stream))
     import torch
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _raw_stream(stream, tensor):
+    """The call's stream handle: ``stream``, or torch's current one on the tensor's device."""
+    if stream is not None:
+        return int(stream)
+    import torch
+    return torch._C._cuda_getCurrentRawStream(tensor.device.index)
 
 
 def _temp(nbytes, device, stream, dtype_name="uint8"):
@@ -655,31 +663,31 @@ def upload_variant(host_words, host_alpha, d_out: int, d_in: int, words=None, ti
 # Attention over a paged cache
 # ---------------------------------------------------------------------------------------------
 
+_KV_DTYPES = {}  # torch dtype -> bitdelta_kv_dtype
+
+
 def _kv_cache(k_pages, v_pages, k_scale, v_scale):
     """bitdelta_kv_cache of two [pages, page_size, kv_heads, head_dim] tensors (bf16 or
     float8_e4m3fn), any strides but contiguous rows."""
     import torch
-    dtypes = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+    if not _KV_DTYPES:
+        _KV_DTYPES.update({torch.bfloat16: 0, torch.float8_e4m3fn: 1})
     for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{what} must be a CUDA/HIP torch tensor")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{what} must be torch.bfloat16 or torch.float8_e4m3fn, got {t.dtype}")
-        if t.dim() != 4:
-            raise ValueError(f"{what} must be [pages, page_size, kv_heads, head_dim]")
-        if t.shape[3] > 1 and t.stride(3) != 1:
-            raise ValueError(f"{what} must have contiguous rows")
-    if k_pages.dtype != v_pages.dtype or k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages must have one shape and type")
-    if k_pages.device != v_pages.device:
-        raise ValueError("k_pages and v_pages must be on one device")
-    c = _KvCache()
-    c.k, c.v, c.dtype = k_pages.data_ptr(), v_pages.data_ptr(), dtypes[k_pages.dtype]
-    c.num_pages, c.page_size, c.kv_heads, c.head_dim = (int(n) for n in k_pages.shape)
-    c.k_stride_page, c.k_stride_token, c.k_stride_head = k_pages.stride()[:3]
-    c.v_stride_page, c.v_stride_token, c.v_stride_head = v_pages.stride()[:3]
-    c.k_scale, c.v_scale = float(k_scale), float(v_scale)
-    return c
+    shape, dtype = k_pages.shape, k_pages.dtype
+    code = _KV_DTYPES.get(dtype)
+    if code is None or v_pages.dtype is not dtype:
+        raise TypeError("k_pages and v_pages must both be torch.bfloat16 or torch.float8_e4m3fn, "
+                        f"got {dtype} and {v_pages.dtype}")
+    if len(shape) != 4 or v_pages.shape != shape:
+        raise ValueError("k_pages and v_pages must be [pages, page_size, kv_heads, head_dim], "
+                         "of one shape")
+    ks, vs = k_pages.stride(), v_pages.stride()
+    if shape[3] > 1 and (ks[3] != 1 or vs[3] != 1):
+        raise ValueError("k_pages and v_pages must have contiguous rows")
+    return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), code, shape[0], shape[1], shape[2],
+                    shape[3], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], k_scale, v_scale)
 
 
 def _attend_rows(q, cache, out, lse, return_lse, scale, stream):
@@ -688,47 +696,55 @@ def _attend_rows(q, cache, out, lse, return_lse, scale, stream):
     import torch
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise TypeError("q must be a CUDA/HIP torch tensor")
-    if q.dtype != torch.bfloat16:
+    if q.dtype is not torch.bfloat16:
         raise TypeError(f"q must be torch.bfloat16, got {q.dtype}")
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
-        raise ValueError(f"q must be [tokens, heads, {cache.head_dim}], not {tuple(q.shape)}")
-    if q.stride(2) != 1:
-        raise ValueError("q must have contiguous rows")
+    shape, dim = q.shape, cache.head_dim
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError(f"q must be [tokens, heads, {dim}], not {tuple(shape)}")
+    qs = q.stride()
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        _on_stream(out, stream)
-    if not out.is_cuda or out.dtype != torch.bfloat16:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        if stream is not None:
+            _on_stream(out, stream)
+    elif not out.is_cuda or out.dtype is not torch.bfloat16:
         raise TypeError("out must be a torch.bfloat16 CUDA/HIP tensor")
-    _check_shape(out, q.shape, "out")
-    if out.stride(2) != 1:
-        raise ValueError("out must have contiguous rows")
-    if lse is None and return_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        _on_stream(lse, stream)
-    r = _AttendRows()
-    r.q, r.out = q.data_ptr(), out.data_ptr()
+    elif out.shape != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, needs {tuple(shape)}")
+    os_ = out.stride()
+    if qs[2] != 1 or os_[2] != 1:
+        raise ValueError("q and out must have contiguous rows")
+    lptr = None
     if lse is not None:
-        _check_shape(lse, q.shape[:2], "lse")
-        r.lse = _dev(lse, "torch.float32", "lse")
-    r.tokens, r.heads = int(q.shape[0]), int(q.shape[1])
-    r.q_stride_token, r.q_stride_head = q.stride()[:2]
-    r.out_stride_token, r.out_stride_head = out.stride()[:2]
-    r.scale = float(cache.head_dim ** -0.5 if scale is None else scale)
-    return r, out, lse
+        _check_shape(lse, shape[:2], "lse")
+        lptr = _dev(lse, "torch.float32", "lse")
+    elif return_lse:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+        if stream is not None:
+            _on_stream(lse, stream)
+        lptr = lse.data_ptr()
+    return _AttendRows(q.data_ptr(), out.data_ptr(), lptr, shape[0], shape[1], qs[0], qs[1], os_[0],
+                       os_[1], dim ** -0.5 if scale is None else scale), out, lse
 
 
 def _table(t, lens, n, what):
     """(pointer, width, lens pointer) of an int32 page table [n, width] and its lengths [n]."""
-    if t.dim() != 2 or t.shape[0] != n:
-        raise ValueError(f"{what} must be [{n}, pages], not {tuple(t.shape)}")
-    _check_shape(lens, (n,), f"{what}'s lengths")
-    return (_dev(t, "torch.int32", what), int(t.shape[1]),
-            _dev(lens, "torch.int32", f"{what}'s lengths"))
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != n:
+        raise ValueError(f"{what} must be [{n}, pages], not {tuple(shape)}")
+    if lens.dim() != 1 or lens.shape[0] != n:
+        raise ValueError(f"{what}'s lengths must be [{n}], not {tuple(lens.shape)}")
+    return _dev(t, "torch.int32", what), shape[1], _dev(lens, "torch.int32", what + "'s lengths")
+
+
+def _host_i32(a):
+    """(array, its address) of a host int32 array."""
+    arr = np.ascontiguousarray(a, dtype=np.int32)
+    return arr, arr.__array_interface__["data"][0]
 
 
 def attend_shared_workspace_bytes(k_pages, heads, table, prefix_table, seg_offsets) -> int:
     """Device workspace an attend_shared call with these tables needs (bytes, 0 if none)."""
-    offs, offs_p = _i32(seg_offsets)
+    offs, offs_p = _host_i32(seg_offsets)
     c = _kv_cache(k_pages, k_pages, 1.0, 1.0)
     pwidth = 0 if prefix_table is None else int(prefix_table.shape[1])
     return int(_lib().bitdelta_attend_shared_workspace_bytes(
@@ -751,7 +767,7 @@ def attend_shared(q, k_pages, v_pages, table, lens, prefix_table, prefix_lens, s
     prefixes), on the device.  Returns bf16 ``out`` like q, and with ``return_lse`` (or ``lse``
     given) also the natural log of each row's softmax sum, float32 [batch, heads].  A sequence
     with no keys gives zeros and -inf."""
-    offs, offs_p = _i32(seg_offsets)
+    offs, offs_p = _host_i32(seg_offsets)
     cache = _kv_cache(k_pages, v_pages, k_scale, v_scale)
     rows, out, lse = _attend_rows(q, cache, out, lse, return_lse, scale, stream)
     tptr, width, lptr = _table(table, lens, rows.tokens, "table")
@@ -764,7 +780,7 @@ def attend_shared(q, k_pages, v_pages, table, lens, prefix_table, prefix_lens, s
         # no prefixes: the batch is one segment without keys (its length pointer is never read
         # past a table of width 0, which holds none)
         pptr, pwidth, plptr = None, 0, lptr
-        offs, offs_p = _i32([0, rows.tokens])
+        offs, offs_p = _host_i32([0, rows.tokens])
         nseg = 1
     else:
         pptr, pwidth, plptr = _table(prefix_table, prefix_lens, nseg, "prefix_table")
@@ -773,7 +789,7 @@ def attend_shared(q, k_pages, v_pages, table, lens, prefix_table, prefix_lens, s
     ws_ptr, ws_bytes, ws = _workspace(workspace, need, q.device, stream)
     _check(_lib().bitdelta_attend_shared(
         ctypes.byref(rows), ctypes.byref(cache), tptr, width, lptr, pptr, pwidth, plptr, offs_p,
-        nseg, ws_ptr, ws_bytes, _stream(stream)), "bitdelta_attend_shared")
+        nseg, ws_ptr, ws_bytes, _raw_stream(stream, q)), "bitdelta_attend_shared")
     return out if lse is None else (out, lse)
 
 
@@ -798,7 +814,7 @@ def attend_window(q, k_pages, v_pages, table, lens, window, sinks=0, q_offsets=N
     ``max_q_len``.  Cache, tables, scales and results as for attend_shared."""
     cache = _kv_cache(k_pages, v_pages, k_scale, v_scale)
     rows, out, lse = _attend_rows(q, cache, out, lse, return_lse, scale, stream)
-    batch = int(lens.shape[0]) if lens.dim() == 1 else -1
+    batch = lens.shape[0] if lens.dim() == 1 else -1
     tptr, width, lptr = _table(table, lens, batch, "table")
     optr = None
     if q_offsets is not None:
@@ -809,7 +825,7 @@ def attend_window(q, k_pages, v_pages, table, lens, window, sinks=0, q_offsets=N
     ws_ptr, ws_bytes, ws = _workspace(workspace, need, q.device, stream)
     _check(_lib().bitdelta_attend_window(
         ctypes.byref(rows), ctypes.byref(cache), batch, tptr, width, lptr, optr, max_q_len, window,
-        sinks, ws_ptr, ws_bytes, _stream(stream)), "bitdelta_attend_window")
+        sinks, ws_ptr, ws_bytes, _raw_stream(stream, q)), "bitdelta_attend_window")
     return out if lse is None else (out, lse)
 
 
@@ -856,5 +872,5 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=
         arg(u, "torch.float32", "u"), arg(temperature, "torch.float32", "temperature"),
         arg(top_k, "torch.int32", "top_k"), arg(top_p, "torch.float32", "top_p"),
         arg(min_p, "torch.float32", "min_p"), arg(out, "torch.int32", "out"),
-        arg(logprob, "torch.float32", "logprob"), _stream(stream)), "bitdelta_sample")
+        arg(logprob, "torch.float32", "logprob"), _raw_stream(stream, logits)), "bitdelta_sample")
     return out if logprob is None else (out, logprob)

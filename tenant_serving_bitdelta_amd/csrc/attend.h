@@ -125,6 +125,8 @@ struct AttendArgs {
   int32_t* scan;                // [batch + 1] first step of each sequence, x kv_heads = of its units
   float* part_o;                // row partials [slot][rows][dim]
   float* part_ml;               // [slot][rows][2]: running maximum (log2 units) and sum
+  int32_t* tile_segs;           // [segments + 1] row tiles before each segment
+  int32_t* tile_scan;           // [segments + 1] steps before each segment, x kv_heads
   float* tile_o;                // tile partials [slot][kTileRows][dim]
   float* tile_ml;               // [slot][kTileRows][2]
   int32_t seg_offsets[kAttendMaxSegments + 1];

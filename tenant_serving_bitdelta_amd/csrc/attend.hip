@@ -304,7 +304,7 @@ struct RowLoop {
 
 // MULTI: units may hold several tokens, which see different keys
 template <int D, bool FP8, int NC, bool MULTI>
-__global__ __launch_bounds__(256, NC <= 2 ? 2 : 1)
+__global__ __launch_bounds__(256, NC == 1 && !MULTI && (FP8 || D == 64) ? 3 : (NC <= 2 ? 2 : 1))
 void attend_row_kernel(const AttendArgs a) {
   using Loop = RowLoop<D, FP8, NC>;
   constexpr int kWaveLds = kRowKeys * D * 2;
@@ -708,6 +708,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
   __shared__ int state[2][kTileKeys];
   __shared__ RowPlace places[2][kTileKeys];
   __shared__ int scan[kAttendMaxSeqs + 1];
+  __shared__ int segs[PREFIX ? kAttendMaxSegments + 1 : 1];
   __shared__ int wave_sum[8];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -721,11 +722,17 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
   if constexpr (PREFIX) {
     // workgroups go round robin over the 8 XCDs: give each XCD one run of the work, so that the
     // row tiles and heads that read the same pages share its L2
+    auto tiles_of = [&](int s) { return (a.seg_offsets[s + 1] - a.seg_offsets[s] + tpt - 1) / tpt; };
+    block_scan<512>(segs, wave_sum, a.nseg, tiles_of);
     block_scan<512>(scan, wave_sum, a.nseg, [&](int s) {
-      const int n = a.seg_offsets[s + 1] - a.seg_offsets[s];
       const int len = clamp_len(a.prefix_lens[s], a.pwidth, a.cache.page_size);
-      return (n + tpt - 1) / tpt * ((len + kTileKeys - 1) / kTileKeys);
+      return tiles_of(s) * ((len + kTileKeys - 1) / kTileKeys);
     });
+    if (blockIdx.x == 0)  // for the joining kernel
+      for (int i = tid; i <= a.nseg; i += 512) {
+        a.tile_segs[i] = segs[i];
+        a.tile_scan[i] = scan[i];
+      }
     total = (int64_t)scan[a.nseg] * a.kv_heads;
     const int workers = split_workers(total, a.tile_workers);
     const int per = (workers + 7) / 8;
@@ -758,9 +765,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       s_end = (int)(x_end - x < steps - s_begin ? s_begin + (x_end - x) : steps);
       t0 = n0 + rt * tpt;
       nt = n - rt * tpt < tpt ? n - rt * tpt : tpt;
-      int ub = 0;  // units before this segment
-      for (int i = 0; i < sg; ++i) ub += (a.seg_offsets[i + 1] - a.seg_offsets[i] + tpt - 1) / tpt;
-      slot = w_id + (int64_t)ub * a.kv_heads + h * tiles + rt;
+      slot = w_id + (int64_t)segs[sg] * a.kv_heads + h * tiles + rt;
       const int32_t* row = a.prefix_table + (int64_t)sg * a.pwidth;
       kl = KeyList{row, row, a.pwidth, a.pwidth, 0, 0, len};
     } else {
@@ -1022,15 +1027,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
 // ---------------------------------------------------------------------------------------------
 template <int D>
 __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a) {
-  __shared__ int pscan[kAttendMaxSegments + 1];
-  __shared__ int wave_sum[4];
   const int tpt = kTileRows / a.group;
-  if (a.nseg > 0 && !a.row_prefix)
-    block_scan<256>(pscan, wave_sum, a.nseg, [&](int s) {
-      const int n = a.seg_offsets[s + 1] - a.seg_offsets[s];
-      const int len = clamp_len(a.prefix_lens[s], a.pwidth, a.cache.page_size);
-      return (n + tpt - 1) / tpt * ((len + kTileKeys - 1) / kTileKeys);
-    });
   constexpr int kQ = D / 4, kWays = 64 / kQ;  // lanes of a row, pieces side by side
   const int lane = threadIdx.x & 63;
   const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -1075,20 +1072,17 @@ __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a)
   }
   // the prefix
   if (a.nseg > 0 && !a.row_prefix) {
-    int sg = 0, ub = 0;
-    while (sg + 1 < a.nseg && a.seg_offsets[sg + 1] <= b) {
-      ub += (a.seg_offsets[sg + 1] - a.seg_offsets[sg] + tpt - 1) / tpt;
-      ++sg;
-    }
+    // the sequence's segment: how many segments end at or before it (at most 64: the last does not)
+    const int sg = __popcll(__ballot(lane < a.nseg && a.seg_offsets[lane + 1] <= b));
     const int n0 = a.seg_offsets[sg];
-    const int tiles = (a.seg_offsets[sg + 1] - n0 + tpt - 1) / tpt;
-    const int seg_steps = pscan[sg + 1] - pscan[sg];
+    const int ub = a.tile_segs[sg], tiles = a.tile_segs[sg + 1] - ub;
+    const int before = a.tile_scan[sg], seg_steps = a.tile_scan[sg + 1] - before;
     if (seg_steps > 0) {
-      const int64_t total = (int64_t)pscan[a.nseg] * a.kv_heads;
+      const int64_t total = (int64_t)a.tile_scan[a.nseg] * a.kv_heads;
       const int steps = seg_steps / tiles;
       const int rt = (b - n0) / tpt;
       const int row = (b - n0 - rt * tpt) * a.group + hh - h * a.group;
-      const int64_t x0 = (int64_t)pscan[sg] * a.kv_heads + ((int64_t)h * tiles + rt) * steps;
+      const int64_t x0 = (int64_t)before * a.kv_heads + ((int64_t)h * tiles + rt) * steps;
       const int workers = split_workers(total, a.tile_workers);
       const int w0 = split_owner(x0, total, workers);
       const int w1 = split_owner(x0 + steps - 1, total, workers);

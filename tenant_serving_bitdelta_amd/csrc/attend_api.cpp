@@ -16,7 +16,8 @@ namespace {
 
 constexpr int64_t kMaxKeys = int64_t(1) << 30;  // positions of a key list stay far below 2^31
 
-// Workgroups of a split launch: three row workgroups, or one tile workgroup, fit a compute unit.
+// Workgroups of a split launch: up to three row workgroups, or one tile workgroup, fit a compute
+// unit.
 constexpr int kRowWorkers = 768;
 constexpr int kTileWorkers = 256;
 
@@ -34,14 +35,14 @@ struct Plan {
   int row_rows;        // rows of a row unit
   int64_t row_units, row_workers;
   int64_t tile_units, tile_workers;
-  size_t scan_bytes, row_o, row_ml, tile_o, tile_ml;
+  size_t scan_bytes, row_o, row_ml, segs_bytes, tile_o, tile_ml;
   size_t total;
 };
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 void lay_out(Plan* p, int64_t batch, int dim) {
-  p->scan_bytes = p->row_o = p->row_ml = p->tile_o = p->tile_ml = 0;
+  p->scan_bytes = p->row_o = p->row_ml = p->segs_bytes = p->tile_o = p->tile_ml = 0;
   if (p->kind == Kind::kRowsSplit || p->kind == Kind::kPrefixTiles) {
     const size_t slots = (size_t)(p->row_units + p->row_workers) * p->row_rows;
     p->scan_bytes = up256((size_t)(batch + 1) * 4);
@@ -50,10 +51,11 @@ void lay_out(Plan* p, int64_t batch, int dim) {
   }
   if (p->kind == Kind::kPrefixTiles) {
     const size_t slots = (size_t)(p->tile_units + p->tile_workers) * bd::kTileRows;
+    p->segs_bytes = up256((BITDELTA_MAX_SEGMENTS + 1) * 4);  // each of two
     p->tile_o = up256(slots * dim * 4);
     p->tile_ml = up256(slots * 8);
   }
-  p->total = p->scan_bytes + p->row_o + p->row_ml + p->tile_o + p->tile_ml;
+  p->total = p->scan_bytes + p->row_o + p->row_ml + 2 * p->segs_bytes + p->tile_o + p->tile_ml;
 }
 
 bitdelta_status check_cache(const bitdelta_kv_cache* c, int32_t heads) {
@@ -191,11 +193,18 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
   a->tile_workers = (int)p.tile_workers;
   a->direct = p.kind == Kind::kRows;
   a->row_prefix = a->nseg > 0 && p.kind != Kind::kPrefixTiles;
-  a->scan = reinterpret_cast<int32_t*>(ws);
-  a->part_o = reinterpret_cast<float*>(ws + p.scan_bytes);
-  a->part_ml = reinterpret_cast<float*>(ws + p.scan_bytes + p.row_o);
-  a->tile_o = reinterpret_cast<float*>(ws + p.scan_bytes + p.row_o + p.row_ml);
-  a->tile_ml = reinterpret_cast<float*>(ws + p.scan_bytes + p.row_o + p.row_ml + p.tile_o);
+  auto take = [&](size_t bytes) {
+    unsigned char* at = ws;
+    ws += bytes;
+    return at;
+  };
+  a->scan = reinterpret_cast<int32_t*>(take(p.scan_bytes));
+  a->part_o = reinterpret_cast<float*>(take(p.row_o));
+  a->part_ml = reinterpret_cast<float*>(take(p.row_ml));
+  a->tile_segs = reinterpret_cast<int32_t*>(take(p.segs_bytes));
+  a->tile_scan = reinterpret_cast<int32_t*>(take(p.segs_bytes));
+  a->tile_o = reinterpret_cast<float*>(take(p.tile_o));
+  a->tile_ml = reinterpret_cast<float*>(take(p.tile_ml));
   if (p.kind == Kind::kTiles) {
     const int tpt = bd::kTileRows / a->group;
     // each sequence rounds its tokens up to whole tiles
