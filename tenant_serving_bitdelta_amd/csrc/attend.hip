@@ -113,6 +113,33 @@ __device__ __forceinline__ u32x2 lds_read_tr(const unsigned char* p) {
                                        (lds_s16x4*)(const_cast<unsigned char*>(p))));
 }
 
+// Copies straight from memory into LDS: 16 (4) bytes per lane, lane l's to the LDS address
+// `to` + 16 l (4 l), the same `to` for the wave.  In assembly because the compiler, which knows what the builtin does, puts
+// a wait for all copies before every transposed LDS read; here each step waits for its own
+// (wait_copies).  The instruction has no result register, and its address is read as it issues.
+__device__ __forceinline__ unsigned lds_address(const void* p) {
+  return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+__device__ __forceinline__ void copy16(const unsigned char* from, unsigned to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(const int32_t* from, unsigned to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to)
+               : "memory", "m0");
+}
+// until at most n of the wave's memory operations, the newest, are not done
+template <int n>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
+}
+// The workgroup meets, its LDS accesses done; copies into LDS may still be on their way.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -586,27 +613,28 @@ void attend_row_kernel(const AttendArgs a) {
 
 // ---------------------------------------------------------------------------------------------
 // Tile kernel: 256 query rows (tokens x the heads of one kv head) against a key list in 64-key
-// steps.  8 waves of 32 rows; K and V tiles in LDS: while a step is worked on the next one's rows
-// are in registers, on their way to the other buffers.  (Letting the second wave of each SIMD run a
-// third of a step late, its product with the values put off to the next step, measured 4% slower.)
+// steps.  8 waves of 32 rows; K and V tiles in LDS.  A bf16 cache's rows go straight from memory
+// into LDS, three steps ahead, in four buffers; an e4m3 cache's rows pass through registers, which
+// widen them, one step ahead, in two.  (Letting the second wave of each SIMD run a third of a step
+// late, its product with the values put off to the next step, measured 4% slower.)
 // ---------------------------------------------------------------------------------------------
 // Byte offsets of a key's rows; bit 0 of k: there is no such key (offsets 0).
 struct RowPlace {
   int64_t k, v;
 };
-// Where the lane's key of a step sits: its table entry, loaded a step before the rows' offsets are
-// worked out from it.
+// Where the lane's key sits: its table entry (null: no such key), and the rows' offsets from it.
 struct KeyLookup {
-  int id, slot;
-  __device__ __forceinline__ void begin(const PagedCache& c, const KeyList& kl, int vp) {
+  const int32_t* entry;
+  int slot;
+  __device__ __forceinline__ KeyLookup(const PagedCache& c, const KeyList& kl, int vp) {
     const int kp = key_position(kl, vp);
     const int page = page_quotient(kp < 0 ? 0 : kp, c.div);
     const int at = key_table_index(kl, vp, page);
     slot = kp - page * c.page_size;
-    id = at >= 0 ? (vp < kl.na ? kl.ta : kl.tb)[at] : -1;
+    entry = at >= 0 ? (vp < kl.na ? kl.ta : kl.tb) + at : nullptr;
   }
-  __device__ __forceinline__ RowPlace end(const PagedCache& c) const {
-    const bool ok = page_id_checked(id, c.num_pages) >= 0;
+  __device__ __forceinline__ RowPlace place(const PagedCache& c, int id) const {
+    const bool ok = entry && page_id_checked(id, c.num_pages) >= 0;
     const int p = ok ? id : 0, t = ok ? slot : 0;
     return RowPlace{page_row_bytes(p, t, c.k_page, c.k_token) | (ok ? 0 : 1),
                     page_row_bytes(p, t, c.v_page, c.v_token)};
@@ -703,10 +731,12 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
   constexpr int kTile = kTileKeys * D * 2;
   constexpr int kSteps = D / 16;   // matrix steps over D of a score tile
   constexpr int kOut = D / 32;     // 32-row tiles of O^T
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // 2 K tiles, 2 V tiles
-  unsigned char* const vbuf = smem + 2 * kTile;
-  __shared__ int state[2][kTileKeys];
+  constexpr int kBuffers = FP8 ? 2 : 4;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // K tiles, then V tiles
+  unsigned char* const vbuf = smem + kBuffers * kTile;
+  __shared__ int state[FP8 ? 2 : 8][kTileKeys];
   __shared__ RowPlace places[2][kTileKeys];
+  __shared__ int entries[8][kTileKeys];
   __shared__ int scan[kAttendMaxSeqs + 1];
   __shared__ int segs[PREFIX ? kAttendMaxSegments + 1 : 1];
   __shared__ int wave_sum[8];
@@ -715,6 +745,9 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane & 31, hf = lane >> 5;
   const int tpt = kTileRows / a.group;  // tokens per tile
+
+  const unsigned smem_at = __builtin_amdgcn_readfirstlane(lds_address(smem));
+  const unsigned entries_at = __builtin_amdgcn_readfirstlane(lds_address(entries));
 
   // ---- work: prefix: a share of all (segment, row tile, kv head) units' steps; window: one unit
   int64_t x = 0, x_end = 1, total = 1;
@@ -803,6 +836,10 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
         qf[s] = live ? *reinterpret_cast<const u32x4*>(qp + 16 * s) : u32x4{0, 0, 0, 0};
+      // wait for the queries here: left to their first use, in the loop, the wait would be for the
+      // copies on their way, too
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) asm volatile("" : "+v"(qf[s]));
     }
     f32x16 o[kOut];
 #pragma unroll
@@ -811,19 +848,23 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
     float m = kNegInf, l = 0.f;
 
-    // The pipeline: the keys of step t are looked up by one wave (wave t mod 8, one lane a key): table
-    // entries loaded in step t - 4, rows' offsets written to LDS in step t - 3; all threads load the
-    // rows in step t - 2 and write them to LDS in step t - 1.
-    TileStage<D, FP8> st;
-    KeyLookup look;
-    const int my_unit = 16 * (tid % TileStage<D, FP8>::kUnits);
-    const unsigned char* const kh = a.cache.k + (int64_t)h * a.cache.k_head + my_unit;
-    const unsigned char* const vh = a.cache.v + (int64_t)h * a.cache.v_head + my_unit;
+    // The pipeline: the keys of step t are looked up by one wave (wave t mod 8, one lane a key).
+    // Table entries are copied into LDS, so that no register waits for them; two steps later the
+    // rows' offsets are worked out, and a step later the rows' loads begin.
+    constexpr int kAhead = FP8 ? 2 : 3;  // steps from the loads to the step they are for
     auto look_begin = [&](int s) {
-      if (((s - s_begin) & 7) == wave) look.begin(a.cache, kl, s * kTileKeys + lane);
+      if (((s - s_begin) & 7) == wave) {
+        const KeyLookup look(a.cache, kl, s * kTileKeys + lane);
+        if (look.entry) copy4(look.entry, entries_at + wave * kTileKeys * 4);
+      }
     };
     auto look_end = [&](int s) {
-      if (((s - s_begin) & 7) == wave) places[(s - s_begin) & 1][lane] = look.end(a.cache);
+      if (((s - s_begin) & 7) == wave) {
+        const KeyLookup look(a.cache, kl, s * kTileKeys + lane);
+        const RowPlace at = look.place(a.cache, entries[wave][lane]);
+        places[(s - s_begin) & 1][lane] = at;
+        if constexpr (!FP8) state[(s - s_begin) & 7][lane] = (at.k & 1) == 0;
+      }
     };
     // edge step: some row of the tile does not see some key of it (the same for all waves)
     auto hides = [&](int base) {
@@ -831,19 +872,44 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       const int f = key_position(kl, base), last = key_position(kl, base + kTileKeys - 1);
       return base < kl.na || last > p0 || p0 + nt - 1 - f >= a.window;
     };
-    look_begin(s_begin);
-    look_begin(s_begin + 1);
-    look_begin(s_begin + 2);
-    look_begin(s_begin + 3);
+    const unsigned char* const kh = a.cache.k + (int64_t)h * a.cache.k_head;
+    const unsigned char* const vh = a.cache.v + (int64_t)h * a.cache.v_head;
+    TileStage<D, FP8> st;
+    // bf16: each wave moves 8 rows of K and of V, a lane 16 bytes: the stored unit lane % kU of row
+    // r holds the row's unit (lane % kU) ^ swizzle(r)
+    constexpr int kU = D / 8, kCopies = kU / 8;  // units of a row; copies of each tensor per wave
+    auto copy_rows = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        const int r0 = 8 * wave + i * (64 / kU), r = r0 + lane / kU, u = lane % kU;
+        const RowPlace at = places[(s - s_begin) & 1][r];
+        const unsigned to = smem_at + ((s - s_begin) & 3) * kTile + r0 * (D * 2);
+        copy16(kh + (at.k & ~15ll) + ((k_unit<D>(r, u) - r * (D * 2))), to);
+        copy16(vh + at.v + (v_unit<D>(r, u) - r * (D * 2)), to + kBuffers * kTile);
+      }
+    };
+    for (int i = 0; i < kAhead + 3; ++i) look_begin(s_begin + i);
+    wait_copies<0>();
     look_end(s_begin);
     look_end(s_begin + 1);
     __syncthreads();  // (also: the last unit's tiles are no longer read)
-    st.fetch(kh, vh, places[0], tid);
-    st.store(smem, vbuf, state[0], hides(s_begin * kTileKeys), tid);
-    st.fetch(kh, vh, places[1], tid);
-    __syncthreads();
-    look_end(s_begin + 2);
-    __syncthreads();
+    if constexpr (FP8) {
+      const int unit = 16 * (tid % TileStage<D, FP8>::kUnits);
+      st.fetch(kh + unit, vh + unit, places[0], tid);
+      st.store(smem, vbuf, state[0], hides(s_begin * kTileKeys), tid);
+      st.fetch(kh + unit, vh + unit, places[1], tid);
+      __syncthreads();
+      look_end(s_begin + 2);
+      __syncthreads();
+    } else {
+      copy_rows(s_begin);
+      if (s_begin + 1 < s_end) copy_rows(s_begin + 1);
+      lds_barrier();
+      look_end(s_begin + 2);
+      look_end(s_begin + 3);
+      lds_barrier();
+      if (s_begin + 2 < s_end) copy_rows(s_begin + 2);
+    }
 
     // O^T += V^T P^T of step s: of 16 keys the lane's 8 are 4 hf .. + 3 and 8 + 4 hf .. + 3
     u32x4 p[4];
@@ -862,11 +928,50 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
         }
     };
     for (int s = s_begin; s < s_end; ++s) {
-      const int buf = (s - s_begin) & 1;
+      const int buf = (s - s_begin) & (kBuffers - 1), note = (s - s_begin) & (FP8 ? 1 : 7);
       const unsigned char* kt = smem + buf * kTile;
       const int base = s * kTileKeys;
-      const int key_state = state[buf][lane];
+      if constexpr (!FP8) {
+        // this step's rows are in place once each wave's own copies are (at most the next two
+        // steps' may still be on their way) and all waves have met; the last step's buffers are
+        // free then
+        if (s + 2 < s_end) wait_copies<4 * kCopies>();
+        else if (s + 1 < s_end) wait_copies<2 * kCopies>();
+        else wait_copies<0>();
+        lds_barrier();
+      }
+      int key_state = state[note][lane];
       const uint64_t valid = __ballot(key_state & 1);
+      if constexpr (!FP8) {
+        const bool edge = hides(base);
+        if (valid != ~0ull || edge) {
+          // absent keys' rows become zeros; values that are not finite, too, where some row does not
+          // see them (added below for the rows that do): thread tid looks at units of row tid / 8
+          const int r = tid >> 3, u0 = (tid & 7) * kCopies;
+          unsigned char* const vt = vbuf + buf * kTile;
+          if (!((valid >> r) & 1)) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i)
+              *reinterpret_cast<u32x4*>(smem + buf * kTile + k_unit<D>(r, u0 + i)) =
+                  *reinterpret_cast<u32x4*>(vt + v_unit<D>(r, u0 + i)) = u32x4{0, 0, 0, 0};
+          } else if (edge) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+              u32x4 v = *reinterpret_cast<const u32x4*>(vt + v_unit<D>(r, u0 + i));
+              if (clear_odd<false>(&v)) {
+                *reinterpret_cast<u32x4*>(vt + v_unit<D>(r, u0 + i)) = v;
+                atomicOr(&state[note][r], 2);
+              }
+            }
+          }
+          lds_barrier();
+          key_state = state[note][lane];
+        }
+        // (the entries of step s + 4, copied before the two newest steps' rows, are there)
+        look_end(s + 4);
+        look_begin(s + 6);
+        if (s + 3 < s_end) copy_rows(s + 3);
+      }
       // does the wave see anything, does every row see everything?
       bool any = wave_live && valid != 0, all = valid == ~0ull;
       if constexpr (!PREFIX) {
@@ -907,14 +1012,18 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
         }
         __builtin_amdgcn_sched_group_barrier(0x008, 2 * kDeep, 0);
       }
-      // ---- the next step's tiles; these buffers were last read before the barrier that began this
-      // step
-      if (s + 1 < s_end) {
-        st.store(smem + (buf ^ 1) * kTile, vbuf + (buf ^ 1) * kTile, state[buf ^ 1],
-                 hides(base + kTileKeys), tid);
-        st.fetch(kh, vh, places[buf], tid);
-        look_end(s + 3);
-        look_begin(s + 4);
+      if constexpr (FP8) {
+        // ---- the next step's tiles; these buffers were last read before the barrier that began
+        // this step
+        if (s + 1 < s_end) {
+          const int unit = 16 * (tid % TileStage<D, FP8>::kUnits);
+          st.store(smem + (buf ^ 1) * kTile, vbuf + (buf ^ 1) * kTile, state[buf ^ 1],
+                   hides(base + kTileKeys), tid);
+          st.fetch(kh + unit, vh + unit, places[buf], tid);
+          // (the loads that st.store waited for are newer than the entries')
+          look_end(s + 3);
+          look_begin(s + 5);
+        }
       }
       if (any) {
         // lane (q, hf) holds keys 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
@@ -981,8 +1090,10 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
           }
         }
       }
-      __syncthreads();
+      if constexpr (FP8) __syncthreads();
     }
+    // no copy into LDS outlives its use: the next unit, or workgroup, has these buffers
+    wait_copies<0>();
 
     // ---- epilogue: lane (q, hf) holds dims 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
     l = half_sum(l);
@@ -1134,7 +1245,7 @@ hipError_t rows_for(const AttendArgs& a, int columns, int blocks, hipStream_t st
 
 template <int D, bool FP8, bool PREFIX>
 hipError_t tiles_for(const AttendArgs& a, int blocks, hipStream_t stream) {
-  constexpr int lds = 4 * kTileKeys * D * 2;
+  constexpr int lds = (FP8 ? 4 : 8) * kTileKeys * D * 2;
   static DeviceOnce once;
   const hipError_t e = set_dynamic_lds_once(
       once, reinterpret_cast<const void*>(&attend_tile_kernel<D, FP8, PREFIX>), lds);
