@@ -192,9 +192,9 @@ struct RowUnit {
   int t0, nq;   // first token row of q, tokens
   int p0;       // position of the first token (window op)
 };
-__device__ __forceinline__ RowUnit row_unit(const AttendArgs& a, int b) {
+__device__ __forceinline__ RowUnit row_unit(const AttendArgs& a, int b, int len) {
   RowUnit u;
-  const int len = clamp_len(a.lens[b], a.width, a.cache.page_size);
+  len = clamp_len(len, a.width, a.cache.page_size);
   const int32_t* row = a.table + (int64_t)b * a.width;
   if (a.nseg > 0) {
     u.t0 = b;
@@ -226,6 +226,9 @@ __device__ __forceinline__ RowUnit row_unit(const AttendArgs& a, int b) {
     u.keys = window_keys(row, a.width, len, u.p0, a.window, a.sinks);
   }
   return u;
+}
+__device__ __forceinline__ RowUnit row_unit(const AttendArgs& a, int b) {
+  return row_unit(a, b, a.lens[b]);
 }
 __device__ __forceinline__ int row_steps(const RowUnit& u) {
   return u.nq > 0 ? (u.keys.n + kRowStep - 1) / kRowStep : 0;
@@ -337,7 +340,7 @@ void attend_row_kernel(const AttendArgs a) {
   constexpr int kWaveLds = kRowKeys * D * 2;
   __shared__ __attribute__((aligned(16))) unsigned char vlds[kRowWaves * kWaveLds];
   __shared__ float ml[kRowWaves][16][2];
-  __shared__ int scan[kAttendMaxSeqs + 1];
+  __shared__ int scan[kAttendMaxSeqs + 1], lens[kAttendMaxSeqs];
   __shared__ int wave_sum[kRowWaves];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -350,7 +353,10 @@ void attend_row_kernel(const AttendArgs a) {
     x = 0;
     x_end = 1;
   } else {
-    block_scan<256>(scan, wave_sum, a.batch, [&](int b) { return row_steps(row_unit(a, b)); });
+    block_scan<256>(scan, wave_sum, a.batch, [&](int b) {
+      lens[b] = a.lens[b];
+      return row_steps(row_unit(a, b, lens[b]));
+    });
     total = (int64_t)scan[a.batch] * a.kv_heads;
     if (blockIdx.x == 0)
       for (int i = tid; i <= a.batch; i += 256) a.scan[i] = scan[i];
@@ -372,7 +378,7 @@ void attend_row_kernel(const AttendArgs a) {
       x = x_end;
     } else {
       b = scan_find(scan, a.batch, (int)(x / a.kv_heads));
-      u = row_unit(a, b);
+      u = row_unit(a, b, lens[b]);
       const int s = row_steps(u);
       const int64_t x0 = (int64_t)scan[b] * a.kv_heads;
       h = (int)((x - x0) / s);
@@ -916,16 +922,15 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
     const int l16 = lane & 15;
     const int v_row = 4 * hf + (l16 >> 2), v_un = 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1);
     const int v_b = 8 * (l16 & 1);
-    auto add_values = [&](int buf) {
+    u32x4 vf[2][kOut];
+    auto read_values = [&](int buf, int kb) {
       const unsigned char* vt = vbuf + buf * kTile;
 #pragma unroll
-      for (int kb = 0; kb < 4; ++kb)
-#pragma unroll
-        for (int i = 0; i < kOut; ++i) {
-          const u32x2 lo = lds_read_tr(vt + v_unit<D>(16 * kb + v_row, 4 * i + v_un) + v_b);
-          const u32x2 hi = lds_read_tr(vt + v_unit<D>(16 * kb + 8 + v_row, 4 * i + v_un) + v_b);
-          o[i] = mfma32(u32x4{lo[0], lo[1], hi[0], hi[1]}, p[kb], o[i]);
-        }
+      for (int i = 0; i < kOut; ++i) {
+        const u32x2 lo = lds_read_tr(vt + v_unit<D>(16 * kb + v_row, 4 * i + v_un) + v_b);
+        const u32x2 hi = lds_read_tr(vt + v_unit<D>(16 * kb + 8 + v_row, 4 * i + v_un) + v_b);
+        vf[kb & 1][i] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
     };
     for (int s = s_begin; s < s_end; ++s) {
       const int buf = (s - s_begin) & (kBuffers - 1), note = (s - s_begin) & (FP8 ? 1 : 7);
@@ -1043,11 +1048,19 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
             }
           }
         }
+        // the first values are on their way while the weights are worked out
+        read_values(buf, 0);
+        __builtin_amdgcn_sched_barrier(0);
         // (elementwise maximum: a NaN among a row's scores passes, the row is NaN then)
-        float tm = kNegInf;
+        float tp[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          tm = __builtin_elementwise_maximum(tm, __builtin_elementwise_maximum((float)sc[0][e], (float)sc[1][e]));
+        for (int e = 0; e < 4; ++e) {
+          tp[e] = sc[0][e];
+#pragma unroll
+          for (int i = 4; i < 32; i += 4) tp[e] = __builtin_elementwise_maximum(tp[e], (float)sc[(i + e) >> 4][(i + e) & 15]);
+        }
+        float tm = __builtin_elementwise_maximum(__builtin_elementwise_maximum(tp[0], tp[1]),
+                                                 __builtin_elementwise_maximum(tp[2], tp[3]));
         tm = half_max(tm) * a.c;
         if (__any(tm > m + kRescale)) {
           const float mn = fmaxf(m, tm);
@@ -1058,20 +1071,25 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
           for (int i = 0; i < kOut; ++i) o[i] *= f;
         }
         const float mb = m == kNegInf ? 0.f : m;
+        float lp[4];
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
           float e[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            e[i] = exp2_fast(__builtin_fmaf(sc[kb >> 1][8 * (kb & 1) + i], a.c, -mb));
-            l += e[i];
-          }
+          for (int i = 0; i < 8; ++i) e[i] = exp2_fast(__builtin_fmaf(sc[kb >> 1][8 * (kb & 1) + i], a.c, -mb));
+          lp[kb] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
           // weights enter the product as bf16 (relative error 2^-9 each, as the values they
           // weigh); the sum l keeps them in fp32
           p[kb] = u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
                         pack_bf16(e[6], e[7])};
         }
-        add_values(buf);
+        l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          if (kb < 3) read_values(buf, kb + 1);
+#pragma unroll
+          for (int i = 0; i < kOut; ++i) o[i] = mfma32(vf[kb & 1][i], p[kb], o[i]);
+        }
         if constexpr (!PREFIX) {
           if (!all) {
             for (uint64_t odd = __ballot(key_state & 2); odd; odd &= odd - 1) {
@@ -1154,15 +1172,29 @@ __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a)
 
   float mx = kNegInf, lt = 0.f;
   f32x4 ot = {0.f, 0.f, 0.f, 0.f};
-  auto add = [&](const float* ml, const float* o) {
-    const float pm = ml[0], pl = ml[1];
-    const f32x4 po = *reinterpret_cast<const f32x4*>(o + 4 * d4);
+  auto add = [&](float pm, float pl, const f32x4& po) {
     const float mn = fmaxf(mx, pm);
     const float mb = mn == kNegInf ? 0.f : mn;
     const float f0 = exp2_fast(mx - mb), f1 = exp2_fast(pm - mb);
     lt = lt * f0 + pl * f1;
     ot = ot * f0 + po * f1;
     mx = mn;
+  };
+  // the pieces of workers w0 .. w1, row `row` of slots of `rows`, four loads in flight
+  auto add_pieces = [&](int w0, int w1, int64_t unit, int rows, int row, const float* ml, const float* o) {
+    for (int w = w0 + way; w <= w1; w += 4 * kWays) {
+      f32x2 pm[4];
+      f32x4 po[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t at = (min(w + i * kWays, w1) + unit) * rows + row;
+        pm[i] = *reinterpret_cast<const f32x2*>(ml + at * 2);
+        po[i] = *reinterpret_cast<const f32x4*>(o + at * D + 4 * d4);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (w + i * kWays <= w1) add(pm[i][0], pm[i][1], po[i]);
+    }
   };
   // own rows
   {
@@ -1174,11 +1206,7 @@ __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a)
       const int workers = split_workers(total, a.workers);
       const int w0 = split_owner(x0, total, workers);
       const int w1 = split_owner(x0 + steps - 1, total, workers);
-      const int64_t unit = (int64_t)b * a.kv_heads + h;
-      for (int w = w0 + way; w <= w1; w += kWays) {
-        const int64_t at = (w + unit) * a.rows + row;
-        add(a.part_ml + at * 2, a.part_o + at * D);
-      }
+      add_pieces(w0, w1, (int64_t)b * a.kv_heads + h, a.rows, row, a.part_ml, a.part_o);
     }
   }
   // the prefix
@@ -1197,11 +1225,7 @@ __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a)
       const int workers = split_workers(total, a.tile_workers);
       const int w0 = split_owner(x0, total, workers);
       const int w1 = split_owner(x0 + steps - 1, total, workers);
-      const int64_t unit = (int64_t)ub * a.kv_heads + h * tiles + rt;
-      for (int w = w0 + way; w <= w1; w += kWays) {
-        const int64_t at = (w + unit) * kTileRows + row;
-        add(a.tile_ml + at * 2, a.tile_o + at * D);
-      }
+      add_pieces(w0, w1, (int64_t)ub * a.kv_heads + h * tiles + rt, kTileRows, row, a.tile_ml, a.tile_o);
     }
   }
   // the ways' sums

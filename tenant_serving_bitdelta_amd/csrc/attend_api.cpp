@@ -16,14 +16,18 @@ namespace {
 
 constexpr int64_t kMaxKeys = int64_t(1) << 30;  // positions of a key list stay far below 2^31
 
-// Workgroups of a split launch: up to three row workgroups, or one tile workgroup, fit a compute
-// unit.
-constexpr int kRowWorkers = 768;
+// Workgroups of a split launch: as many as the 256 compute units hold at a time (more would start
+// when the first have ended, and take as long again), which their registers decide.
+int row_workers(int columns, int64_t max_q, const bitdelta_kv_cache& c) {
+  if (columns == 1 && max_q == 1 && (c.dtype == BITDELTA_KV_FP8 || c.head_dim == 64)) return 768;
+  return columns <= 2 ? 512 : 256;
+}
 constexpr int kTileWorkers = 256;
 
 // A unit (sequence, kv head) whose key list is at most this many 128-key steps long is done by one
-// workgroup, without partials and the launch that joins them.
-constexpr int kDirectSteps = 8;
+// workgroup, without partials and the launch that joins them.  A step takes such a workgroup about
+// 2 us, the split and joined form of a short call about 14 us in all (9 steps: 22.9 against 14).
+constexpr int kDirectSteps = 6;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -129,7 +133,7 @@ Plan plan_shared(int64_t batch, int32_t heads, const bitdelta_kv_cache& c, int32
   }
   const int64_t keys = p.kind == Kind::kPrefixTiles ? own : own + pre;
   const int64_t steps = p.row_units * ((keys + bd::kRowStep - 1) / bd::kRowStep);
-  p.row_workers = std::min<int64_t>(kRowWorkers, std::max<int64_t>(1, steps));
+  p.row_workers = std::min<int64_t>(row_workers(p.columns, 1, c), std::max<int64_t>(1, steps));
   lay_out(&p, batch, c.head_dim);
   return p;
 }
@@ -150,7 +154,8 @@ Plan plan_window(int32_t heads, const bitdelta_kv_cache& c, int32_t batch, int32
                                          (int64_t)window + max_q - 1 + sinks);
   const int64_t steps = (keys + bd::kRowStep - 1) / bd::kRowStep;
   p.kind = steps <= kDirectSteps ? Kind::kRows : Kind::kRowsSplit;
-  p.row_workers = std::min<int64_t>(kRowWorkers, std::max<int64_t>(1, p.row_units * steps));
+  p.row_workers = std::min<int64_t>(row_workers(p.columns, max_q, c),
+                                    std::max<int64_t>(1, p.row_units * steps));
   lay_out(&p, batch, c.head_dim);
   return p;
 }
