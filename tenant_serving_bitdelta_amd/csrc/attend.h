@@ -119,6 +119,7 @@ struct AttendArgs {
   float v_scale;
   int32_t workers;              // row kernel workgroups
   int32_t tile_workers;         // tile kernel workgroups that split the prefixes
+  int32_t halves;               // tile kernel: units of up to 128 rows take two key tiles a step
   int32_t row_prefix;           // row kernel: 1 = a sequence's keys start with its prefix
   int32_t direct;               // row kernel: one workgroup per unit, written without partials
   // workspace

@@ -621,7 +621,9 @@ void attend_row_kernel(const AttendArgs a) {
 // Tile kernel: 256 query rows (tokens x the heads of one kv head) against a key list in 64-key
 // steps.  8 waves of 32 rows; K and V tiles in LDS.  A bf16 cache's rows go straight from memory
 // into LDS, three steps ahead, in four buffers; an e4m3 cache's rows pass through registers, which
-// widen them, one step ahead, in two.  (Letting the second wave of each SIMD run a third of a step
+// widen them, one step ahead, in two.  Where a segment's rows fill at most half the waves (and the
+// cache is bf16), the other half takes a second key tile of the same step, and both halves' sums are
+// joined later with the pieces.  (Letting the second wave of each SIMD run a third of a step
 // late, its product with the values put off to the next step, measured 4% slower.)
 // ---------------------------------------------------------------------------------------------
 // Byte offsets of a key's rows; bit 0 of k: there is no such key (offsets 0).
@@ -732,6 +734,16 @@ struct TileStage {
   }
 };
 
+// segments whose rows fit half a tile: their units take two 64-key tiles a step
+__device__ __forceinline__ bool halved(const AttendArgs& a, int sg) {
+  return a.halves && (a.seg_offsets[sg + 1] - a.seg_offsets[sg]) * a.group <= kTileRows / 2;
+}
+__device__ __forceinline__ int prefix_steps(const AttendArgs& a, int sg) {
+  const int len = clamp_len(a.prefix_lens[sg], a.pwidth, a.cache.page_size);
+  const int keys = halved(a, sg) ? 2 * kTileKeys : kTileKeys;
+  return (len + keys - 1) / keys;
+}
+
 template <int D, bool FP8, bool PREFIX>
 __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a) {
   constexpr int kTile = kTileKeys * D * 2;
@@ -741,7 +753,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // K tiles, then V tiles
   unsigned char* const vbuf = smem + kBuffers * kTile;
   __shared__ int state[FP8 ? 2 : 8][kTileKeys];
-  __shared__ RowPlace places[2][kTileKeys];
+  __shared__ RowPlace places[4][kTileKeys];
   __shared__ int entries[8][kTileKeys];
   __shared__ int scan[kAttendMaxSeqs + 1];
   __shared__ int segs[PREFIX ? kAttendMaxSegments + 1 : 1];
@@ -763,10 +775,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
     // row tiles and heads that read the same pages share its L2
     auto tiles_of = [&](int s) { return (a.seg_offsets[s + 1] - a.seg_offsets[s] + tpt - 1) / tpt; };
     block_scan<512>(segs, wave_sum, a.nseg, tiles_of);
-    block_scan<512>(scan, wave_sum, a.nseg, [&](int s) {
-      const int len = clamp_len(a.prefix_lens[s], a.pwidth, a.cache.page_size);
-      return tiles_of(s) * ((len + kTileKeys - 1) / kTileKeys);
-    });
+    block_scan<512>(scan, wave_sum, a.nseg, [&](int s) { return tiles_of(s) * prefix_steps(a, s); });
     if (blockIdx.x == 0)  // for the joining kernel
       for (int i = tid; i <= a.nseg; i += 512) {
         a.tile_segs[i] = segs[i];
@@ -788,20 +797,27 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
 
   while (x < x_end) {
     KeyList kl;
-    int t0, nt, p0 = 0, h, s_begin, s_end;
+    int t0, nt, p0 = 0, h, s_begin, s_end;  // steps of one key tile
     int64_t slot = 0;
+    bool half = false;
     if constexpr (PREFIX) {
       const int sg = scan_find(scan, a.nseg, (int)(x / a.kv_heads));
       const int n0 = a.seg_offsets[sg], n = a.seg_offsets[sg + 1] - n0;
       const int len = clamp_len(a.prefix_lens[sg], a.pwidth, a.cache.page_size);
-      const int steps = (len + kTileKeys - 1) / kTileKeys;
+      const int steps = prefix_steps(a, sg);
       const int tiles = (n + tpt - 1) / tpt;
+      half = halved(a, sg);
       int64_t r = x - (int64_t)scan[sg] * a.kv_heads;  // units: kv head major, then row tile
       h = (int)(r / ((int64_t)tiles * steps));
       r -= (int64_t)h * tiles * steps;
       const int rt = (int)(r / steps);
       s_begin = (int)(r - (int64_t)rt * steps);
       s_end = (int)(x_end - x < steps - s_begin ? s_begin + (x_end - x) : steps);
+      x += s_end - s_begin;
+      if (half) {
+        s_begin *= 2;
+        s_end = min(2 * s_end, (len + kTileKeys - 1) / kTileKeys);
+      }
       t0 = n0 + rt * tpt;
       nt = n - rt * tpt < tpt ? n - rt * tpt : tpt;
       slot = w_id + (int64_t)segs[sg] * a.kv_heads + h * tiles + rt;
@@ -827,14 +843,15 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       s_end = (kl.n + kTileKeys - 1) / kTileKeys;
     }
 
-    // ---- this lane's query row: 32 wave + q of the tile
-    const int row = 32 * wave + q;
+    // ---- this lane's query row: 32 * (wave's rows) + q of the tile
+    const int wave_rows = half ? wave & 3 : wave;
+    const int row = 32 * wave_rows + q;
     const int t = row / a.group, hh = h * a.group + row - t * a.group;
     const bool live = t < nt;
     const int pq = p0 + t;
     // positions of the wave's first and last live token
-    const int wt0 = 32 * wave / a.group;
-    const int wt1 = (32 * wave + 31) / a.group < nt ? (32 * wave + 31) / a.group : nt - 1;
+    const int wt0 = 32 * wave_rows / a.group;
+    const int wt1 = (32 * wave_rows + 31) / a.group < nt ? (32 * wave_rows + 31) / a.group : nt - 1;
     const bool wave_live = wt0 < nt;
     u32x4 qf[kSteps];
     {
@@ -868,7 +885,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
       if (((s - s_begin) & 7) == wave) {
         const KeyLookup look(a.cache, kl, s * kTileKeys + lane);
         const RowPlace at = look.place(a.cache, entries[wave][lane]);
-        places[(s - s_begin) & 1][lane] = at;
+        places[(s - s_begin) & 3][lane] = at;
         if constexpr (!FP8) state[(s - s_begin) & 7][lane] = (at.k & 1) == 0;
       }
     };
@@ -888,7 +905,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
 #pragma unroll
       for (int i = 0; i < kCopies; ++i) {
         const int r0 = 8 * wave + i * (64 / kU), r = r0 + lane / kU, u = lane % kU;
-        const RowPlace at = places[(s - s_begin) & 1][r];
+        const RowPlace at = places[(s - s_begin) & 3][r];
         const unsigned to = smem_at + ((s - s_begin) & 3) * kTile + r0 * (D * 2);
         copy16(kh + (at.k & ~15ll) + ((k_unit<D>(r, u) - r * (D * 2))), to);
         copy16(vh + at.v + (v_unit<D>(r, u) - r * (D * 2)), to + kBuffers * kTile);
@@ -896,25 +913,19 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
     };
     for (int i = 0; i < kAhead + 3; ++i) look_begin(s_begin + i);
     wait_copies<0>();
-    look_end(s_begin);
-    look_end(s_begin + 1);
-    __syncthreads();  // (also: the last unit's tiles are no longer read)
+    __syncthreads();  // the last unit's tiles and notes are no longer read
+    for (int i = 0; i <= kAhead; ++i) look_end(s_begin + i);
+    __syncthreads();
     if constexpr (FP8) {
       const int unit = 16 * (tid % TileStage<D, FP8>::kUnits);
       st.fetch(kh + unit, vh + unit, places[0], tid);
       st.store(smem, vbuf, state[0], hides(s_begin * kTileKeys), tid);
       st.fetch(kh + unit, vh + unit, places[1], tid);
       __syncthreads();
-      look_end(s_begin + 2);
-      __syncthreads();
     } else {
       copy_rows(s_begin);
       if (s_begin + 1 < s_end) copy_rows(s_begin + 1);
-      lds_barrier();
-      look_end(s_begin + 2);
-      look_end(s_begin + 3);
-      lds_barrier();
-      if (s_begin + 2 < s_end) copy_rows(s_begin + 2);
+      if (!half && s_begin + 2 < s_end) copy_rows(s_begin + 2);
     }
 
     // O^T += V^T P^T of step s: of 16 keys the lane's 8 are 4 hf .. + 3 and 8 + 4 hf .. + 3
@@ -932,7 +943,30 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
         vf[kb & 1][i] = u32x4{lo[0], lo[1], hi[0], hi[1]};
       }
     };
-    for (int s = s_begin; s < s_end; ++s) {
+    // rows of step s that are absent become zeros; values that are not finite, too, where some row
+    // does not see them (added below for the rows that do): thread tid looks at units of row tid / 8
+    auto mend = [&](int s, uint64_t valid, bool edge) {
+      const int r = tid >> 3, u0 = (tid & 7) * kCopies, at = (s - s_begin) & 3;
+      unsigned char* const vt = vbuf + at * kTile;
+      if (!((valid >> r) & 1)) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          *reinterpret_cast<u32x4*>(smem + at * kTile + k_unit<D>(r, u0 + i)) = u32x4{0, 0, 0, 0};
+          *reinterpret_cast<u32x4*>(vt + v_unit<D>(r, u0 + i)) = u32x4{0, 0, 0, 0};
+        }
+      } else if (edge) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          u32x4 v = *reinterpret_cast<const u32x4*>(vt + v_unit<D>(r, u0 + i));
+          if (clear_odd<false>(&v)) {
+            *reinterpret_cast<u32x4*>(vt + v_unit<D>(r, u0 + i)) = v;
+            atomicOr(&state[(s - s_begin) & 7][r], 2);
+          }
+        }
+      }
+    };
+    for (int s0 = s_begin; s0 < s_end; s0 += half ? 2 : 1) {
+      const int s = s0 + (half ? wave >> 2 : 0);  // this wave's tile
       const int buf = (s - s_begin) & (kBuffers - 1), note = (s - s_begin) & (FP8 ? 1 : 7);
       const unsigned char* kt = smem + buf * kTile;
       const int base = s * kTileKeys;
@@ -940,42 +974,36 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
         // this step's rows are in place once each wave's own copies are (at most the next two
         // steps' may still be on their way) and all waves have met; the last step's buffers are
         // free then
-        if (s + 2 < s_end) wait_copies<4 * kCopies>();
-        else if (s + 1 < s_end) wait_copies<2 * kCopies>();
+        if (!half && s + 2 < s_end) wait_copies<4 * kCopies>();
+        else if (!half && s + 1 < s_end) wait_copies<2 * kCopies>();
         else wait_copies<0>();
         lds_barrier();
       }
       int key_state = state[note][lane];
-      const uint64_t valid = __ballot(key_state & 1);
+      uint64_t valid = __ballot(key_state & 1);
       if constexpr (!FP8) {
         const bool edge = hides(base);
-        if (valid != ~0ull || edge) {
-          // absent keys' rows become zeros; values that are not finite, too, where some row does not
-          // see them (added below for the rows that do): thread tid looks at units of row tid / 8
-          const int r = tid >> 3, u0 = (tid & 7) * kCopies;
-          unsigned char* const vt = vbuf + buf * kTile;
-          if (!((valid >> r) & 1)) {
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i)
-              *reinterpret_cast<u32x4*>(smem + buf * kTile + k_unit<D>(r, u0 + i)) =
-                  *reinterpret_cast<u32x4*>(vt + v_unit<D>(r, u0 + i)) = u32x4{0, 0, 0, 0};
-          } else if (edge) {
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-              u32x4 v = *reinterpret_cast<const u32x4*>(vt + v_unit<D>(r, u0 + i));
-              if (clear_odd<false>(&v)) {
-                *reinterpret_cast<u32x4*>(vt + v_unit<D>(r, u0 + i)) = v;
-                atomicOr(&state[note][r], 2);
-              }
-            }
-          }
+        if (half) {  // two tiles, of which the second may be past the end
+          const uint64_t v0 = __ballot(state[(s0 - s_begin) & 7][lane] & 1);
+          const uint64_t v1 = s0 + 1 < s_end ? __ballot(state[(s0 + 1 - s_begin) & 7][lane] & 1) : ~0ull;
+          if (v0 != ~0ull) mend(s0, v0, false);
+          if (v1 != ~0ull) mend(s0 + 1, v1, false);
+          if ((v0 & v1) != ~0ull) lds_barrier();
+          if (s >= s_end) valid = 0;
+        } else if (valid != ~0ull || edge) {
+          mend(s, valid, edge);
           lds_barrier();
           key_state = state[note][lane];
         }
         // (the entries of step s + 4, copied before the two newest steps' rows, are there)
-        look_end(s + 4);
-        look_begin(s + 6);
-        if (s + 3 < s_end) copy_rows(s + 3);
+        look_end(s0 + 4);
+        look_begin(s0 + 6);
+        if (half) {
+          look_end(s0 + 5);
+          look_begin(s0 + 7);
+          if (s0 + 2 < s_end) copy_rows(s0 + 2);
+        }
+        if (s0 + 3 < s_end) copy_rows(s0 + 3);
       }
       // does the wave see anything, does every row see everything?
       bool any = wave_live && valid != 0, all = valid == ~0ull;
@@ -1024,7 +1052,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
           const int unit = 16 * (tid % TileStage<D, FP8>::kUnits);
           st.store(smem + (buf ^ 1) * kTile, vbuf + (buf ^ 1) * kTile, state[buf ^ 1],
                    hides(base + kTileKeys), tid);
-          st.fetch(kh + unit, vh + unit, places[buf], tid);
+          st.fetch(kh + unit, vh + unit, places[(s + 2 - s_begin) & 3], tid);
           // (the loads that st.store waited for are newer than the entries')
           look_end(s + 3);
           look_begin(s + 5);
@@ -1117,7 +1145,8 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
     l = half_sum(l);
     if (live) {
       if constexpr (PREFIX) {
-        float* op = a.tile_o + (slot * kTileRows + row) * D + 4 * hf;
+        const int64_t at = slot * kTileRows + row + (half ? (wave >> 2) * (kTileRows / 2) : 0);
+        float* op = a.tile_o + at * D + 4 * hf;
 #pragma unroll
         for (int i = 0; i < kOut; ++i)
 #pragma unroll
@@ -1125,8 +1154,8 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
             *reinterpret_cast<f32x4*>(op + 32 * i + 8 * e) =
                 f32x4{o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
         if (hf == 0) {
-          a.tile_ml[(slot * kTileRows + row) * 2] = m;
-          a.tile_ml[(slot * kTileRows + row) * 2 + 1] = l;
+          a.tile_ml[at * 2] = m;
+          a.tile_ml[at * 2 + 1] = l;
         }
       } else {
         const float inv = l > 0.f ? a.v_scale / l : (l == 0.f ? 0.f : l);
@@ -1143,11 +1172,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
               l == 0.f ? kNegInf : (m + __builtin_log2f(l)) * kLn2;
       }
     }
-    if constexpr (PREFIX) {
-      x += s_end - s_begin;
-    } else {
-      break;
-    }
+    if constexpr (!PREFIX) break;
   }
 }
 
@@ -1225,7 +1250,9 @@ __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a)
       const int workers = split_workers(total, a.tile_workers);
       const int w0 = split_owner(x0, total, workers);
       const int w1 = split_owner(x0 + steps - 1, total, workers);
-      add_pieces(w0, w1, (int64_t)ub * a.kv_heads + h * tiles + rt, kTileRows, row, a.tile_ml, a.tile_o);
+      const int64_t unit = (int64_t)ub * a.kv_heads + h * tiles + rt;
+      add_pieces(w0, w1, unit, kTileRows, row, a.tile_ml, a.tile_o);
+      if (halved(a, sg)) add_pieces(w0, w1, unit, kTileRows, row + kTileRows / 2, a.tile_ml, a.tile_o);
     }
   }
   // the ways' sums

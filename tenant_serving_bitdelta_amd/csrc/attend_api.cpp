@@ -196,6 +196,7 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
   a->rows = p.row_rows;
   a->workers = (int)p.row_workers;
   a->tile_workers = (int)p.tile_workers;
+  a->halves = !fp8;
   a->direct = p.kind == Kind::kRows;
   a->row_prefix = a->nseg > 0 && p.kind != Kind::kPrefixTiles;
   auto take = [&](size_t bytes) {
