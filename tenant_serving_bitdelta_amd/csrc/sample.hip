@@ -41,10 +41,12 @@ constexpr float kNegInf = -__builtin_inff();
 // directly: the kernel's time is largely latency, and much code run once costs fetches.
 struct Shared {
   uint64_t cand[kCap];
+  double cum[kCap];
   union {
-    double cum[kCap];
     unsigned long long bins[kBins];
+    double bin_mass[kBins];  // running weights, once the tallies have been read
   };
+  int bin_count[kBins];  // running counts
   uint16_t hits[kParts * kThreads];  // parts to read again: thread + kThreads * part
   int bucket[kThreads];
   double wave_d[kWaves];
@@ -52,8 +54,9 @@ struct Shared {
   int wave_i[kWaves], wave_n[2][kWaves];
   int count, nhits, best, most;
   int found;
-  double found_mass;
-  int found_count;
+  uint64_t few_token;
+  double few_mass;
+  int few_keep;
 };
 __shared__ Shared sh;
 
@@ -129,6 +132,7 @@ __device__ __noinline__ double exp_f64(double x) {
   e = __builtin_fma(e, r, 1.0);
   return __builtin_ldexp(e, (int)n);
 }
+__device__ __noinline__ double log_f64(double x) { return log(x); }
 // ln w and w; the largest logit weighs 1, also where it is infinite
 __device__ __forceinline__ double log_weight(float l, float top, double inv_t) {
   return l == top ? 0.0 : ((double)l - (double)top) * inv_t;
@@ -149,7 +153,8 @@ __device__ __forceinline__ double weight(float l, float top, double inv_t) {
 struct Bins {
   double offset, scale;  // of the place
   int low;               // bits below the count
-  float units;           // units of y in 1
+  float units;           // units of y in 1, a power of two
+  double unit;           // 1 / units
   float c1, c2, c3, c4;  // y in units as a polynomial of the 28 bits
   // false: places do not fit (T is so small that only the largest logit counts)
   __device__ __forceinline__ bool begin_at(double ref) {
@@ -162,6 +167,7 @@ struct Bins {
     const int cb = 32 - __builtin_clz((unsigned)vocab);  // a count takes up to cb bits
     low = 63 - cb;
     units = __builtin_ldexpf(1.0f, min(low - cb + 6, 36));
+    unit = 1.0 / (double)units;
     const float x1 = 1.0f / (kBinScale * 268435456.0f);  // 2^-34
     c1 = x1 * units;
     c2 = -0.5f * x1 * c1;
@@ -183,16 +189,58 @@ struct Bins {
   __device__ __forceinline__ int count(unsigned long long t) const { return (int)(t >> low); }
   // of a bin whose upper logit weighs 1
   __device__ __forceinline__ double weight(unsigned long long t) const {
-    return (double)count(t) - (double)(t & ((1ull << low) - 1)) / (double)units;
+    return (double)count(t) - (double)(t & ((1ull << low) - 1)) * unit;
   }
 };
 
+// ---- within a wave: lane i's sum of the lanes up to it (lane 63: of all), by moves between lanes
+// that need no shared memory.  kCtrl 0x110 + n: from n lanes below in the row of 16; 0x142, 0x143:
+// the last lane of the row, of the half, below to the next one.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int lane_move(int x, int otherwise) {
+  return __builtin_amdgcn_update_dpp(otherwise, x, kCtrl, kRows, 0xF, false);
+}
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double lane_move(double x) {
+  const long long b = __double_as_longlong(x);
+  const unsigned lo = (unsigned)lane_move<kCtrl, kRows>((int)b, 0);
+  const unsigned hi = (unsigned)lane_move<kCtrl, kRows>((int)(b >> 32), 0);
+  return __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
+}
+__device__ __forceinline__ double wave_scan(double x) {
+  x += lane_move<0x111, 0xF>(x);
+  x += lane_move<0x112, 0xF>(x);
+  x += lane_move<0x114, 0xF>(x);
+  x += lane_move<0x118, 0xF>(x);
+  x += lane_move<0x142, 0xA>(x);
+  return x + lane_move<0x143, 0xC>(x);
+}
+__device__ __forceinline__ int wave_scan(int x) {
+  x += lane_move<0x111, 0xF>(x, 0);
+  x += lane_move<0x112, 0xF>(x, 0);
+  x += lane_move<0x114, 0xF>(x, 0);
+  x += lane_move<0x118, 0xF>(x, 0);
+  x += lane_move<0x142, 0xA>(x, 0);
+  return x + lane_move<0x143, 0xC>(x, 0);
+}
+template <int kCtrl, int kRows>
+__device__ __forceinline__ float lane_move(float x) {  // where there is none: its own
+  return __int_as_float(lane_move<kCtrl, kRows>(__float_as_int(x), __float_as_int(x)));
+}
+__device__ __forceinline__ float wave_most(float x) {  // lane 63: of all
+  x = fmaxf(x, lane_move<0x111, 0xF>(x));
+  x = fmaxf(x, lane_move<0x112, 0xF>(x));
+  x = fmaxf(x, lane_move<0x114, 0xF>(x));
+  x = fmaxf(x, lane_move<0x118, 0xF>(x));
+  x = fmaxf(x, lane_move<0x142, 0xA>(x));
+  return fmaxf(x, lane_move<0x143, 0xC>(x));
+}
+
 // ---- sums over the workgroup, in a fixed order, to all threads
 __device__ __noinline__ double block_sum(double x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
+  x = wave_scan(x);
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh.wave_d[threadIdx.x >> 6] = x;
+  if ((threadIdx.x & 63) == 63) sh.wave_d[threadIdx.x >> 6] = x;
   __syncthreads();
   double t = 0;
 #pragma unroll
@@ -200,10 +248,9 @@ __device__ __noinline__ double block_sum(double x) {
   return t;
 }
 __device__ __noinline__ int block_count(int x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
+  x = wave_scan(x);
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh.wave_i[threadIdx.x >> 6] = x;
+  if ((threadIdx.x & 63) == 63) sh.wave_i[threadIdx.x >> 6] = x;
   __syncthreads();
   int t = 0;
 #pragma unroll
@@ -214,14 +261,10 @@ struct Range {
   float most, least;
 };
 __device__ __noinline__ Range block_range(float x) {
-  float y = x;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    x = fmaxf(x, __shfl_xor(x, d, 64));
-    y = fminf(y, __shfl_xor(y, d, 64));
-  }
+  const float y = -wave_most(-x);
+  x = wave_most(x);
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) {
+  if ((threadIdx.x & 63) == 63) {
     sh.wave_f[threadIdx.x >> 6] = x;
     sh.wave_g[threadIdx.x >> 6] = y;
   }
@@ -241,17 +284,8 @@ struct Before {
 };
 __device__ __noinline__ Before block_prefix(int n, double m) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int y = n;
-  double z = m;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int a = __shfl_up(y, d, 64);
-    const double b = __shfl_up(z, d, 64);
-    if (lane >= d) {
-      y += a;
-      z += b;
-    }
-  }
+  const int y = wave_scan(n);
+  const double z = wave_scan(m);
   __syncthreads();
   if (lane == 63) {
     sh.wave_i[wave] = y;
@@ -486,6 +520,32 @@ __device__ __noinline__ int count_heavy(int n, double m, float top, double inv_t
   return block_count(x);
 }
 
+// ---- up to 64 collected tokens: one wave orders and weighs them, a lane each, with no barriers
+struct Few {
+  uint64_t c;     // the lane's token in the order; 0: none
+  double w, cum;  // its weight, and the running sum
+};
+__device__ __noinline__ Few order_few(int n, float top, double inv_t) {
+  const int lane = threadIdx.x & 63;
+  uint64_t c = lane < n ? sh.cand[lane] : 0;
+  int rank = 0;  // tokens before it
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const uint64_t lo = (unsigned)__builtin_amdgcn_readlane((int)c, j);
+    const uint64_t hi = (unsigned)__builtin_amdgcn_readlane((int)(c >> 32), j);
+    rank += (hi << 32 | lo) > c;
+  }
+  if (lane >= n) rank = lane;
+  const unsigned lo = (unsigned)__builtin_amdgcn_ds_permute(4 * rank, (int)c);
+  const unsigned hi = (unsigned)__builtin_amdgcn_ds_permute(4 * rank, (int)(c >> 32));
+  c = (uint64_t)hi << 32 | lo;
+  const double w = lane < n ? weight(logit_of(c), top, inv_t) : 0.0;
+  return Few{c, w, wave_scan(w)};
+}
+__device__ __forceinline__ int lanes_below(int n, double t, bool or_equal, const Few& f) {
+  return __popcll(__ballot((int)(threadIdx.x & 63) < n && (or_equal ? f.cum <= t : f.cum < t)));
+}
+
 // ---- bisection: the last resort
 // Count and weight of the row's tokens at or above a composite.
 template <bool F32>
@@ -568,63 +628,66 @@ __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f,
   const int tid = threadIdx.x;
   const double inv_scale = 1.0 / bins.scale, ref = (bins.offset - 25165824.0) * inv_scale;
   const double lead = (double)(bins.place(top) & 0xFFFFFFFFFFull) * (1.0 / 268435456.0);  // of the largest
-  // running counts and weights (of the largest logit: 1) at the end of this thread's bins
-  int cnt[kOwn], cnt0 = 0;
-  double mass[kOwn], mass0 = 0;
+  // running counts and weights (of the largest logit: 1) before and after this thread's bins
+  int cnt0 = 0, cnt1 = 0;
+  double mass0 = 0, mass1 = 0;
   {
-    // bins far above the largest logit are empty
+    unsigned long long t[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) t[i] = sh.bins[kOwn * tid + i];
+    // a bin's upper logit weighs e^(-1/64) of the one's before (bins above the largest are empty)
+    double e = exp_f64((lead - (double)(kOwn * tid)) * (1.0 / kBinScale) - 1.0) * 2.718281828459045235;
+    double m[kOwn];
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-      const int b = kOwn * tid + i;
-      const unsigned long long t = sh.bins[b];
-      const double e = (lead - (double)b) * (1.0 / kBinScale);
-      cnt0 += bins.count(t);
-      if (t) mass0 += exp_f64(e - 1.0) * 2.718281828459045235 * bins.weight(t);
-      cnt[i] = cnt0;
-      mass[i] = mass0;
+      cnt1 += bins.count(t[i]);
+      m[i] = mass1 += e * bins.weight(t[i]);
+      e *= 0.98449643700540840596;  // e^(-1/64)
     }
-    const Before b = block_prefix(cnt0, mass0);
-    cnt0 = b.count;
+    const Before b = block_prefix(cnt1, mass1);
+    cnt0 = cnt1 = b.count;
     mass0 = b.mass;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-      cnt[i] += cnt0;
-      mass[i] += mass0;
+      sh.bin_count[kOwn * tid + i] = cnt1 += bins.count(t[i]);
+      sh.bin_mass[kOwn * tid + i] = mass1 = mass0 + m[i];
     }
   }
-  if (tid == kThreads - 1) sh.found_mass = mass[kOwn - 1];
+  if (tid == 0) sh.found = kBins - 1;
   __syncthreads();
-  int keep = f.vocab;                  // tokens kept
-  double zk = sh.found_mass, zn = zk;  // weight of the first k, of the tokens kept
+  // the value before is the one that the thread before ends with, to the last bit
+  mass0 = tid ? sh.bin_mass[kOwn * tid - 1] : 0.0;
+  int keep = f.vocab;                         // tokens kept
+  double zk = sh.bin_mass[kBins - 1], zn = zk;  // weight of the first k, of the tokens kept
   Answer r = {0, 0.0, false};
-  __syncthreads();
 #pragma unroll 1
   for (int stage = 0; stage < 4; ++stage) {
     if (stage == 0 ? f.k == f.vocab : (stage == 1 ? f.p >= 1.0 : (stage == 2 && f.minp == 0.0))) continue;
     // the border's bin: the first whose value passes the target, the last bin if none does
-    const double target = stage == 0   ? (double)f.k
-                          : stage == 1 ? f.p * zk
-                          : stage == 2 ? floor(lead - log(f.minp) * kBinScale)
-                                       : f.u * zn;
-    bool earlier = false;
-#pragma unroll
-    for (int i = -1; i < kOwn; ++i) {
-      const int b = kOwn * tid + i, c = i < 0 ? cnt0 : cnt[i < 0 ? 0 : i];
-      const double m = i < 0 ? mass0 : mass[i < 0 ? 0 : i];
-      const double x = stage == 0 ? (double)c : (stage == 2 ? (double)b : m);
-      const bool here = b >= 0 && (stage == 3 ? x > target : x >= target);
-      if (i >= 0 && !earlier && (here || b == kBins - 1)) {
-        sh.found = b;
-        sh.found_count = i == 0 ? cnt0 : cnt[i > 0 ? i - 1 : 0];
-        sh.found_mass = i == 0 ? mass0 : mass[i > 0 ? i - 1 : 0];
-        sh.best = c;
+    double target = f.k;
+    bool here = cnt0 < f.k && cnt1 >= f.k;  // among this thread's bins?
+    if (stage == 1) {
+      target = f.p * zk;
+      here = mass0 < target && mass1 >= target;
+    } else if (stage == 2) {
+      target = fmin(fmax(floor(lead - log_f64(f.minp) * kBinScale), 0.0), kBins - 1.0);
+      here = (int)target / kOwn == tid;
+    } else if (stage == 3) {
+      target = f.u * zn;
+      here = mass0 <= target && mass1 > target;
+    }
+    if (here) {
+      int at = kOwn * tid;
+      for (; at < kOwn * tid + kOwn - 1; ++at) {
+        const double x = stage == 0 ? (double)sh.bin_count[at] : (stage == 2 ? (double)at : sh.bin_mass[at]);
+        if (stage == 3 ? x > target : x >= target) break;
       }
-      earlier = here;
+      atomicMin(&sh.found, at);  // (by rounding, running weights may pass a target twice)
     }
     if (tid == 0) sh.count = sh.nhits = 0;
     __syncthreads();
-    const int bin = sh.found, before = sh.found_count, n = sh.best - before;
-    const double mass_before = sh.found_mass;
+    const int bin = sh.found, before = bin ? sh.bin_count[bin - 1] : 0, n = sh.bin_count[bin] - before;
+    const double mass_before = bin ? sh.bin_mass[bin - 1] : 0.0;
     if (n > kCap) return r;
     // the bin's tokens; bounds in logits, with a margin for their rounding, pass over most others
     const double up = ref - (double)bin * inv_scale, down = up - inv_scale;
@@ -636,30 +699,56 @@ __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f,
     if (sh.nhits > kParts * kThreads / 4) collect_row<F32>(row, lo, hi, keep_it);
     else collect_hits<F32>(row, ev, ei, lo, hi, keep_it);
     __syncthreads();
-    sort_candidates(n);
-    weigh(n, top, f.inv_t);
-    if (stage == 0) {
-      const int j = f.k - before;
-      if (j <= n) {  // (else fewer than k tokens are not masked: all of them)
-        keep = f.k;
-        zk = zn = mass_before + sh.cum[j - 1];
+    // sums of weights before the border are those of the bins before and of the bin's own tokens
+    int last = -1;    // the last of the bin's tokens that is kept
+    double sum = 0;   // their weight up to it
+    uint64_t token = 0;
+    const int limit = min(n, keep - before);  // tokens of the bin that a draw may take
+    const bool few = n <= 64;
+    if (few) {
+      if (tid < 64) {
+        const Few c = order_few(n, top, f.inv_t);
+        const double t = target - mass_before;
+        if (stage == 0) last = f.k - before <= n ? f.k - before - 1 : -1;
+        else if (stage == 1) last = min(lanes_below(n, t, false, c), n - 1);
+        else if (stage == 2) last = __popcll(__ballot(tid < n && c.w >= f.minp)) - 1;
+        else last = min(lanes_below(n, t, true, c), limit - 1);
+        sum = __shfl(c.cum, max(last, 0), 64);
+        token = __shfl(c.c, max(last, 0), 64);
+        if (tid == 0) {
+          sh.few_keep = last;
+          sh.few_mass = sum;
+          sh.few_token = token;
+        }
       }
-    } else if (stage == 1) {
-      const int m = min(count_below(n, target - mass_before, false), n - 1);
-      if (before + m + 1 < keep) {
-        keep = before + m + 1;
-        zn = mass_before + (m >= 0 ? sh.cum[m] : 0.0);
-      }
-    } else if (stage == 2) {
-      const int m = count_heavy(n, f.minp, top, f.inv_t);
-      if (before + m < keep) {
-        keep = max(before + m, 1);
-        zn = fmax(mass_before + (m > 0 ? sh.cum[m - 1] : 0.0), 1.0);
-      }
+      __syncthreads();
+      last = sh.few_keep;
+      sum = sh.few_mass;
+      token = sh.few_token;
     } else {
-      const int m = min(min(count_below(n, target - mass_before, true), n - 1), keep - 1 - before);
-      if (m >= 0) r = Answer{sh.cand[m], zn, true};
+      sort_candidates(n);
+      weigh(n, top, f.inv_t);
+      const double t = target - mass_before;
+      if (stage == 0) last = f.k - before <= n ? f.k - before - 1 : -1;
+      else if (stage == 1) last = min(count_below(n, t, false), n - 1);
+      else if (stage == 2) last = count_heavy(n, f.minp, top, f.inv_t) - 1;
+      else last = min(count_below(n, t, true), limit - 1);
+      sum = sh.cum[max(last, 0)];
+      token = sh.cand[max(last, 0)];
     }
+    sum = mass_before + (last >= 0 ? sum : 0.0);
+    if (stage == 0) {
+      if (last >= 0) {  // (else fewer than k tokens are not masked: all of them)
+        keep = f.k;
+        zk = zn = sum;
+      }
+    } else if (stage == 3) {
+      if (last >= 0) r = Answer{token, zn, true};
+    } else if (before + last + 1 < keep) {
+      keep = max(before + last + 1, 1);
+      zn = stage == 2 ? fmax(sum, 1.0) : sum;
+    }
+    if (tid == 0) sh.found = kBins - 1;
     __syncthreads();
   }
   return r;
@@ -794,7 +883,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
       tau = kNegInf;
       if (p >= 1.0 && minp > 0.0) {
         // every token that min_p keeps (and a margin for the rounding of this bound)
-        const float t = (float)((double)top + log(minp) / inv_t);
+        const float t = (float)((double)top + log_f64(minp) / inv_t);
         tau = top < __builtin_inff() ? t - fabsf(t) * 1e-5f - 1e-30f : top;
       }
     }
@@ -812,6 +901,17 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
           atomicMin(&sh.best, (int)(0xFFFFFFFFu - (unsigned)sh.cand[j]));
         __syncthreads();
         r = Answer{composite(top, sh.best), 1.0, true};
+      } else if (n <= 64) {
+        if (tid >= 64) return;
+        const Few c = order_few(n, top, inv_t);
+        const int kk = min(k, n);
+        int keep = kk;
+        if (p < 1.0) keep = min(lanes_below(kk, p * __shfl(c.cum, kk - 1, 64), false, c) + 1, kk);
+        if (minp > 0.0) keep = min(keep, __popcll(__ballot(lane < n && c.w >= minp)));
+        keep = max(keep, 1);
+        const double zn = __shfl(c.cum, keep - 1, 64);
+        const int j = lanes_below(keep, u * zn, true, c);
+        r = Answer{(uint64_t)__shfl((unsigned long long)c.c, min(j, keep - 1), 64), zn, true};
       } else {
         sort_candidates(n);
         weigh(n, top, inv_t);
@@ -845,7 +945,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
   if (tid == 0) {
     a.tokens[b] = (int)(0xFFFFFFFFu - (unsigned)r.token);
     if (a.logprob)
-      a.logprob[b] = greedy ? 0.0f : (float)(log_weight(logit_of(r.token), top, inv_t) - log(r.kept));
+      a.logprob[b] = greedy ? 0.0f : (float)(log_weight(logit_of(r.token), top, inv_t) - log_f64(r.kept));
   }
 }
 
