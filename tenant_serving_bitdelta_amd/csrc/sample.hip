@@ -43,7 +43,7 @@ struct Shared {
   uint64_t cand[kCap];
   double cum[kCap];
   union {
-    unsigned long long bins[kBins];
+    unsigned long long bins[kBins + 64];  // tallies; the last 64, one a lane, are not used
     double bin_mass[kBins];  // running weights, once the tallies have been read
   };
   int bin_count[kBins];  // running counts
@@ -141,25 +141,28 @@ __device__ __forceinline__ double weight(float l, float top, double inv_t) {
   return l == kNegInf ? 0.0 : exp_f64(log_weight(l, top, inv_t));
 }
 
-// The bins.  A logit's place is (ref - l) * 64 / T, kept as a fixed-point number: 12 bits of bin, 28
-// of the place within it.  Never less for a smaller logit; what lies beyond the bins counts as the
-// last one's.  One fused product and sum with an offset of 1.5 * 2^24 leaves place * 2^28 in the
-// low bits.
+// The bins.  A logit's place is (ref - l) * 64 / T, kept as a fixed-point number: the bin, and 32
+// bits of the place within it.  Never less for a smaller logit; what lies beyond the bins counts as
+// the last one's.  One fused product and sum in fp64 with an offset of 1.5 * 2^20 leaves the bin in
+// the low bits of the upper half, the place within it in the lower half.
 //
 // A token at place b + 64 x of bin b weighs e^(-b / 64) (1 - y), y = 1 - e^-x < 2^-6.  A bin's
 // tally is one 64-bit integer, count * 2^low + sum of y in units: additions of integers do not
-// depend on their order.  y is computed in fp32, so a weight is off by about 1e-9 of itself at
-// most; these errors average out over a sum.
+// depend on their order.  y is a cubic in fp32 (x - x^2 / 2 + x^3 / 6 - x^4 / 24 with the last term
+// replaced by the cubic nearest to it over [0, 2^-6]), so a weight is off by about 1e-9 of itself
+// at most; these errors average out over a sum.
+constexpr double kOffset = 1572864.0;
+constexpr unsigned kOffsetHigh = 0x41380000u;  // its upper half
 struct Bins {
   double offset, scale;  // of the place
-  int low;               // bits below the count
-  float units;           // units of y in 1, a power of two
+  int low;               // bits below the count, at least 42
+  float units;           // units of y in 1, a power of two up to 2^36: y in units fits 32 bits
   double unit;           // 1 / units
-  float c1, c2, c3, c4;  // y in units as a polynomial of the 28 bits
+  float c1, c2, c3;      // y in units as a polynomial of the 32 bits
   // false: places do not fit (T is so small that only the largest logit counts)
   __device__ __forceinline__ bool begin_at(double ref) {
-    offset = ref * scale + 25165824.0;
-    return fabs(ref * scale) < 4194304.0;
+    offset = ref * scale + kOffset;
+    return fabs(ref * scale) < 1073741824.0;
   }
   __device__ __forceinline__ Bins(int vocab, double inv_t) {
     scale = inv_t * kBinScale;
@@ -168,23 +171,23 @@ struct Bins {
     low = 63 - cb;
     units = __builtin_ldexpf(1.0f, min(low - cb + 6, 36));
     unit = 1.0 / (double)units;
-    const float x1 = 1.0f / (kBinScale * 268435456.0f);  // 2^-34
-    c1 = x1 * units;
-    c2 = -0.5f * x1 * c1;
-    c3 = (-1.0f / 3.0f) * x1 * c2;
-    c4 = -0.25f * x1 * c3;
+    constexpr double a = 1.0 / kBinScale, x1 = a / 4294967296.0;  // 2^-6, and x of the lowest bit
+    c1 = (float)((1.0 - a * a * a / 96.0) * x1) * units;
+    c2 = (float)((-0.5 + a * a * (1.25 / 24.0)) * x1 * x1) * units;
+    c3 = (float)((1.0 / 6.0 - a / 12.0) * x1 * x1 * x1) * units;
   }
+  // bin (or more than that, where it is beyond the bins) * 2^32 + place within it
   __device__ __forceinline__ uint64_t place(float l) const {
-    const double end = 25165824.0 + kBins - 0.0625;
-    return (uint64_t)__double_as_longlong(fmin(__builtin_fma(-(double)l, scale, offset), end));
+    const uint64_t x = (uint64_t)__double_as_longlong(__builtin_fma(-(double)l, scale, offset));
+    return x - ((uint64_t)kOffsetHigh << 32);
   }
-  __device__ __forceinline__ static int bin(uint64_t place) {
-    return (int)((unsigned)(place >> 28) & (kBins - 1));
+  __device__ __forceinline__ static unsigned bin(uint64_t place) {
+    return min((unsigned)(place >> 32), (unsigned)kBins - 1);
   }
   __device__ __forceinline__ unsigned long long tally(uint64_t place) const {
-    const float f = (float)((unsigned)place & 0xFFFFFFFu);
-    const float y = f * __builtin_fmaf(f, __builtin_fmaf(f, __builtin_fmaf(f, c4, c3), c2), c1);
-    return (1ull << low) + (unsigned)(y + 0.5f);
+    const float f = (float)(unsigned)place;
+    const float y = __builtin_fmaf(f, __builtin_fmaf(f, __builtin_fmaf(f, c3, c2), c1), 0.5f);
+    return (unsigned long long)(1u << (low - 32)) << 32 | (unsigned)y;
   }
   __device__ __forceinline__ int count(unsigned long long t) const { return (int)(t >> low); }
   // of a bin whose upper logit weighs 1
@@ -529,8 +532,9 @@ __device__ __noinline__ Few order_few(int n, float top, double inv_t) {
   const int lane = threadIdx.x & 63;
   uint64_t c = lane < n ? sh.cand[lane] : 0;
   int rank = 0;  // tokens before it
-#pragma unroll 4
-  for (int j = 0; j < n; ++j) {
+#pragma unroll
+  for (int j = 0; j < 64; ++j) {  // (the lanes past n hold 0, which is before no token)
+    if (j % 16 == 0 && j >= n) break;
     const uint64_t lo = (unsigned)__builtin_amdgcn_readlane((int)c, j);
     const uint64_t hi = (unsigned)__builtin_amdgcn_readlane((int)(c >> 32), j);
     rank += (hi << 32 | lo) > c;
@@ -626,8 +630,8 @@ __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f,
                                           const Bins& bins, const float* part, float ev, int ei) {
   constexpr int kOwn = kBins / kThreads;
   const int tid = threadIdx.x;
-  const double inv_scale = 1.0 / bins.scale, ref = (bins.offset - 25165824.0) * inv_scale;
-  const double lead = (double)(bins.place(top) & 0xFFFFFFFFFFull) * (1.0 / 268435456.0);  // of the largest
+  const double inv_scale = 1.0 / bins.scale, ref = (bins.offset - kOffset) * inv_scale;
+  const double lead = (double)bins.place(top) * (1.0 / 4294967296.0);  // of the largest
   // running counts and weights (of the largest logit: 1) before and after this thread's bins
   int cnt0 = 0, cnt1 = 0;
   double mass0 = 0, mass1 = 0;
@@ -693,7 +697,7 @@ __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f,
     const double up = ref - (double)bin * inv_scale, down = up - inv_scale;
     const double slack = 1e-6 * (fabs(up) + fabs(down)) + 1e-3 * inv_scale;
     const float hi = (float)(up + slack), lo = bin == kBins - 1 ? kNegInf : (float)(down - slack);
-    auto keep_it = [&](float l) { return Bins::bin(bins.place(l)) == bin; };
+    auto keep_it = [&](float l) { return (int)Bins::bin(bins.place(l)) == bin; };
     list_hits(part, lo);
     __syncthreads();
     if (sh.nhits > kParts * kThreads / 4) collect_row<F32>(row, lo, hi, keep_it);
@@ -797,11 +801,12 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
   };
   // a logit beyond the bins (many, if T is small) is counted by its thread and added at the end
   int beyond = 0;
-  auto tally_one = [&](float l) {  // (not for -inf and NaN)
+  auto tally_one = [&](float l) {
+    // (no branch: what lies beyond goes to a place of the lane's own)
     const uint64_t at = bins.place(l);
-    const int bin = Bins::bin(at);
-    if (bin < kBins - 1) atomicAdd(&sh.bins[bin], bins.tally(at));
-    else if (l > kNegInf) ++beyond;
+    const bool in = (unsigned)(at >> 32) < kBins - 1;
+    atomicAdd(&sh.bins[in ? (unsigned)(at >> 32) : kBins + lane], bins.tally(at));
+    beyond += (int)(!in & (l > kNegInf));
   };
   auto tally_batch = [&](const u32x4* r, int i0) {
 #pragma unroll
@@ -928,7 +933,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
   }
   const Filters f = {greedy ? 1 : k, vocab, greedy ? 2.0 : p, greedy ? 0.0 : minp, u, inv_t};
   if (!r.found && vocab <= kMaxBinVocab && top < __builtin_inff()) {
-    if (!bins_ready || __builtin_fma(-(double)top, bins.scale, bins.offset) < 25165824.0) {
+    if (!bins_ready || __builtin_fma(-(double)top, bins.scale, bins.offset) < kOffset) {
       // too many tokens for the first way, or bins that began too low: tally from the top
       __syncthreads();
       for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = 0;
