@@ -90,11 +90,16 @@ __host__ __device__ __forceinline__ KeyList window_keys(const int32_t* row, int 
 __host__ __device__ __forceinline__ int split_workers(int64_t total, int workers) {
   return total < workers ? (int)total : workers;
 }
+// a / b of values that are not negative; 64-bit divisions cost hundreds of instructions
+__host__ __device__ __forceinline__ int64_t split_quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
 __host__ __device__ __forceinline__ int64_t split_begin(int64_t w, int64_t total, int workers) {
-  return w * total / workers;
+  return split_quotient(w * total, workers);
 }
 __host__ __device__ __forceinline__ int split_owner(int64_t step, int64_t total, int workers) {
-  return (int)(((step + 1) * workers - 1) / total);
+  return (int)split_quotient((step + 1) * workers - 1, total);
 }
 
 struct AttendArgs {

@@ -1184,11 +1184,8 @@ __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a)
   const int tpt = kTileRows / a.group;
   constexpr int kQ = D / 4, kWays = 64 / kQ;  // lanes of a row, pieces side by side
   const int lane = threadIdx.x & 63;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t per = (int64_t)a.max_q * a.heads;
-  if (id >= a.batch * per) return;
-  const int b = (int)(id / per);
-  const int rest = (int)(id - b * per);
+  const int rest = blockIdx.x * 4 + (threadIdx.x >> 6), b = blockIdx.y;
+  if (rest >= a.max_q * a.heads) return;
   const int tq = rest / a.heads, hh = rest - tq * a.heads;
   const int h = hh / a.group;
   const RowUnit u = row_unit(a, b);
@@ -1205,36 +1202,23 @@ __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a)
     ot = ot * f0 + po * f1;
     mx = mn;
   };
-  // the pieces of workers w0 .. w1, row `row` of slots of `rows`, four loads in flight
-  auto add_pieces = [&](int w0, int w1, int64_t unit, int rows, int row, const float* ml, const float* o) {
-    for (int w = w0 + way; w <= w1; w += 4 * kWays) {
-      f32x2 pm[4];
-      f32x4 po[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t at = (min(w + i * kWays, w1) + unit) * rows + row;
-        pm[i] = *reinterpret_cast<const f32x2*>(ml + at * 2);
-        po[i] = *reinterpret_cast<const f32x4*>(o + at * D + 4 * d4);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (w + i * kWays <= w1) add(pm[i][0], pm[i][1], po[i]);
-    }
-  };
-  // own rows
+  // own pieces: of workers own_w .. own_w + own_n - 1
+  int own_n = 0;
+  int64_t own_at = 0;  // the first one's row
   {
-    const int row = tq * a.group + hh - h * a.group;
     const int64_t total = (int64_t)a.scan[a.batch] * a.kv_heads;
     const int steps = a.scan[b + 1] - a.scan[b];
     if (steps > 0) {
       const int64_t x0 = (int64_t)a.scan[b] * a.kv_heads + (int64_t)h * steps;
       const int workers = split_workers(total, a.workers);
       const int w0 = split_owner(x0, total, workers);
-      const int w1 = split_owner(x0 + steps - 1, total, workers);
-      add_pieces(w0, w1, (int64_t)b * a.kv_heads + h, a.rows, row, a.part_ml, a.part_o);
+      own_n = split_owner(x0 + steps - 1, total, workers) + 1 - w0;
+      own_at = (w0 + (int64_t)b * a.kv_heads + h) * a.rows + tq * a.group + hh - h * a.group;
     }
   }
-  // the prefix
+  // the prefix's
+  int pre_n = 0, pre_all = 0;  // workers, pieces: two per worker if the unit is halved
+  int64_t pre_at = 0;
   if (a.nseg > 0 && !a.row_prefix) {
     // the sequence's segment: how many segments end at or before it (at most 64: the last does not)
     const int sg = __popcll(__ballot(lane < a.nseg && a.seg_offsets[lane + 1] <= b));
@@ -1249,11 +1233,29 @@ __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a)
       const int64_t x0 = (int64_t)before * a.kv_heads + ((int64_t)h * tiles + rt) * steps;
       const int workers = split_workers(total, a.tile_workers);
       const int w0 = split_owner(x0, total, workers);
-      const int w1 = split_owner(x0 + steps - 1, total, workers);
-      const int64_t unit = (int64_t)ub * a.kv_heads + h * tiles + rt;
-      add_pieces(w0, w1, unit, kTileRows, row, a.tile_ml, a.tile_o);
-      if (halved(a, sg)) add_pieces(w0, w1, unit, kTileRows, row + kTileRows / 2, a.tile_ml, a.tile_o);
+      pre_n = split_owner(x0 + steps - 1, total, workers) + 1 - w0;
+      pre_all = halved(a, sg) ? 2 * pre_n : pre_n;
+      pre_at = (w0 + (int64_t)ub * a.kv_heads + h * tiles + rt) * kTileRows + row;
     }
+  }
+  // all pieces, four loads in flight
+  const int pieces = own_n + pre_all;
+  for (int i0 = way; i0 < pieces; i0 += 4 * kWays) {
+    f32x2 pm[4];
+    f32x4 po[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = min(i0 + i * kWays, pieces - 1), t = n - own_n;
+      const bool own = t < 0;
+      const int64_t at = own ? own_at + (int64_t)n * a.rows
+                             : pre_at + (int64_t)(t < pre_n ? t : t - pre_n) * kTileRows +
+                                   (t < pre_n ? 0 : kTileRows / 2);
+      pm[i] = *reinterpret_cast<const f32x2*>((own ? a.part_ml : a.tile_ml) + at * 2);
+      po[i] = *reinterpret_cast<const f32x4*>((own ? a.part_o : a.tile_o) + at * D + 4 * d4);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i0 + i * kWays < pieces) add(pm[i][0], pm[i][1], po[i]);
   }
   // the ways' sums
 #pragma unroll
@@ -1336,13 +1338,12 @@ hipError_t launch_attend_tiles(const AttendArgs& a, int dim, bool fp8, bool pref
 }
 
 hipError_t launch_attend_combine(const AttendArgs& a, int dim, hipStream_t stream) {
-  const int64_t waves = (int64_t)a.batch * a.max_q * a.heads;
-  const int blocks = (int)((waves + 3) / 4);
+  const dim3 grid((a.max_q * a.heads + 3) / 4, a.batch);  // at most 64 rows per kv head
   clear_stale_error();
   if (dim == 64)
-    hipLaunchKernelGGL(attend_combine_kernel<64>, dim3(blocks), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(attend_combine_kernel<64>, grid, dim3(256), 0, stream, a);
   else if (dim == 128)
-    hipLaunchKernelGGL(attend_combine_kernel<128>, dim3(blocks), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(attend_combine_kernel<128>, grid, dim3(256), 0, stream, a);
   else
     return hipErrorInvalidValue;
   return hipGetLastError();
