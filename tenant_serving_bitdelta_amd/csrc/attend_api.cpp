@@ -25,9 +25,29 @@ int row_workers(int columns, int64_t max_q, const bitdelta_kv_cache& c) {
 constexpr int kTileWorkers = 256;
 
 // A unit (sequence, kv head) whose key list is at most this many 128-key steps long is done by one
-// workgroup, without partials and the launch that joins them.  A step takes such a workgroup about
-// 2 us, the split and joined form of a short call about 14 us in all (9 steps: 22.9 against 14).
-constexpr int kDirectSteps = 6;
+// workgroup, without partials and the launch that joins them.  Few units: a step takes such a
+// workgroup about 2 us, a split and joined short call 20 us in all (8 kv heads, bf16, head_dim 128,
+// one sequence: 6 steps 18.0 against 20.7 us, 12 steps 30.6 against 21.0).  As many units as
+// workgroups at a time fill the machine unsplit (64 sequences: 12 steps 77 against 84 us); beyond
+// 12 steps one long list among short ones would be waited for.
+int direct_steps(int64_t units) { return units >= 512 ? 12 : 6; }
+
+// Are prefixes worth a launch of their own?  Reading a prefix once per segment instead of once per
+// sequence saves this many bytes, most of which the caches would have served; the tile launch and its
+// pieces cost about 10 us.  Measured with 8 kv heads, bf16, head_dim 128, prefixes read by the tile
+// against the row kernel: saving 67 MB 36.4 against 34.1 us, 101 MB 34.8 against 33.1, 201 MB 39.7
+// against 47.9, 503 MB 61.3 against 92.8.
+constexpr int64_t kShareBytes = int64_t(128) << 20;
+
+// Does a call with several rows a unit go to the tile kernel?  Beyond 64 rows always.  Below, a tile
+// workgroup has idle rows, but reads a unit's keys at the same speed whatever its rows are, one unit a
+// compute unit; the row kernel's time grows with its rows, and it splits a unit over workgroups.
+// Rows x units at 4096 keys, bf16, head_dim 128, row against tile kernel: 64 x 8 39 against 86 us,
+// 64 x 64 84 against 85, 64 x 256 286 against 100, 32 x 64 47 against 81, 32 x 256 136 against 100,
+// 16 x 256 108 against 99.
+bool tiles_for_rows(int64_t rows, int64_t units) {
+  return rows > 64 || (rows > 32 && units >= 64) || (rows > 16 && units >= 192);
+}
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -117,12 +137,13 @@ Plan plan_shared(int64_t batch, int32_t heads, const bitdelta_kv_cache& c, int32
   p.columns = columns_for(group);
   p.row_units = batch * c.kv_heads;
   const int64_t own = (int64_t)width * c.page_size, pre = (int64_t)pwidth * c.page_size;
-  int most = 0;
-  for (int i = 0; i < nseg; ++i) most = std::max(most, offs[i + 1] - offs[i]);
-  if (own + pre <= (int64_t)kDirectSteps * bd::kRowStep) {
+  int used = 0;  // segments with sequences
+  for (int i = 0; i < nseg; ++i) used += offs[i + 1] > offs[i];
+  const int64_t row_bytes = 2 * (int64_t)c.head_dim * (c.dtype == BITDELTA_KV_FP8 ? 1 : 2);
+  if (own + pre <= (int64_t)direct_steps(p.row_units) * bd::kRowStep) {
     p.kind = Kind::kRows;
-  } else if (most < 2 || pwidth == 0) {
-    p.kind = Kind::kRowsSplit;  // nothing is shared
+  } else if ((batch - used) * pre * c.kv_heads * row_bytes < kShareBytes) {
+    p.kind = Kind::kRowsSplit;
   } else {
     p.kind = Kind::kPrefixTiles;
     const int tpt = bd::kTileRows / group;
@@ -143,7 +164,7 @@ Plan plan_window(int32_t heads, const bitdelta_kv_cache& c, int32_t batch, int32
   Plan p{};
   const int group = heads / c.kv_heads;
   const int64_t rows = (int64_t)max_q * group;
-  if (rows > 64) {
+  if (tiles_for_rows(rows, (int64_t)batch * c.kv_heads)) {
     p.kind = Kind::kTiles;
     return p;
   }
@@ -153,7 +174,7 @@ Plan plan_window(int32_t heads, const bitdelta_kv_cache& c, int32_t batch, int32
   const int64_t keys = std::min<int64_t>((int64_t)width * c.page_size,
                                          (int64_t)window + max_q - 1 + sinks);
   const int64_t steps = (keys + bd::kRowStep - 1) / bd::kRowStep;
-  p.kind = steps <= kDirectSteps ? Kind::kRows : Kind::kRowsSplit;
+  p.kind = steps <= direct_steps(p.row_units) ? Kind::kRows : Kind::kRowsSplit;
   p.row_workers = std::min<int64_t>(row_workers(p.columns, max_q, c),
                                     std::max<int64_t>(1, p.row_units * steps));
   lay_out(&p, batch, c.head_dim);

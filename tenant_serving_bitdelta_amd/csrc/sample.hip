@@ -29,8 +29,9 @@ constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kParts = 4;       // a thread's vectors i, i + 4, ... make its part i
 constexpr int kCap = 4096;      // collected tokens at most
 constexpr int kPer = kCap / kThreads;  // of them per thread: kPer t .. kPer t + kPer - 1
-constexpr int kMaxK = 2048;     // top-k up to this goes by the maxima of the threads' parts
-constexpr int kFewK = 128;      // up to this many go by one maximum per thread, more by kParts
+// Top-k up to this goes by the maxima of the threads' parts, beyond by the bins (32 rows of 131072:
+// k = 50 19.7 against 35.9 us, 1000 34.4 against 39.4, 2000 58.8 against 45.5).
+constexpr int kMaxK = 1024;
 constexpr int kBins = 4096;     // of 1/kBinScale each in logit / T; the last takes the rest
 constexpr int kBinScale = 64;
 constexpr int kMaxBinVocab = 1 << 20;
@@ -860,19 +861,18 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
     float tau = top;
     if (!greedy && known_k) {
       // the k-th largest of the maxima, by bisection over their keys: every wave counts its own.  A
-      // bound that a few more reach will do.  All threads reach the least of their maxima.
-      const bool few = k <= kFewK;
+      // bound that a few more reach will do.  All threads reach the least of their
+      // largest ones.
       unsigned key[kParts];
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) key[q] = to_key(q == 0 && few ? mine : part[q]);
-      unsigned lo = k <= kThreads ? to_key(range.least) : 0, hi = to_key(top);
+      for (int q = 0; q < kParts; ++q) key[q] = to_key(part[q]);
+      unsigned lo = to_key(range.least), hi = to_key(top);  // kMaxK = kThreads maxima reach the least
 #pragma unroll 1
       for (int turn = 0; lo < hi; turn ^= 1) {
         const unsigned mid = lo + (hi - lo) / 2 + 1;
-        int n = __popcll(__ballot(key[0] >= mid));
-        if (!few)
+        int n = 0;
 #pragma unroll
-          for (int q = 1; q < kParts; ++q) n += __popcll(__ballot(key[q] >= mid));
+        for (int q = 0; q < kParts; ++q) n += __popcll(__ballot(key[q] >= mid));
         if (lane == 0) sh.wave_n[turn][tid >> 6] = n;
         __syncthreads();
         n = 0;

@@ -124,6 +124,36 @@ def test_shared(case):
     check(out, lse, shared_ref(qf, kf, vf, page, table, lens, ptable, plens, offs, sc, dim ** -0.5))
 
 
+def widen(ptable, sizes, page, hk, dim, kv):
+    """The prefix table with unused columns until sharing the prefixes is worth the tile kernel."""
+    saved = (sum(sizes) - sum(n > 0 for n in sizes)) * page * hk * 2 * dim * (1 if kv == "fp8" else 2)
+    more = np.full((len(ptable), -(-(130 << 20) // saved)), -1, dtype=np.int32)
+    return np.concatenate([ptable, more], axis=1)
+
+
+@pytest.mark.parametrize("case", [i for i, c in enumerate(SHARED) if max(c[0]) > 1])
+def test_shared_prefix_in_tiles(case):
+    sizes, plens, olens, heads, hk, dim, page, kv, extra, layout = SHARED[case]
+    rng = np.random.default_rng(50 + case)
+    n = sum(sizes)
+    lens = [olens[(i + 1) % len(olens)] for i in range(n)]
+    offs = np.concatenate([[0], np.cumsum(sizes)])
+    need = sum(-(-x // page) for x in lens + plens)
+    free = list(rng.permutation(need + 3))
+    table = tables(rng, lens, page, max(-(-max(lens) // page), 0) + extra, free)
+    ptable = tables(rng, plens, page, max(-(-max(plens) // page), 0), free)
+    if plens[0] > page:  # a page that is none
+        ptable[0, 1] = need + 3
+    ptable = widen(ptable, sizes, page, hk, dim, kv)
+    k, v, kf, vf, sc = make_cache(rng, need + 3, page, hk, dim, kv, layout)
+    q, qf = make_q(rng, n, heads, dim)
+    assert bd.attend_shared_workspace_bytes(k, heads, i32(table), i32(ptable), offs) > \
+        bd.attend_shared_workspace_bytes(k, heads, i32(table), i32(ptable[:, :1]), offs)
+    out, lse = bd.attend_shared(q, k, v, i32(table), i32(lens), i32(ptable), i32(plens), offs,
+                                k_scale=sc[0], v_scale=sc[1], return_lse=True)
+    check(out, lse, shared_ref(qf, kf, vf, page, table, lens, ptable, plens, offs, sc, dim ** -0.5))
+
+
 # new tokens per sequence, cached lengths, heads, kv heads, dim, page, type, window, sinks, extra
 # table width, cache layout
 WINDOW = [
@@ -319,6 +349,27 @@ def test_cache_beyond_32_bit_offsets():
                                [0, 3], sc, dim ** -0.5))
 
 
+@pytest.mark.parametrize("batch,hk,group,most", [(16, 4, 16, 3), (48, 4, 12, 2), (64, 8, 1, 1)])
+def test_window_kernel_choice(batch, hk, group, most):
+    """Many units of 33..64 rows, of 17..32 rows (tile kernel), and single tokens over lists of up
+    to 12 steps that no workgroup shares."""
+    rng = np.random.default_rng(batch)
+    page, width = 16, 12 if most > 1 else 90
+    q_lens = rng.integers(0 if most > 1 else 1, most + 1, batch).tolist()
+    q_lens[3] = most
+    lens = [int(rng.integers(n, 60)) for n in q_lens]
+    lens[3], lens[5] = (180 if most > 1 else 1400), q_lens[5]
+    need = sum(-(-x // page) for x in lens)
+    table = tables(rng, lens, page, width, list(rng.permutation(need)))
+    k, v, kf, vf, sc = make_cache(rng, need, page, hk, 64, "bf16")
+    q, qf = make_q(rng, sum(q_lens), hk * group, 64)
+    offs = i32(np.concatenate([[0], np.cumsum(q_lens)])) if most > 1 else None
+    window = 40 if most > 1 else 2000
+    out, lse = bd.attend_window(q, k, v, i32(table), i32(lens), window, 2, q_offsets=offs,
+                                max_q_len=most, return_lse=True)
+    check(out, lse, window_ref(qf, kf, vf, page, table, lens, q_lens, window, 2, sc, 0.125))
+
+
 def _graph_call(kind):
     rng = np.random.default_rng(11)
     if kind == "shared":
@@ -368,6 +419,35 @@ def test_graph_replays_and_other_streams(kind):
         torch.randn(1 << 20, device="cuda").sum().item()
         want = [x.clone() for x in call()]
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+
+
+def test_graph_replays_prefix_tiles():
+    rng = np.random.default_rng(12)
+    sizes, plens, page, hk, dim = [3, 20], [900, 400], 16, 2, 128
+    lens, offs = rng.integers(20, 300, 23).tolist(), [0, 3, 23]
+    free = list(rng.permutation(600))
+    table, ptable = tables(rng, lens, page, 50, free), tables(rng, plens, page, 60, free)
+    ptable = widen(ptable, sizes, page, hk, dim, "bf16")
+    k, v, kf, vf, sc = make_cache(rng, 600, page, hk, dim, "bf16")
+    q, _ = make_q(rng, 23, 16, dim)
+    t, l, pt, pl = i32(table), i32(lens), i32(ptable), i32(plens)
+    call = lambda: bd.attend_shared(q, k, v, t, l, pt, pl, offs, return_lse=True)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        res = call()
+    for i in range(4):
+        new, qf = make_q(rng, 23, 16, dim)
+        q.copy_(new)
+        l.sub_(3)
+        pl.sub_(70)
+        g.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in res]
+        torch.randn(1 << 20, device="cuda").sum().item()
+        assert all(torch.equal(a, b) for a, b in zip(got, call())), i
+    check(*got, shared_ref(qf, kf, vf, page, table, l.tolist(), ptable, pl.tolist(), offs, sc, dim ** -0.5))
 
 
 def test_binding_refusals():
