@@ -454,7 +454,7 @@ int64_t bitdelta_residency_used_bytes(bitdelta_residency* r);
  * call's queries see (beyond the lengths, before the window) is never used, NaN included.
  *
  * Limits (else UNSUPPORTED): head_dim 64 or 128, at most 64 query heads per kv head, 1024
- * sequences per call, 2^30 tokens per sequence.
+ * sequences per call, 2^30 tokens per sequence, page and token strides below 2^36 bytes.
  */
 #define BITDELTA_ATTEND_MAX_SEQS 1024
 #define BITDELTA_ATTEND_MAX_GROUP 64
@@ -560,7 +560,8 @@ size_t bitdelta_attend_window_workspace_bytes(int64_t tokens, int32_t heads,
  *   n_p = the smallest n with sum of the first n weights >= top_p * sum of the first k;
  *   n_m = the number of tokens with w_j >= min_p.
  * The token drawn is the first whose running sum of weights exceeds u times the sum of the first
- * n; logprob = ln(its weight / that sum).  Weights and sums are fp64.
+ * n; logprob = ln(its weight / that sum).  Weights are fp64 where a border between tokens is
+ * decided; the sum over a row without a top-k up to 1024 carries about 1e-9 of itself.
  *
  *   logits       [dev] logits_dtype (bitdelta_out_dtype: what bitdelta_matmul writes), row r at
  *                r * row_stride elements, vocab values; naturally aligned.

@@ -114,9 +114,9 @@ __device__ __forceinline__ u32x2 lds_read_tr(const unsigned char* p) {
 }
 
 // Copies straight from memory into LDS: 16 (4) bytes per lane, lane l's to the LDS address
-// `to` + 16 l (4 l), the same `to` for the wave.  In assembly because the compiler, which knows what the builtin does, puts
-// a wait for all copies before every transposed LDS read; here each step waits for its own
-// (wait_copies).  The instruction has no result register, and its address is read as it issues.
+// `to` + 16 l (4 l), the same `to` for the wave.  In assembly because the compiler, which knows what
+// the builtin does, puts a wait for all copies before every transposed LDS read; here each step waits
+// for its own (wait_copies).  The instruction has no result register, and its address is read as it issues.
 __device__ __forceinline__ unsigned lds_address(const void* p) {
   return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
@@ -278,7 +278,12 @@ __device__ __forceinline__ int scan_find(const int* scan, int count, int x) {
 // a key list.  Bound by reading the cache: each of a workgroup's 4 waves takes 32 keys of a
 // 128-key step on its own (no barrier in the loop), its K rows straight from memory into operand
 // registers (4 lanes take 64 bytes of a row) and its V rows through 8 KiB of its own LDS.  The
-// waves' sums meet at the end of a piece.
+// waves' sums meet at the end of a piece.  A split launch gives each of as many workgroups as fit at
+// a time an equal run of all units' steps, so unequal lengths leave none idle; more workgroups than
+// fit took a second turn (145 against 120 us for the own keys of 256 sequences, bf16, dim 128).
+// Measured: 64 sequences x 8 kv heads of 6.9k keys, e4m3, dim 128, 902 MB in 187 us, 4.8 TB/s, what a
+// large copy reaches; the 448 MB of own keys of 256 sequences, bf16, in 121 us, 3.7 TB/s; one
+// sequence's 4.3 MB 9 us, which is latency.
 // ---------------------------------------------------------------------------------------------
 template <int D, bool FP8, int NC>
 struct RowLoop {
@@ -623,8 +628,16 @@ void attend_row_kernel(const AttendArgs a) {
 // into LDS, three steps ahead, in four buffers; an e4m3 cache's rows pass through registers, which
 // widen them, one step ahead, in two.  Where a segment's rows fill at most half the waves (and the
 // cache is bf16), the other half takes a second key tile of the same step, and both halves' sums are
-// joined later with the pieces.  (Letting the second wave of each SIMD run a third of a step
-// late, its product with the values put off to the next step, measured 4% slower.)
+// joined later with the pieces (64 sequences of 14 segments: 70.0 -> 65.6 us).
+//
+// Bound by the chain of a step within a wave: scores (32 matrix instructions), softmax, values (32),
+// about 2.2 us, with two waves a SIMD to fill each other's gaps; vector and matrix instructions each
+// are busy 44% of the time.  Measured, bf16, dim 128, 64 heads on 8: 8192 new tokens of 16384, window
+// 4096, 1.10 TFLOP in 1130 us, 970 TFLOP/s (a large matrix product reaches 1184); 4 requests of up to
+// 2048 tokens, window 1024, 108 GFLOP in 167 us, 650 TFLOP/s.  Prefixes of 256 sequences in 14 segments: 53 GFLOP on 300 MB in 110 us.
+// Tried and slower or no faster: the second wave of each SIMD a third of a step late (4% slower),
+// wave priorities around the products (1291 against 1225 us), a barrier every second step (1225
+// against 1220), values with infinities or NaN multiplied key by key (spills, 5 times slower).
 // ---------------------------------------------------------------------------------------------
 // Byte offsets of a key's rows; bit 0 of k: there is no such key (offsets 0).
 struct RowPlace {
@@ -1177,7 +1190,10 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
 }
 
 // ---------------------------------------------------------------------------------------------
-// Combine: one wave per query row adds the row's partials of both kernels, in a fixed order.
+// Combine: one wave per query row adds the row's partials of both kernels, in a fixed order: lanes of
+// 4 dims each, 64 / (dim / 4) pieces side by side, four loads each in flight.  Bound by finding the
+// pieces (divisions) and the loads' latency: 16384 rows of 3 to 5 pieces 18 us, 64 rows of 96 4 us.  Two
+// rows a wave took 15.6 us for the former, but 6.1 for the latter.
 // ---------------------------------------------------------------------------------------------
 template <int D>
 __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a) {

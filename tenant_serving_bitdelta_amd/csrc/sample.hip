@@ -7,7 +7,7 @@
 // the first whose running sum of weights exceeds u times the sum of the first n.
 //
 // Only a prefix of the order is ever needed.  A workgroup reads its row once and keeps, per
-// thread, the largest value of each of 8 parts.  The k-th largest of the threads' maxima is a
+// thread, the largest value of each of 4 parts.  The k-th largest of the parts' maxima is a
 // bound that at least k tokens reach and few more do: the parts whose maximum reaches it are read
 // again and the tokens at or above it collected, ordered, weighed and summed.  Weights and sums
 // are fp64, so that a draw next to a border between two tokens falls on the side where the
@@ -15,10 +15,19 @@
 //
 // Where no top-k says how many tokens to collect (top-p alone, or no filter at all), the reading
 // instead counts and weighs the tokens in bins of 1/64 in (l_0 - l) / T, which gives the row's
-// weight and confines each border (top-p, min-p, the draw) to a bin or few; the tokens of those bins
-// are collected, and the borders are resolved as before.  Where even that collects too many
-// (thousands of equal logits), the borders are found by bisection over (logit, index), one reading
-// per step.
+// weight (to about 1e-9 of it) and confines each border (top-k, top-p, min-p, the draw) to a bin;
+// the tokens of that bin are collected, and the border is resolved as before.  Where even that
+// collects too many (thousands of equal logits), the borders are found by bisection over (logit,
+// index), one reading per step.
+//
+// What bounds it.  One workgroup a row: the rows are few (a decode batch), a row is small (512 KiB)
+// and a second launch to join parts of rows costs as much as a row's reading.  A row of 131072 fp32
+// logits: greedy 8 us (6.5 of them the reading, the rate of one compute unit), top-k 50 11, top-k
+// 1000 27, top-p 0.9 29 (18 the reading with its tallies: vector instructions and LDS atomics), no
+// filter 50 (13 of them reading the row again for a bin of thousands).  256 such rows with mixed
+// settings, 134 MB: 64 us, 2.1 TB/s; 64 x 128000 bf16, top-k 50 with top-p: 16 us.
+// Histograms by LDS atomics in the first reading without the maxima, every weight in fp64, took 158 us
+// a row and more.
 #include "bd_internal.h"
 #include "sample.h"
 
@@ -30,7 +39,7 @@ constexpr int kParts = 4;       // a thread's vectors i, i + 4, ... make its par
 constexpr int kCap = 4096;      // collected tokens at most
 constexpr int kPer = kCap / kThreads;  // of them per thread: kPer t .. kPer t + kPer - 1
 // Top-k up to this goes by the maxima of the threads' parts, beyond by the bins (32 rows of 131072:
-// k = 50 19.7 against 35.9 us, 1000 34.4 against 39.4, 2000 58.8 against 45.5).
+// k = 200 24.9 against 36.5 us, 1000 34.7 against 39.4, 2000 59.0 against 45.5).
 constexpr int kMaxK = 1024;
 constexpr int kBins = 4096;     // of 1/kBinScale each in logit / T; the last takes the rest
 constexpr int kBinScale = 64;
@@ -401,9 +410,10 @@ __device__ __forceinline__ void list_hits(const float* part, float lo) {
 }
 
 // Sorts sh.cand[0 .. n) in descending order (all threads).  Up to 256 tokens by rank, the number of
-// greater ones, which all waves count (each a slice of the comparisons).  More: kThreads buckets of
-// equal width from the largest logit down to the least, and the rank within the bucket; a bitonic
-// network where a bucket gets too many for that.
+// greater ones, which all waves count (each a slice of the comparisons; 100 tokens 22.3 us a call
+// against 24.8 by buckets, 200 24.7 against 26.1).  More: kThreads buckets of equal width from the
+// largest logit down to the least, and the rank within the bucket; a bitonic network where a bucket
+// gets too many for that.
 __device__ __noinline__ void sort_candidates(int n) {
   const int tid = threadIdx.x;
   sh.bucket[tid] = 0;
@@ -525,6 +535,7 @@ __device__ __noinline__ int count_heavy(int n, double m, float top, double inv_t
 }
 
 // ---- up to 64 collected tokens: one wave orders and weighs them, a lane each, with no barriers
+// (32 rows of 131072 with top-p 0.9: 31.7 us, 35.0 with the workgroup's sort and sums)
 struct Few {
   uint64_t c;     // the lane's token in the order; 0: none
   double w, cum;  // its weight, and the running sum
@@ -701,6 +712,8 @@ __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f,
     auto keep_it = [&](float l) { return (int)Bins::bin(bins.place(l)) == bin; };
     list_hits(part, lo);
     __syncthreads();
+    // (32 rows of 131072: top-p 0.9, few parts: hits 31.4, row 48.3 us; top-p 0.99 at T = 1.3, most
+    // parts: 84.4 against 68.2)
     if (sh.nhits > kParts * kThreads / 4) collect_row<F32>(row, lo, hi, keep_it);
     else collect_hits<F32>(row, ev, ei, lo, hi, keep_it);
     __syncthreads();
