@@ -235,7 +235,7 @@ def _temp(nbytes, device, stream, dtype_name="uint8"):
     those kernels still use it, so on another stream the block is recorded as in use there."""
     import torch
     dtype = getattr(torch, dtype_name)
-    n = max(int(nbytes), 1) // torch.empty((), dtype=dtype).element_size()
+    n = max(int(nbytes), 1) // dtype.itemsize
     t = torch.empty(max(n, 1), dtype=dtype, device=device)
     if stream is not None and int(stream) != torch.cuda.current_stream(device).cuda_stream:
         t.record_stream(torch.cuda.ExternalStream(int(stream), device=device))
@@ -855,22 +855,29 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=
         raise ValueError("logits must have contiguous rows")
     stride = int(logits.stride(0)) if rows > 1 else max(int(logits.stride(0)), vocab)
 
+    want = logits.shape[:1]
+
     def arg(t, dtype, what):
         if t is None:
             return None
-        _check_shape(t, (rows,), what)
-        return _dev(t, dtype, what)
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == want \
+                and t.is_contiguous():
+            return t.data_ptr()
+        _check_shape(t, want, what)
+        return _dev(t, str(dtype), what)
 
+    f32, i32 = torch.float32, torch.int32
     if out is None:
         out = torch.empty(rows, dtype=torch.int32, device=logits.device)
-        _on_stream(out, stream)
+        if stream is not None:
+            _on_stream(out, stream)
     if logprob is None and return_logprob:
         logprob = torch.empty(rows, dtype=torch.float32, device=logits.device)
-        _on_stream(logprob, stream)
+        if stream is not None:
+            _on_stream(logprob, stream)
     _check(_lib().bitdelta_sample(
         logits.data_ptr(), 0 if logits.dtype == torch.bfloat16 else 1, rows, vocab, stride,
-        arg(u, "torch.float32", "u"), arg(temperature, "torch.float32", "temperature"),
-        arg(top_k, "torch.int32", "top_k"), arg(top_p, "torch.float32", "top_p"),
-        arg(min_p, "torch.float32", "min_p"), arg(out, "torch.int32", "out"),
-        arg(logprob, "torch.float32", "logprob"), _raw_stream(stream, logits)), "bitdelta_sample")
+        arg(u, f32, "u"), arg(temperature, f32, "temperature"), arg(top_k, i32, "top_k"),
+        arg(top_p, f32, "top_p"), arg(min_p, f32, "min_p"), arg(out, i32, "out"),
+        arg(logprob, f32, "logprob"), _raw_stream(stream, logits)), "bitdelta_sample")
     return out if logprob is None else (out, logprob)

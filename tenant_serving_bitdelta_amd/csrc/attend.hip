@@ -635,7 +635,9 @@ void attend_row_kernel(const AttendArgs a) {
 // are busy 44% of the time.  Measured, bf16, dim 128, 64 heads on 8: 8192 new tokens of 16384, window
 // 4096, 1.10 TFLOP in 1130 us, 970 TFLOP/s (a large matrix product reaches 1184); 4 requests of up to
 // 2048 tokens, window 1024, 108 GFLOP in 167 us, 650 TFLOP/s.  Prefixes of 256 sequences in 14 segments: 53 GFLOP on 300 MB in 110 us.
-// Tried and slower or no faster: the second wave of each SIMD a third of a step late (4% slower),
+// Tried and slower or no faster: the next step's scores under this step's softmax (1133 in the
+// compiler's order, 1171 to 1211 interleaved by hand: vector and matrix cycles add up to 88%, so little
+// is left to overlap), the second wave of each SIMD a third of a step late (4% slower),
 // wave priorities around the products (1291 against 1225 us), a barrier every second step (1225
 // against 1220), values with infinities or NaN multiplied key by key (spills, 5 times slower).
 // ---------------------------------------------------------------------------------------------
