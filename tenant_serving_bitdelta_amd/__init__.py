@@ -703,7 +703,7 @@ def _attend_rows(q, cache, out, lse, return_lse, scale, stream):
         raise ValueError(f"q must be [tokens, heads, {dim}], not {tuple(shape)}")
     qs = q.stride()
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if stream is not None:
             _on_stream(out, stream)
     elif not out.is_cuda or out.dtype is not torch.bfloat16:
@@ -718,7 +718,7 @@ def _attend_rows(q, cache, out, lse, return_lse, scale, stream):
         _check_shape(lse, shape[:2], "lse")
         lptr = _dev(lse, "torch.float32", "lse")
     elif return_lse:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+        lse = torch.empty(shape[0], shape[1], dtype=torch.float32, device=q.device)
         if stream is not None:
             _on_stream(lse, stream)
         lptr = lse.data_ptr()
