@@ -109,6 +109,29 @@ def test_ties(vocab, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [8192, 9001, 70003])
+def test_thousands_of_nearly_equal_logits(vocab, dtype):
+    """More tokens around a border than are ever collected."""
+    rng = np.random.default_rng(vocab)
+    x = torch.zeros((12, vocab), device="cuda")
+    x[1, ::2] = -0.0
+    x[2:4] = torch.from_numpy(rng.integers(0, 2, size=(2, vocab)).astype(np.float32))
+    x[4:8] = torch.from_numpy(rng.normal(scale=0.004, size=(4, vocab)).astype(np.float32))
+    x[8:] = torch.from_numpy(rng.normal(loc=-20, scale=0.004, size=(4, vocab)).astype(np.float32))
+    x[9, 5], x[11, 77] = -10.0, -19.0
+    x[5, 100:200], x[6, ::3], x[10, 1::2] = float("nan"), -float("inf"), -float("inf")
+    x = x.to(dtype)
+    u = rng.random(12)
+    u[0], u[1], u[4], u[8] = 0.5, 1.0 - 2.0 ** -24, 1.0 - 2.0 ** -24, 0.0
+    check(x, u)
+    check(x, u, p=np.linspace(0.1, 0.9, 12))
+    check(x, u, k=rng.integers(1, 60, size=12))
+    check(x, u, k=rng.integers(1025, vocab, size=12), p=np.linspace(0.2, 1.0, 12))
+    check(x, u, m=np.full(12, 0.5), p=np.linspace(1.0, 0.3, 12))
+    check(x, u, t=np.linspace(0.01, 4, 12), m=np.full(12, 0.9))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_masked_infinite_and_nan_logits(dtype):
     rng = np.random.default_rng(3)
     x = peaked(rng, 12, 9001, torch.float32).cpu().numpy()
