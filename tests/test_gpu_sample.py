@@ -188,6 +188,19 @@ def test_strides_and_offsets(dtype):
             check(wide[:, off:off + n], rng.random(6), k=np.full(6, 40), p=np.full(6, 0.95))
 
 
+def test_rows_beyond_the_bins():
+    """More than 2^20 tokens: no bins; borders by bisection where there is no top-k."""
+    rng = np.random.default_rng(8)
+    vocab = (1 << 20) + 77
+    x = torch.from_numpy(rng.normal(scale=2.0, size=(3, vocab)).astype(np.float32)).cuda()
+    x[1, 1 << 20] = 14.0
+    x[2, ::2] = 0.25
+    u = rng.random(3)
+    check(x, u)
+    check(x, u, p=np.array([0.9, 0.5, 0.99]), k=np.array([0, 30, 5000]))
+    check(x, u, t=np.array([0.5, 0.0, 2.0]), m=np.array([0.1, 0.0, 0.01]))
+
+
 def test_rows_beyond_32_bit_offsets():
     vocab, rows = 200000, 11000  # 4.4 GB of bf16
     x = torch.zeros((rows, vocab), dtype=torch.bfloat16, device="cuda")
