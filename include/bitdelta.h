@@ -566,7 +566,8 @@ size_t bitdelta_attend_window_workspace_bytes(int64_t tokens, int32_t heads,
  *   logits       [dev] logits_dtype (bitdelta_out_dtype: what bitdelta_matmul writes), row r at
  *                r * row_stride elements, vocab values; naturally aligned.
  *   u            [dev] float32 [rows], uniform in [0, 1) (values outside count as the nearest).
- *   temperature  [dev] float32 [rows] or NULL (1); <= 0 or NaN: the first token of the order.
+ *   temperature  [dev] float32 [rows] or NULL (1); <= 0 or NaN: the first token of the order; +inf:
+ *                every token that is not masked (-inf) weighs 1.
  *   top_k        [dev] int32 [rows] or NULL; <= 0: off.
  *   top_p        [dev] float32 [rows] or NULL; >= 1 or NaN: off.
  *   min_p        [dev] float32 [rows] or NULL; <= 0 or NaN: off.

@@ -170,10 +170,11 @@ struct Bins {
   float units;           // units of y in 1, a power of two up to 2^36: y in units fits 32 bits
   double unit;           // 1 / units
   float c1, c2, c3;      // y in units as a polynomial of the 32 bits
-  // false: places do not fit (T is so small that only the largest logit counts)
+  // false: places do not fit (T is so small that only the largest logit counts), or there are none (T
+  // is infinite: all in one bin whose width in logits has no number)
   __device__ __forceinline__ bool begin_at(double ref) {
     offset = ref * scale + kOffset;
-    return fabs(ref * scale) < 1073741824.0;
+    return scale > 0.0 && fabs(ref * scale) < 1073741824.0;
   }
   __device__ __forceinline__ Bins(int vocab, double inv_t) {
     scale = inv_t * kBinScale;
@@ -726,7 +727,8 @@ __device__ __noinline__ Answer by_rank(const Row<F32> row, const Filters f, floa
 
 // The answer from the tallied bins: each border in turn (top-k,
 // top-p, min-p, the draw) lies in one bin, whose tokens are collected and sorted.  part: this
-// thread's maxima; ev, ei: its single element.  Not found: too many tokens in a bin.
+// thread's maxima; ev, ei: its single element.  Not found: too many tokens in a bin (or not those that
+// were tallied).
 template <bool F32>
 __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f, float top,
                                           const Bins& bins, const float* part, float ev, int ei) {
@@ -807,6 +809,9 @@ __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f,
     if (sh.nhits > kParts * kThreads / 4) collect_row<F32>(row, lo, hi, keep_it);
     else collect_hits<F32>(row, ev, ei, lo, hi, keep_it);
     __syncthreads();
+    // only what was collected is ordered: a token that was tallied but lies outside the bounds would
+    // leave a place that nobody wrote
+    if (sh.count != n) return r;
     // sums of weights before the border are those of the bins before and of the bin's own tokens
     int last = -1;    // the last of the bin's tokens that is kept
     double sum = 0;   // their weight up to it

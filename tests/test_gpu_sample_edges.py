@@ -1,0 +1,59 @@
+"""Token sampling at the ends of its settings, against the 64-bit form: tokens have to be equal, the
+log-probability is rounded to float32 once from fp64 sums (half a step, 2^-24 of it)."""
+import numpy as np
+import pytest
+
+import sample_ref as R
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+bd = pytest.importorskip("tenant_serving_bitdelta_amd")
+
+
+@pytest.fixture(autouse=True)
+def _announce(request):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    print(f"\n[gpu case] {request.node.nodeid}", flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def put(x, dtype=np.float32):
+    return None if x is None else torch.from_numpy(np.asarray(x, dtype=dtype)).cuda()
+
+
+def check(logits, u, t=None, k=None, p=None, m=None):
+    """Against the 64-bit form; an infinite temperature weighs every token that is not masked alike,
+    as 1e300 does in 64 bits."""
+    tok, lp = bd.sample(logits, put(u), put(t), put(k, np.int32), put(p), put(m), return_logprob=True)
+    tok, lp, x = tok.cpu().numpy(), lp.cpu().numpy(), logits.double().cpu().numpy()
+    pick = lambda a, r, d: d if a is None else float(np.float32(a[r]))  # noqa: E731
+    for r in range(x.shape[0]):
+        want, wl = R.sample_row(x[r], pick(u, r, 0.0), min(pick(t, r, 1.0), 1e300),
+                                0 if k is None else int(k[r]), pick(p, r, 1.0), pick(m, r, 0.0))
+        assert tok[r] == want, (r, tok[r], want)
+        assert abs(lp[r] - wl) <= 2.0 ** -24 * abs(wl) + 1e-12, (r, lp[r], wl)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab,allowed", [(7, 1.0), (1025, 1.0), (2048, 1.0), (4096, 1.0), (9001, 1.0),
+                                           (100003, 0.02), (100003, 0.0002)])
+def test_infinite_temperature_is_a_uniform_draw(vocab, allowed, dtype):
+    rng = np.random.default_rng(vocab)
+    rows = 8
+    x = rng.normal(scale=3.0, size=(rows, vocab)).astype(np.float32)
+    if allowed < 1:
+        x[rng.random(x.shape) >= allowed] = -np.inf
+        x[:, 17] = 2.0
+    x = torch.from_numpy(x).cuda().to(dtype)
+    u, t = rng.random(rows), np.full(rows, np.inf)
+    check(x, u, t)
+    check(x, u, t, p=np.linspace(0.1, 0.95, rows))
+    check(x, u, t, m=np.full(rows, 0.5))
+    check(x, u, t, m=np.full(rows, 0.5), p=np.linspace(0.95, 0.1, rows))
+    check(x, u, t, k=np.full(rows, 40))
+    check(x, u, t, k=np.full(rows, 1500), p=np.full(rows, 0.7))
+    check(x, u, np.where(np.arange(rows) % 2, np.inf, 0.8))
+    check(x, u, np.full(rows, 3e38))
