@@ -1020,6 +1020,7 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
         }
         if (s0 + 3 < s_end) copy_rows(s0 + 3);
       }
+      uint64_t odd = PREFIX ? 0 : __ballot(key_state & 2);  // keys whose values were taken out
       // does the wave see anything, does every row see everything?
       bool any = wave_live && valid != 0, all = valid == ~0ull;
       if constexpr (!PREFIX) {
@@ -1134,20 +1135,19 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
           for (int i = 0; i < kOut; ++i) o[i] = mfma32(vf[kb & 1][i], p[kb], o[i]);
         }
         if constexpr (!PREFIX) {
-          if (!all) {
-            for (uint64_t odd = __ballot(key_state & 2); odd; odd &= odd - 1) {
-              const int vp = base + __builtin_ctzll(odd);
-              const unsigned char* row_v = value_row(a.cache, kl, vp, h);
-              if (!row_v) continue;
-              const bool seen = sees(kl, pq, a.window, a.sinks, vp);
+          // (also where this wave's rows see all keys: the values were taken out for the whole tile)
+          for (; odd; odd &= odd - 1) {
+            const int vp = base + __builtin_ctzll(odd);
+            const unsigned char* row_v = value_row(a.cache, kl, vp, h);
+            if (!row_v) continue;
+            const bool seen = sees(kl, pq, a.window, a.sinks, vp);
 #pragma unroll
-              for (int i = 0; i < kOut; ++i)
+            for (int i = 0; i < kOut; ++i)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const float x = o[i][e];
-                  o[i][e] = seen ? x + odd_value<FP8>(row_v, 32 * i + 8 * (e >> 2) + 4 * hf + (e & 3)) : x;
-                }
-            }
+              for (int e = 0; e < 16; ++e) {
+                const float x = o[i][e];
+                o[i][e] = seen ? x + odd_value<FP8>(row_v, 32 * i + 8 * (e >> 2) + 4 * hf + (e & 3)) : x;
+              }
           }
         }
       }

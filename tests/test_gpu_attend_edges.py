@@ -1,0 +1,104 @@
+"""Paged attention on the GPU where values are not finite, against the plain 64-bit form, with the
+tolerances of test_gpu_attend.py."""
+import numpy as np
+import pytest
+
+import test_gpu_attend as A
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+bd = pytest.importorskip("tenant_serving_bitdelta_amd")
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(autouse=True)
+def _announce(request):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    print(f"\n[gpu case] {request.node.nodeid}", flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def setup(rng, q_lens, lens, heads, hk, dim=128, page=16, kv="bf16", extra=0):
+    need = sum(-(-x // page) for x in lens) + 1
+    table = A.tables(rng, lens, page, -(-max(lens) // page) + extra, list(rng.permutation(need)))
+    k, v, kf, vf, sc = A.make_cache(rng, need, page, hk, dim, kv)
+    q, qf = A.make_q(rng, sum(q_lens), heads, dim)
+    return table, k, v, kf, vf, sc, q, qf, A.i32(np.concatenate([[0], np.cumsum(q_lens)]))
+
+
+def poke(pages, page, slot, head, d, value):
+    """One stored value; e4m3 by its byte (all ones below the sign: NaN)."""
+    if pages.dtype == torch.float8_e4m3fn:
+        assert np.isnan(value)
+        pages.view(torch.uint8)[page, slot, head, d] = 0x7F
+    else:
+        pages[page, slot, head, d] = value
+
+
+# new tokens, cached lengths, heads, kv heads, dim, window: tiles of 256 and of 32 tokens where some
+# waves see all of an edge step's keys and others do not; a window whose left edge crosses tiles; the row
+# kernel with several tokens, in one piece and split
+SEEN = [
+    ([300], [300], 4, 4, 128, 4096),
+    ([200], [210], 16, 2, 128, 4096),
+    ([200], [210], 16, 2, 64, 4096),
+    ([280], [400], 3, 3, 64, 90),
+    ([130, 90], [130, 100], 8, 2, 128, 70),
+    ([4], [30], 8, 2, 128, 4096),
+    ([3, 2], [1900, 40], 8, 2, 64, 4096),
+    ([8, 5], [1900, 300], 8, 2, 128, 100),
+]
+
+
+@pytest.mark.parametrize("kv,value", [("bf16", NAN), ("bf16", INF), ("bf16", -INF), ("fp8", NAN)])
+@pytest.mark.parametrize("case", range(len(SEEN)))
+def test_window_value_that_is_not_finite_reaches_every_token_that_sees_it(case, kv, value):
+    q_lens, lens, heads, hk, dim, window = SEEN[case]
+    rng = np.random.default_rng(300 + case)
+    table, k, v, kf, vf, sc, q, qf, offs = setup(rng, q_lens, lens, heads, hk, dim, kv=kv)
+    at = {}  # sequence, kv head -> (key, dim of the value)
+    for b, (n, length) in enumerate(zip(q_lens, lens)):
+        for g in range(hk):
+            j = [length - n + min(10, n // 2), length - 1, max(length - n - 20, 0), length - n // 2][(b + g) % 4]
+            at[b, g] = j, int(rng.integers(dim))
+            poke(v, int(table[b, j // 16]), j % 16, g, at[b, g][1], value)
+    out, lse = bd.attend_window(q, k, v, A.i32(table), A.i32(lens), window, 0, q_offsets=offs,
+                                max_q_len=max(q_lens), k_scale=sc[0], v_scale=sc[1], return_lse=True)
+    o = out.double().cpu().numpy()
+    ref = A.window_ref(qf, kf, vf, 16, table, lens, q_lens, window, 0, sc, dim ** -0.5)
+    t = 0
+    for b, (n, length) in enumerate(zip(q_lens, lens)):
+        for pos in range(length - n, length):
+            hit = np.zeros((heads, dim), dtype=bool)
+            for g in range(hk):
+                j, d = at[b, g]
+                if j <= pos < j + window:
+                    hit[g * (heads // hk):(g + 1) * (heads // hk), d] = True
+            assert not np.isfinite(o[t][hit]).any(), (b, pos)
+            ro, mix, _ = ref[t]
+            ok = np.abs(o[t] - ro) <= A.BF16 * np.abs(ro) + (A.BF16 + A.SCORE) * mix
+            assert (ok | hit).all(), (b, pos, np.argwhere(~(ok | hit))[:4])
+            t += 1
+
+
+@pytest.mark.parametrize("q_lens,lens", [([1, 1], [40, 90]), ([1, 1], [40, 2000]), ([3, 2], [40, 2000]),
+                                         ([70, 40], [70, 300])])
+def test_window_unseen_e4m3_cache_is_never_used(q_lens, lens):
+    """NaN in every slot of an e4m3 cache that no query of the call sees changes nothing."""
+    rng = np.random.default_rng(21)
+    window, sinks = 30, 3
+    table, k, v, kf, vf, sc, q, qf, offs = setup(rng, q_lens, lens, 8, 2, kv="fp8", extra=2)
+    used = np.zeros(k.shape[:2], dtype=bool)
+    for b, n in enumerate(q_lens):
+        for j in range(lens[b]):
+            if j >= lens[b] - n - window + 1 or j < sinks:
+                used[table[b, j // 16], j % 16] = True
+    bad = torch.from_numpy(~used).cuda()
+    k.view(torch.uint8)[bad], v.view(torch.uint8)[bad] = 0x7F, 0xFF
+    out, lse = bd.attend_window(q, k, v, A.i32(table), A.i32(lens), window, sinks, q_offsets=offs,
+                                max_q_len=max(q_lens), k_scale=sc[0], v_scale=sc[1], return_lse=True)
+    A.check(out, lse, A.window_ref(qf, kf, vf, 16, table, lens, q_lens, window, sinks, sc, 128 ** -0.5))
