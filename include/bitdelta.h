@@ -532,8 +532,9 @@ size_t bitdelta_attend_shared_workspace_bytes(int64_t tokens, int32_t heads,
  *
  *   q_offsets   [dev] int32 [batch + 1], ascending, or NULL: one token per sequence (decode;
  *               then rows->tokens = batch and max_q_len = 1).
- *   max_q_len   [host] at least the longest chunk of the call; query rows beyond it, or outside
- *               [0, tokens), are not computed.
+ *   max_q_len   [host] at least the longest chunk of the call.  A chunk's query rows beyond its
+ *               first max_q_len, and those outside [0, tokens), are not computed (their out and lse
+ *               stay as they are); the others keep their positions.
  *   window      >= 1; sinks >= 0.
  *   workspace   as above, bitdelta_attend_window_workspace_bytes(...).
  * batch = 0 or tokens = 0 is a no-op.  Errors as bitdelta_attend_shared.

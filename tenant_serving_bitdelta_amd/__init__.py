@@ -801,7 +801,7 @@ def attend_window_workspace_bytes(k_pages, heads, table, tokens, max_q_len, wind
         window, sinks))
 
 
-def attend_window(q, k_pages, v_pages, table, lens, window, sinks=0, q_offsets=None, max_q_len=1,
+def attend_window(q, k_pages, v_pages, table, lens, window, sinks=0, q_offsets=None, max_q_len=None,
                   scale=None, k_scale=1.0, v_scale=1.0, out=None, lse=None, return_lse=False,
                   workspace=None, stream=None):
     """Causal attention of each sequence's last tokens over a paged cache, with a sliding window
@@ -810,13 +810,17 @@ def attend_window(q, k_pages, v_pages, table, lens, window, sinks=0, q_offsets=N
     among them as the last ones.
 
     ``q``: bf16 [tokens, heads, head_dim]; sequence b's rows are q_offsets[b] .. q_offsets[b + 1]
-    (int32 [batch + 1] on the device; None: one token per sequence), none longer than
-    ``max_q_len``.  Cache, tables, scales and results as for attend_shared."""
+    (int32 [batch + 1] on the device; None: one token per sequence).  ``max_q_len`` is at least the
+    longest chunk (None: 1 without q_offsets, else the number of tokens; the real length picks better
+    kernels); a chunk's rows beyond its first ``max_q_len`` are not computed.  Cache, tables, scales
+    and results as for attend_shared."""
     cache = _kv_cache(k_pages, v_pages, k_scale, v_scale)
     rows, out, lse = _attend_rows(q, cache, out, lse, return_lse, scale, stream)
     batch = lens.shape[0] if lens.dim() == 1 else -1
     tptr, width, lptr = _table(table, lens, batch, "table")
     optr = None
+    if max_q_len is None:
+        max_q_len = 1 if q_offsets is None else max(rows.tokens, 1)
     if q_offsets is not None:
         _check_shape(q_offsets, (batch + 1,), "q_offsets")
         optr = _dev(q_offsets, "torch.int32", "q_offsets")

@@ -83,6 +83,26 @@ __host__ __device__ __forceinline__ KeyList window_keys(const int32_t* row, int 
   return l;
 }
 
+// The query rows of a chunk that are computed: of the rows q0 .. q1 - 1 the first max_q, and of those
+// the ones in [0, tokens).  Row q1 - 1 is the token at position len - 1, whether it is computed or not.
+struct ChunkRows {
+  int first, count;
+  int p0;  // position of the first
+};
+__host__ __device__ __forceinline__ ChunkRows chunk_rows(int q0, int q1, int len, int max_q, int tokens) {
+  const int64_t limit = (int64_t)q0 + max_q;
+  const int first = q0 > 0 ? q0 : 0;
+  int64_t end = q1 < limit ? q1 : limit;
+  if (end > tokens) end = tokens;
+  ChunkRows c;
+  c.first = first;
+  c.count = end > first ? (int)(end - first) : 0;
+  // far below 0 (offsets that are none) every token is without keys, wherever it is
+  const int64_t p0 = (int64_t)len - ((int64_t)q1 - first);
+  c.p0 = p0 < -(1 << 30) ? -(1 << 30) : (int)(p0 < len ? p0 : len);
+  return c;
+}
+
 // Work split: `total` steps over `workers` workgroups, worker w taking steps
 // [w * total / workers, (w + 1) * total / workers).  Never more workers than steps, so that each
 // worker has a step, and a unit's pieces are those of all workers from its first step's owner to

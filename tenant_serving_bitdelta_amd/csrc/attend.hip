@@ -212,18 +212,18 @@ __device__ __forceinline__ RowUnit row_unit(const AttendArgs& a, int b, int len)
       u.keys.n = plen + len;
     }
   } else {
-    int q0 = b, nq = 1;
+    u.t0 = b;
+    u.nq = 1;
+    u.p0 = len - 1;
     if (a.q_offsets) {
-      q0 = a.q_offsets[b];
-      nq = a.q_offsets[b + 1] - q0;
-      nq = nq < 0 ? 0 : (nq > a.max_q ? a.max_q : nq);
-      if (q0 < 0 || q0 > a.tokens) nq = 0;
-      else if (nq > a.tokens - q0) nq = a.tokens - q0;
+      const ChunkRows c = chunk_rows(a.q_offsets[b], a.q_offsets[b + 1], len, a.max_q, a.tokens);
+      u.t0 = c.first;
+      u.nq = c.count;
+      u.p0 = c.p0;
     }
-    u.t0 = q0;
-    u.nq = nq;
-    u.p0 = len - nq;
-    u.keys = window_keys(row, a.width, len, u.p0, a.window, a.sinks);
+    // keys up to the last token: a unit of one token has no masks
+    const int end = u.p0 + u.nq;
+    u.keys = window_keys(row, a.width, end < 0 ? 0 : end, u.p0, a.window, a.sinks);
   }
   return u;
 }

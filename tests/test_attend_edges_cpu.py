@@ -1,0 +1,29 @@
+"""Paged attention without a GPU, at the ends of its arguments: the rows of a chunk that are computed,
+and refusals (the addresses are fake)."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+bd = pytest.importorskip("tenant_serving_bitdelta_amd")
+if not os.path.exists(bd.LIB_PATH):
+    pytest.skip("libbitdelta.so not built", allow_module_level=True)
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_rows_of_a_chunk(tmp_path):
+    hipcc = next((c for c in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc"))
+                  if c and os.path.exists(c)), None)
+    if hipcc is None:
+        pytest.skip("hipcc not available")
+    exe = str(tmp_path / "attend_chunk_check")
+    r = subprocess.run([hipcc, "-O1", "-std=c++17", "-Xarch_host", "-fsanitize=undefined", "-Xarch_host",
+                        "-fno-sanitize-recover=all", os.path.join(ROOT, "tests", "attend_chunk_check.cpp"),
+                        "-o", exe], capture_output=True, text=True, timeout=600)
+    if r.returncode != 0 and "sanitizer" in r.stderr.lower() and "not found" in r.stderr:
+        pytest.skip("sanitizer runtime not available")
+    assert r.returncode == 0, r.stderr[-4000:]
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", (r.stdout + r.stderr)[-4000:]

@@ -1,5 +1,5 @@
-"""Paged attention on the GPU where values are not finite, against the plain 64-bit form, with the
-tolerances of test_gpu_attend.py."""
+"""Paged attention on the GPU at the ends of its arguments and with values that are not finite, against
+the plain 64-bit form, with the tolerances of test_gpu_attend.py."""
 import numpy as np
 import pytest
 
@@ -102,3 +102,61 @@ def test_window_unseen_e4m3_cache_is_never_used(q_lens, lens):
     out, lse = bd.attend_window(q, k, v, A.i32(table), A.i32(lens), window, sinks, q_offsets=offs,
                                 max_q_len=max(q_lens), k_scale=sc[0], v_scale=sc[1], return_lse=True)
     A.check(out, lse, A.window_ref(qf, kf, vf, 16, table, lens, q_lens, window, sinks, sc, 128 ** -0.5))
+
+
+# new tokens, cached lengths, heads, kv heads, a chunk limit below the longest: single tokens, the row
+# kernel (one piece, split), the tile kernel
+CUT = [
+    ([5, 1, 3], [40, 30, 90], 8, 2, 1),
+    ([5, 1, 3], [1900, 30, 1300], 8, 2, 1),
+    ([7, 2, 9], [40, 30, 90], 8, 2, 3),
+    ([7, 2, 9], [1900, 2, 1300], 8, 2, 4),
+    ([150, 40], [300, 40], 8, 2, 100),
+    ([150, 40, 3], [149, 20, 3], 16, 1, 77),
+]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("case", range(len(CUT)))
+def test_rows_beyond_max_q_len_are_left_out_and_the_others_keep_their_places(case, kv):
+    q_lens, lens, heads, hk, most = CUT[case]
+    rng = np.random.default_rng(400 + case)
+    table, k, v, kf, vf, sc, q, qf, offs = setup(rng, q_lens, lens, heads, hk, kv=kv)
+    window, sinks = 60, 2
+    out = torch.full_like(q, 7.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    bd.attend_window(q, k, v, A.i32(table), A.i32(lens), window, sinks, q_offsets=offs, max_q_len=most,
+                     k_scale=sc[0], v_scale=sc[1], out=out, lse=lse)
+    ref = A.window_ref(qf, kf, vf, 16, table, lens, q_lens, window, sinks, sc, 128 ** -0.5)
+    done = np.concatenate([np.arange(n) < most for n in q_lens])
+    A.check(out[torch.from_numpy(done).cuda()], lse[torch.from_numpy(done).cuda()],
+            [r for r, d in zip(ref, done) if d])
+    left = torch.from_numpy(~done).cuda()
+    assert bool((out[left] == 7.0).all()) and bool((lse[left] == 7.0).all())
+
+
+@pytest.mark.parametrize("first,cut", [(0, 4), (-3, 0), (-2, 5)])
+@pytest.mark.parametrize("q_lens,lens", [([9, 8], [300, 100]), ([9, 8], [1900, 1300]), ([90, 80], [300, 100])])
+def test_rows_outside_the_tokens_are_left_out_and_the_others_keep_their_places(q_lens, lens, first, cut):
+    """Offsets that begin before row 0 or end past the last row."""
+    rng = np.random.default_rng(41)
+    table, k, v, kf, vf, sc, q, qf, _ = setup(rng, q_lens, lens, 8, 2)
+    total = sum(q_lens)
+    offs = np.concatenate([[0], np.cumsum(q_lens)]) + first
+    rows = slice(max(-first, 0), total - cut)  # of the whole list of tokens, those that are given
+    out, lse = bd.attend_window(q[rows].contiguous(), k, v, A.i32(table), A.i32(lens), 60, 2,
+                                q_offsets=A.i32(offs), max_q_len=max(q_lens), return_lse=True)
+    ref = A.window_ref(qf, kf, vf, 16, table, lens, q_lens, 60, 2, sc, 128 ** -0.5)
+    A.check(out, lse, ref[rows])
+
+
+@pytest.mark.parametrize("most", [None, 500])
+@pytest.mark.parametrize("q_lens,lens", [([1, 1], [40, 300]), ([3, 1, 0, 2], [40, 300, 5, 900]),
+                                         ([90, 33], [300, 40])])
+def test_max_q_len_above_the_longest_chunk(q_lens, lens, most):
+    """A limit that no chunk reaches; without one it is the number of rows."""
+    rng = np.random.default_rng(42)
+    table, k, v, kf, vf, sc, q, qf, offs = setup(rng, q_lens, lens, 8, 2)
+    kw = {} if most is None else {"max_q_len": most}
+    out, lse = bd.attend_window(q, k, v, A.i32(table), A.i32(lens), 60, 2, q_offsets=offs, return_lse=True, **kw)
+    A.check(out, lse, A.window_ref(qf, kf, vf, 16, table, lens, q_lens, 60, 2, sc, 128 ** -0.5))
