@@ -236,7 +236,7 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
     const int tpt = bd::kTileRows / a->group;
     // each sequence rounds its tokens up to whole tiles
     const int64_t tiles = std::min<int64_t>(a->tokens / tpt + a->batch,
-                                            (int64_t)a->batch * ((a->max_q + tpt - 1) / tpt));
+                                            a->batch * (((int64_t)a->max_q + tpt - 1) / tpt));
     return bd::status_of_hip(bd::launch_attend_tiles(*a, c.head_dim, fp8, false,
                                                      (int)(tiles * a->kv_heads), st));
   }

@@ -160,3 +160,14 @@ def test_max_q_len_above_the_longest_chunk(q_lens, lens, most):
     kw = {} if most is None else {"max_q_len": most}
     out, lse = bd.attend_window(q, k, v, A.i32(table), A.i32(lens), 60, 2, q_offsets=offs, return_lse=True, **kw)
     A.check(out, lse, A.window_ref(qf, kf, vf, 16, table, lens, q_lens, 60, 2, sc, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("q_lens,lens", [([1, 1], [40, 300]), ([3, 1, 0, 2], [40, 300, 5, 900]),
+                                         ([90, 33], [300, 40])])
+def test_max_q_len_of_no_limit(q_lens, lens):
+    """The largest limit there is."""
+    rng = np.random.default_rng(43)
+    table, k, v, kf, vf, sc, q, qf, offs = setup(rng, q_lens, lens, 8, 2)
+    out, lse = bd.attend_window(q, k, v, A.i32(table), A.i32(lens), 60, 2, q_offsets=offs,
+                                max_q_len=2 ** 31 - 1, return_lse=True)
+    A.check(out, lse, A.window_ref(qf, kf, vf, 16, table, lens, q_lens, 60, 2, sc, 128 ** -0.5))
