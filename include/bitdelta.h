@@ -454,7 +454,8 @@ int64_t bitdelta_residency_used_bytes(bitdelta_residency* r);
  * call's queries see (beyond the lengths, before the window) is never used, NaN included.
  *
  * Limits (else UNSUPPORTED): head_dim 64 or 128, at most 64 query heads per kv head, 1024
- * sequences per call, 2^30 tokens per sequence, page and token strides below 2^36 bytes.
+ * sequences per call, 2^30 tokens per sequence, 2^30 query rows (tokens x heads), 2^21 (sequence, kv
+ * head) pairs, page and token strides below 2^36 bytes.
  */
 #define BITDELTA_ATTEND_MAX_SEQS 1024
 #define BITDELTA_ATTEND_MAX_GROUP 64

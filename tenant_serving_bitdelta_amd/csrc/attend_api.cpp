@@ -15,6 +15,10 @@ bitdelta_status status_of_hip(hipError_t e);
 namespace {
 
 constexpr int64_t kMaxKeys = int64_t(1) << 30;  // positions of a key list stay far below 2^31
+// A launch holds fewer than 2^32 threads: 512 of each of at most 2^30 / 193 row tiles of a call's
+// tokens (a tile of 256 rows is filled to 193 at least) and one more tile of each (sequence, kv head).
+constexpr int64_t kMaxRows = int64_t(1) << 30;   // tokens x heads
+constexpr int64_t kMaxUnits = int64_t(1) << 21;  // sequences x kv heads
 
 // Workgroups of a split launch: as many as the 256 compute units hold at a time (more would start
 // when the first have ended, and take as long again), which their registers decide.
@@ -274,7 +278,8 @@ bool shared_sizes_ok(int64_t tokens, int32_t heads, const bitdelta_kv_cache* cac
   *s = check_cache(cache, heads);
   if (*s == BITDELTA_OK && (width < 0 || pwidth < 0)) *s = BITDELTA_ERR_INVALID_ARG;
   if (*s == BITDELTA_OK) *s = check_segments(tokens, offs, nseg);
-  if (*s == BITDELTA_OK && (tokens > BITDELTA_ATTEND_MAX_SEQS ||
+  if (*s == BITDELTA_OK && (tokens > BITDELTA_ATTEND_MAX_SEQS || tokens * heads > kMaxRows ||
+                            tokens * cache->kv_heads > kMaxUnits ||
                             ((int64_t)width + pwidth) * cache->page_size > kMaxKeys))
     *s = BITDELTA_ERR_UNSUPPORTED;
   return *s == BITDELTA_OK;
@@ -287,7 +292,7 @@ bitdelta_status check_window(int64_t tokens, int32_t heads, const bitdelta_kv_ca
   if (s != BITDELTA_OK) return s;
   if (batch < 0 || width < 0 || max_q < 1 || window < 1 || sinks < 0) return BITDELTA_ERR_INVALID_ARG;
   if (batch > BITDELTA_ATTEND_MAX_SEQS || (int64_t)width * cache->page_size > kMaxKeys ||
-      tokens * heads > (int64_t(1) << 30))
+      tokens * heads > kMaxRows || (int64_t)batch * cache->kv_heads > kMaxUnits)
     return BITDELTA_ERR_UNSUPPORTED;
   return BITDELTA_OK;
 }

@@ -6,6 +6,8 @@ import subprocess
 
 import pytest
 
+import test_attend_cpu as C
+
 bd = pytest.importorskip("tenant_serving_bitdelta_amd")
 if not os.path.exists(bd.LIB_PATH):
     pytest.skip("libbitdelta.so not built", allow_module_level=True)
@@ -27,3 +29,12 @@ def test_rows_of_a_chunk(tmp_path):
     assert r.returncode == 0, r.stderr[-4000:]
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", (r.stdout + r.stderr)[-4000:]
+
+
+@pytest.mark.parametrize("call", [C._shared, C._window])
+@pytest.mark.parametrize("tokens,heads,kv_heads", [(1024, 1 << 14, 1 << 14), (1, (1 << 30) + 64, (1 << 24) + 1),
+                                                   (1024, 1 << 21, 1 << 15), (700, 2997, 2997)])
+def test_refuses_more_than_a_launch_holds(call, tokens, heads, kv_heads):
+    kw = {"offs": (0, tokens)} if call is C._shared else {"batch": tokens}
+    assert call(rows=C._rows(tokens=tokens, heads=heads), cache=C._cache(kv_heads=kv_heads), **kw) \
+        == C.UNSUPPORTED
