@@ -4,6 +4,10 @@ Thin ctypes marshalling only: every step of compression and of the fused reconst
 multiply runs in the library's HIP kernels.  torch is used to hold device memory and to name
 the current HIP stream.  If the library is not built this module raises on first use; there
 is no fallback of any kind.
+
+Every call runs on ``stream``, a raw HIP stream handle (None: torch's current stream).  What it
+allocates itself is allocated on that stream; a call waits for no other stream's work, nor does
+any other stream wait for it.
 """
 from __future__ import annotations
 
@@ -229,24 +233,32 @@ def _raw_stream(stream, tensor):
     return torch._C._cuda_getCurrentRawStream(tensor.device.index)
 
 
-def _temp(nbytes, device, stream, dtype_name="uint8"):
-    """A scratch device tensor for one call whose kernels run on ``stream`` (None: torch's
-    current stream).  torch's caching allocator must not hand the block to another tensor while
-    those kernels still use it, so on another stream the block is recorded as in use there."""
+def _empty(shape, dtype, device, stream, kept=True):
+    """An uninitialised device tensor for a call whose kernels run on ``stream`` (None: torch's
+    current stream).  torch's caching allocator orders a block's uses by the stream it was allocated
+    on: a block freed on the current stream may still be in use by that stream's queued work, which
+    ``stream`` does not wait for.  So on another stream the tensor is allocated there, and, if the
+    caller gets it (``kept``), recorded as in use on the current one."""
     import torch
-    dtype = getattr(torch, dtype_name)
-    n = max(int(nbytes), 1) // dtype.itemsize
-    t = torch.empty(max(n, 1), dtype=dtype, device=device)
-    if stream is not None and int(stream) != torch.cuda.current_stream(device).cuda_stream:
-        t.record_stream(torch.cuda.ExternalStream(int(stream), device=device))
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if int(stream) == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if kept:
+        t.record_stream(current)
     return t
 
 
-def _on_stream(t, stream):
-    """Record a result made on torch's current stream as in use on the call's own."""
+def _temp(nbytes, device, stream, dtype_name="uint8"):
+    """A scratch device tensor for one call whose kernels run on ``stream`` (None: torch's
+    current stream)."""
     import torch
-    if stream is not None and int(stream) != torch.cuda.current_stream(t.device).cuda_stream:
-        t.record_stream(torch.cuda.ExternalStream(int(stream), device=t.device))
+    dtype = getattr(torch, dtype_name)
+    n = max(int(nbytes), 1) // dtype.itemsize
+    return _empty(max(n, 1), dtype, device, stream, kept=False)
 
 
 def _numel_at_least(t, n, what):
@@ -513,8 +525,8 @@ def matmul(x, w_base, variants, seg_offsets, seg_variant, y=None, out_dtype="bf1
     """Fused y = x (W_base + alpha_v sign_v)^T over a token batch grouped by variant."""
     import torch
     if y is None:
-        y = torch.empty((x.shape[0], w_base.shape[0]), device=x.device,
-                        dtype=torch.bfloat16 if out_dtype == "bf16" else torch.float32)
+        y = _empty((x.shape[0], w_base.shape[0]),
+                   torch.bfloat16 if out_dtype == "bf16" else torch.float32, x.device, stream)
     if path != "auto":
         matmul_grouped([(x, w_base, y, variants)], seg_offsets, seg_variant, out_dtype, path,
                        stream, workspace)
@@ -611,7 +623,7 @@ def reconstruct(w_base, variant, w_eff=None, stream=None):
         raise ValueError("w_base must be [d_out, d_in]")
     d_out, d_in = int(w_base.shape[0]), int(w_base.shape[1])
     if w_eff is None:
-        w_eff = torch.empty((d_out, d_in), dtype=torch.bfloat16, device=w_base.device)
+        w_eff = _empty((d_out, d_in), torch.bfloat16, w_base.device, stream)
     _check_shape(w_eff, (d_out, d_in), "w_eff")
     v = _Variant()
     _variant_struct(v, variant, d_out, d_in)
@@ -703,9 +715,7 @@ def _attend_rows(q, cache, out, lse, return_lse, scale, stream):
         raise ValueError(f"q must be [tokens, heads, {dim}], not {tuple(shape)}")
     qs = q.stride()
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        if stream is not None:
-            _on_stream(out, stream)
+        out = _empty(shape, q.dtype, q.device, stream)
     elif not out.is_cuda or out.dtype is not torch.bfloat16:
         raise TypeError("out must be a torch.bfloat16 CUDA/HIP tensor")
     elif out.shape != shape:
@@ -718,9 +728,7 @@ def _attend_rows(q, cache, out, lse, return_lse, scale, stream):
         _check_shape(lse, shape[:2], "lse")
         lptr = _dev(lse, "torch.float32", "lse")
     elif return_lse:
-        lse = torch.empty(shape[0], shape[1], dtype=torch.float32, device=q.device)
-        if stream is not None:
-            _on_stream(lse, stream)
+        lse = _empty(shape[:2], torch.float32, q.device, stream)
         lptr = lse.data_ptr()
     return _AttendRows(q.data_ptr(), out.data_ptr(), lptr, shape[0], shape[1], qs[0], qs[1], os_[0],
                        os_[1], dim ** -0.5 if scale is None else scale), out, lse
@@ -872,13 +880,9 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=
 
     f32, i32 = torch.float32, torch.int32
     if out is None:
-        out = torch.empty(rows, dtype=torch.int32, device=logits.device)
-        if stream is not None:
-            _on_stream(out, stream)
+        out = _empty(rows, i32, logits.device, stream)
     if logprob is None and return_logprob:
-        logprob = torch.empty(rows, dtype=torch.float32, device=logits.device)
-        if stream is not None:
-            _on_stream(logprob, stream)
+        logprob = _empty(rows, f32, logits.device, stream)
     _check(_lib().bitdelta_sample(
         logits.data_ptr(), 0 if logits.dtype == torch.bfloat16 else 1, rows, vocab, stride,
         arg(u, f32, "u"), arg(temperature, f32, "temperature"), arg(top_k, i32, "top_k"),
