@@ -563,7 +563,10 @@ size_t bitdelta_attend_window_workspace_bytes(int64_t tokens, int32_t heads,
  *   n_m = the number of tokens with w_j >= min_p.
  * The token drawn is the first whose running sum of weights exceeds u times the sum of the first
  * n; logprob = ln(its weight / that sum).  Weights are fp64 where a border between tokens is
- * decided; the sum over a row without a top-k up to 1024 carries about 1e-9 of itself.
+ * decided; the sum over a row without a top-k up to 1024 carries about 1e-9 of itself.  Where more
+ * than 4096 tokens lie within T / 64 of each other around a border, it is found among sums of weights
+ * rounded so that all n tokens of the row are off by at most n^2 2^-64 of the largest weight together
+ * (1e-9 at 2^17 tokens, 6e-8 at 2^20); beyond 2^20 tokens sums are fp64.
  *
  *   logits       [dev] logits_dtype (bitdelta_out_dtype: what bitdelta_matmul writes), row r at
  *                r * row_stride elements, vocab values; naturally aligned.

@@ -57,3 +57,26 @@ def test_infinite_temperature_is_a_uniform_draw(vocab, allowed, dtype):
     check(x, u, t, k=np.full(rows, 1500), p=np.full(rows, 0.7))
     check(x, u, np.where(np.arange(rows) % 2, np.inf, 0.8))
     check(x, u, np.full(rows, 3e38))
+
+
+def test_draws_from_a_long_tail_of_equal_logits():
+    """One large logit and 2^17 equal ones far below: a draw among those is at the token where the
+    definition puts it.  Sums of weights are off by 2^-30 each (header), the running one and the whole,
+    so the token by at most 2^-29 / w, plus one for a border."""
+    vocab, rows = (1 << 17) - 1, 24
+    # of the floats around ln 1e-9 the one whose weight is farthest from a multiple of 2^-43
+    cand = np.float32(-20.7) - np.arange(4000, dtype=np.float32) * np.float32(2.0 ** -19)
+    w = np.exp(cand.astype(np.float64))
+    at = np.argmin(np.abs(w * 2.0 ** 43 % 1.0 - 0.45))
+    x = np.full((rows, vocab), cand[at], np.float32)
+    x[:, 5] = 0.0
+    u = (1.0 - np.arange(1, rows + 1) * 2.0 ** -18).astype(np.float32)
+    tok, lp = bd.sample(torch.from_numpy(x).cuda(), put(u), return_logprob=True)
+    tok, lp = tok.cpu().numpy(), lp.cpu().numpy()
+    total = 1.0 + (vocab - 1) * w[at]
+    for r in range(rows):
+        j = np.floor((float(u[r]) * total - 1.0) / w[at])  # of the equal ones, in the order of indices
+        assert 0 < j < vocab - 1
+        want = j if j < 5 else j + 1
+        assert abs(tok[r] - want) <= 2.0 ** -29 / w[at] + 1, (r, tok[r], want)
+        assert abs(lp[r] - (np.log(w[at]) - np.log(total))) <= 2.0 ** -24 * abs(lp[r]) + 2.0 ** -29
