@@ -126,8 +126,9 @@ struct Row {
 __device__ __noinline__ double exp_f64(double x) {
   x = fmax(x, -745.0);
   const double n = __builtin_rint(x * 1.4426950408889634074);
-  double r = __builtin_fma(n, -0.693147180369123816490, x);  // ln 2 in two parts, the first short
-  r = __builtin_fma(n, -1.90821492927058770002e-10, r);
+  // ln 2 in two parts: its first 40 bits, of which n (11 bits) times is exact, and the rest
+  double r = __builtin_fma(n, -0x1.62e42fefa2p-1, x);
+  r = __builtin_fma(n, -0x1.9ef35793c7673p-41, r);
   double e = 1.0 / 479001600.0;
   e = __builtin_fma(e, r, 1.0 / 39916800.0);
   e = __builtin_fma(e, r, 1.0 / 3628800.0);
