@@ -490,7 +490,8 @@ typedef struct {
   int32_t heads;
   int64_t q_stride_token, q_stride_head;
   int64_t out_stride_token, out_stride_head;
-  float scale; /* finite, > 0; usually 1 / sqrt(head_dim)                                       */
+  float scale; /* finite, > 0; usually 1 / sqrt(head_dim).  scale * k_scale * log2(e) has to be a
+                * normal float32 (neither infinite nor below 2^-126), else INVALID_ARG          */
 } bitdelta_attend_rows;
 
 /*

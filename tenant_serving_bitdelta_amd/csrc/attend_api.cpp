@@ -107,6 +107,15 @@ bitdelta_status check_cache(const bitdelta_kv_cache* c, int32_t heads) {
   return BITDELTA_OK;
 }
 
+// what scores are multiplied by to enter exp2
+float score_factor(const bitdelta_attend_rows& r, const bitdelta_kv_cache& c) {
+  return (float)((double)r.scale * c.k_scale * 1.4426950408889634);
+}
+// Each scale may be a number whose product is none: infinite, it makes a score of 0 NaN, and 0 a masked one.
+bitdelta_status check_scales(const bitdelta_attend_rows& r, const bitdelta_kv_cache& c) {
+  return isnormal(score_factor(r, c)) ? BITDELTA_OK : BITDELTA_ERR_INVALID_ARG;
+}
+
 bitdelta_status check_rows(const bitdelta_attend_rows* r, int64_t max_tokens) {
   if (!r || r->tokens < 0) return BITDELTA_ERR_INVALID_ARG;
   if (r->tokens > max_tokens) return BITDELTA_ERR_UNSUPPORTED;
@@ -209,7 +218,7 @@ void fill(bd::AttendArgs* a, const bitdelta_attend_rows& r, const bitdelta_kv_ca
   a->heads = r.heads;
   a->kv_heads = c.kv_heads;
   a->group = r.heads / c.kv_heads;
-  a->c = (float)((double)r.scale * c.k_scale * 1.4426950408889634);
+  a->c = score_factor(r, c);
   a->v_scale = c.v_scale;
 }
 
@@ -325,7 +334,8 @@ bitdelta_status bitdelta_attend_shared(const bitdelta_attend_rows* rows,
   if (!shared_sizes_ok(rows->tokens, rows->heads, cache, table_width, prefix_width, seg_offsets,
                        num_segments, &s))
     return s;
-  s = check_table(table, table_width, lens, cache->page_size);
+  s = check_scales(*rows, *cache);
+  if (s == BITDELTA_OK) s = check_table(table, table_width, lens, cache->page_size);
   if (s == BITDELTA_OK) s = check_table(prefix_table, prefix_width, prefix_lens, cache->page_size);
   if (s != BITDELTA_OK) return s;
   const Plan p = plan_shared(rows->tokens, rows->heads, *cache, table_width, prefix_width,
@@ -368,6 +378,7 @@ bitdelta_status bitdelta_attend_window(const bitdelta_attend_rows* rows,
   if (s != BITDELTA_OK) return s;
   if (batch == 0 || rows->tokens == 0) return BITDELTA_OK;
   s = check_window(rows->tokens, rows->heads, cache, batch, table_width, max_q_len, window, sinks);
+  if (s == BITDELTA_OK) s = check_scales(*rows, *cache);
   if (s == BITDELTA_OK) s = check_table(table, table_width, lens, cache->page_size);
   if (s != BITDELTA_OK) return s;
   if (!aligned(q_offsets, 4)) return BITDELTA_ERR_ALIGNMENT;

@@ -38,3 +38,12 @@ def test_refuses_more_than_a_launch_holds(call, tokens, heads, kv_heads):
     kw = {"offs": (0, tokens)} if call is C._shared else {"batch": tokens}
     assert call(rows=C._rows(tokens=tokens, heads=heads), cache=C._cache(kv_heads=kv_heads), **kw) \
         == C.UNSUPPORTED
+
+
+@pytest.mark.parametrize("call", [C._shared, C._window])
+@pytest.mark.parametrize("scale,k_scale,status", [
+    (1e30, 1e30, C.INVALID), (1e-30, 1e-30, C.INVALID), (3e38, 2.0, C.INVALID), (1e-38, 0.5, C.INVALID),
+    (1e30, 1e-30, C.WORKSPACE), (1e-20, 1e-10, C.WORKSPACE), (1e20, 1e18, C.WORKSPACE)])
+def test_refuses_scales_whose_product_is_no_number(call, scale, k_scale, status):
+    """(a workspace too small is refused after them)"""
+    assert call(rows=C._rows(scale=scale), cache=C._cache(k_scale=k_scale), ws_bytes=1000) == status
