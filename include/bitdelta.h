@@ -504,7 +504,7 @@ typedef struct {
  *   rows          q, out: tokens = the number of sequences, in segment order.
  *   table         [dev] int32 [tokens][table_width];  lens [dev] int32 [tokens].
  *   prefix_table  [dev] int32 [num_segments][prefix_width];  prefix_lens [dev] int32
- *                 [num_segments].  prefix_width may be 0 (no prefixes).
+ *                 [num_segments].  prefix_width may be 0 (no prefixes): then neither is read.
  *   seg_offsets   [host] int32 [num_segments + 1], 0 = first <= ... <= last = tokens;
  *                 num_segments <= BITDELTA_MAX_SEGMENTS.
  *   workspace     [dev] at least bitdelta_attend_shared_workspace_bytes(...) bytes, 16-byte

@@ -784,13 +784,8 @@ def attend_shared(q, k_pages, v_pages, table, lens, prefix_table, prefix_lens, s
     nseg = offs.size - 1
     if (prefix_table is None) != (prefix_lens is None):
         raise ValueError("give prefix_table and prefix_lens, or neither")
-    if prefix_table is None:
-        # no prefixes: the batch is one segment without keys (its length pointer is never read
-        # past a table of width 0, which holds none)
-        pptr, pwidth, plptr = None, 0, lptr
-        offs, offs_p = _host_i32([0, rows.tokens])
-        nseg = 1
-    else:
+    pptr, pwidth, plptr = None, 0, None
+    if prefix_table is not None:
         pptr, pwidth, plptr = _table(prefix_table, prefix_lens, nseg, "prefix_table")
     need = 0 if workspace is not None else int(_lib().bitdelta_attend_shared_workspace_bytes(
         rows.tokens, rows.heads, ctypes.byref(cache), width, pwidth, offs_p, nseg))

@@ -336,7 +336,8 @@ bitdelta_status bitdelta_attend_shared(const bitdelta_attend_rows* rows,
     return s;
   s = check_scales(*rows, *cache);
   if (s == BITDELTA_OK) s = check_table(table, table_width, lens, cache->page_size);
-  if (s == BITDELTA_OK) s = check_table(prefix_table, prefix_width, prefix_lens, cache->page_size);
+  if (s == BITDELTA_OK && prefix_width > 0)
+    s = check_table(prefix_table, prefix_width, prefix_lens, cache->page_size);
   if (s != BITDELTA_OK) return s;
   const Plan p = plan_shared(rows->tokens, rows->heads, *cache, table_width, prefix_width,
                              seg_offsets, num_segments);
@@ -354,6 +355,12 @@ bitdelta_status bitdelta_attend_shared(const bitdelta_attend_rows* rows,
   a.max_q = 1;
   a.nseg = num_segments;
   for (int i = 0; i <= num_segments; ++i) a.seg_offsets[i] = seg_offsets[i];
+  if (prefix_width == 0) {
+    // no prefixes: one segment, with a length that counts as 0 in a table of width 0 whatever it is
+    a.prefix_lens = lens;
+    a.nseg = 1;
+    a.seg_offsets[1] = a.tokens;
+  }
   return run(&a, p, *cache, workspace, stream);
 }
 

@@ -47,3 +47,10 @@ def test_refuses_more_than_a_launch_holds(call, tokens, heads, kv_heads):
 def test_refuses_scales_whose_product_is_no_number(call, scale, k_scale, status):
     """(a workspace too small is refused after them)"""
     assert call(rows=C._rows(scale=scale), cache=C._cache(k_scale=k_scale), ws_bytes=1000) == status
+
+
+@pytest.mark.parametrize("offs,status", [
+    ((0, 4), C.WORKSPACE), ((0, 2, 4), C.WORKSPACE), ((0, 3), C.SHAPE), ((1, 4), C.SHAPE),
+    ((0, 3, 2, 4), C.SHAPE), (tuple([0] * 66) + (4,), C.INVALID)])
+def test_segments_are_checked_without_prefixes(offs, status):
+    assert C._shared(pt=None, pw=0, pl=None, offs=offs, ws_bytes=1000) == status

@@ -171,3 +171,15 @@ def test_max_q_len_of_no_limit(q_lens, lens):
     out, lse = bd.attend_window(q, k, v, A.i32(table), A.i32(lens), 60, 2, q_offsets=offs,
                                 max_q_len=2 ** 31 - 1, return_lse=True)
     A.check(out, lse, A.window_ref(qf, kf, vf, 16, table, lens, q_lens, 60, 2, sc, 128 ** -0.5))
+
+
+def test_segment_offsets_are_checked_without_prefixes():
+    rng = np.random.default_rng(61)
+    table, k, v, kf, vf, sc, q, qf, _ = setup(rng, [1, 1], [40, 33], 8, 2)
+    t, l = A.i32(table), A.i32([40, 33])
+    ref = A.window_ref(qf, kf, vf, 16, table, [40, 33], [1, 1], 4000, 0, sc, 128 ** -0.5)
+    for offs in ([0, 2], [0, 1, 2], [0, 0, 2, 2]):
+        A.check(*bd.attend_shared(q, k, v, t, l, None, None, offs, return_lse=True), ref)
+    for offs in ([0, 1], [1, 2], [0, 3], [0, 2, 1, 2], [0], [0] * 66 + [2]):
+        with pytest.raises(bd.BitDeltaError):
+            bd.attend_shared(q, k, v, t, l, None, None, offs)
