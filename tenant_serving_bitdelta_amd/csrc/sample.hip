@@ -1070,9 +1070,24 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
 hipError_t launch_sample(const SampleArgs& a, bool f32, hipStream_t stream) {
   if (a.rows < 1 || a.vocab < 1) return hipErrorInvalidValue;
   clear_stale_error();
-  if (f32) hipLaunchKernelGGL(sample_kernel<true>, dim3(a.rows), dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL(sample_kernel<false>, dim3(a.rows), dim3(kThreads), 0, stream, a);
-  return hipGetLastError();
+  constexpr int kMost = 1 << 21;  // rows of a launch, which holds fewer than 2^32 threads
+  for (int first = 0; first < a.rows; first += kMost) {
+    SampleArgs part = a;
+    part.rows = min(a.rows - first, kMost);
+    part.logits = static_cast<const unsigned char*>(a.logits) + first * a.row_stride * (f32 ? 4 : 2);
+    part.u += first;
+    if (a.temperature) part.temperature += first;
+    if (a.top_k) part.top_k += first;
+    if (a.top_p) part.top_p += first;
+    if (a.min_p) part.min_p += first;
+    part.tokens += first;
+    if (a.logprob) part.logprob += first;
+    if (f32) hipLaunchKernelGGL(sample_kernel<true>, dim3(part.rows), dim3(kThreads), 0, stream, part);
+    else hipLaunchKernelGGL(sample_kernel<false>, dim3(part.rows), dim3(kThreads), 0, stream, part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace bd

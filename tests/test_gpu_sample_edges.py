@@ -80,3 +80,17 @@ def test_draws_from_a_long_tail_of_equal_logits():
         want = j if j < 5 else j + 1
         assert abs(tok[r] - want) <= 2.0 ** -29 / w[at] + 1, (r, tok[r], want)
         assert abs(lp[r] - (np.log(w[at]) - np.log(total))) <= 2.0 ** -24 * abs(lp[r]) + 2.0 ** -29
+
+
+def test_more_rows_than_one_launch_takes():
+    """2^22 rows of 1024 threads are more than a grid holds."""
+    rows = (1 << 22) + 3
+    x = torch.zeros((rows, 3), device="cuda")
+    x[::2, 1], x[1::2, 2] = 5.0, 5.0
+    x[-1] = torch.tensor([9.0, 0.0, 0.0])
+    u = torch.zeros(rows, device="cuda")
+    tok, lp = bd.sample(x, u, top_k=torch.ones(rows, dtype=torch.int32, device="cuda"),
+                        return_logprob=True)
+    want = 1 + torch.arange(rows, device="cuda", dtype=torch.int32) % 2
+    want[-1] = 0
+    assert torch.equal(tok, want) and not bool(lp.any())
