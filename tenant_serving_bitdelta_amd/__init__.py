@@ -96,6 +96,11 @@ def _lib():
         # system one) whose kernels and device memory do not mix.
         import torch  # noqa: F401
         L = ctypes.CDLL(LIB_PATH)
+        # entry points that came without a new ABI version
+        for name in ("bitdelta_attend_shared", "bitdelta_attend_window", "bitdelta_sample"):
+            if not hasattr(L, name):
+                raise RuntimeError(f"{LIB_PATH} has no {name}: it is older than this package; run "
+                                   "__graft_entry__.build() again")
         L.bitdelta_abi_version.restype = ctypes.c_int
         L.bitdelta_status_string.restype = ctypes.c_char_p
         L.bitdelta_status_string.argtypes = [ctypes.c_int]
