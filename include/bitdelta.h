@@ -473,15 +473,16 @@ typedef struct {
   int32_t page_size; /* tokens per page, any number >= 1                                        */
   int32_t kv_heads;
   int32_t head_dim;
-  /* strides in elements, each a multiple of 16 bytes; the head_dim values of a row are
-   * contiguous */
+  /* strides in elements, each a multiple of 16 bytes (any value where the dimension is 1); the
+   * head_dim values of a row are contiguous */
   int64_t k_stride_page, k_stride_token, k_stride_head;
   int64_t v_stride_page, v_stride_token, v_stride_head;
   float k_scale, v_scale; /* what a stored value is multiplied by; finite, > 0                  */
 } bitdelta_kv_cache;
 
 /* Query and output rows: token t, head h at t * stride_token + h * stride_head (in elements; q's
- * multiples of 8, out's of 4), head_dim contiguous values.  q is 16-byte, out 8-byte aligned. */
+ * multiples of 8, out's of 4; any value for a single token or head), head_dim contiguous values.  q is
+ * 16-byte, out 8-byte aligned. */
 typedef struct {
   const void* q; /* [dev] bf16                                                                  */
   void* out;     /* [dev] bf16                                                                  */

@@ -97,11 +97,15 @@ bitdelta_status check_cache(const bitdelta_kv_cache* c, int32_t heads) {
   if (c->head_dim != 64 && c->head_dim != 128) return BITDELTA_ERR_UNSUPPORTED;
   if (heads / c->kv_heads > BITDELTA_ATTEND_MAX_GROUP) return BITDELTA_ERR_UNSUPPORTED;
   const int64_t unit = c->dtype == BITDELTA_KV_FP8 ? 16 : 8;  // elements of 16 bytes
-  for (int64_t s : {c->k_stride_page, c->k_stride_token, c->k_stride_head, c->v_stride_page,
-                    c->v_stride_token, c->v_stride_head}) {
-    if (s < 0) return BITDELTA_ERR_INVALID_ARG;
-    if (s % unit != 0) return BITDELTA_ERR_ALIGNMENT;
-    if (s / unit > 0xFFFFFFFFll) return BITDELTA_ERR_UNSUPPORTED;
+  // strides of dimensions of one element are never stepped over: any value will do
+  const struct { int64_t stride; int32_t n; } steps[] = {
+      {c->k_stride_page, c->num_pages}, {c->k_stride_token, c->page_size}, {c->k_stride_head, c->kv_heads},
+      {c->v_stride_page, c->num_pages}, {c->v_stride_token, c->page_size}, {c->v_stride_head, c->kv_heads}};
+  for (const auto& s : steps) {
+    if (s.n == 1) continue;
+    if (s.stride < 0) return BITDELTA_ERR_INVALID_ARG;
+    if (s.stride % unit != 0) return BITDELTA_ERR_ALIGNMENT;
+    if (s.stride / unit > 0xFFFFFFFFll) return BITDELTA_ERR_UNSUPPORTED;
   }
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return BITDELTA_ERR_ALIGNMENT;
   return BITDELTA_OK;
@@ -121,12 +125,13 @@ bitdelta_status check_rows(const bitdelta_attend_rows* r, int64_t max_tokens) {
   if (r->tokens > max_tokens) return BITDELTA_ERR_UNSUPPORTED;
   if (r->tokens == 0) return BITDELTA_OK;
   if (!r->q || !r->out || !(r->scale > 0.f) || !isfinite(r->scale)) return BITDELTA_ERR_INVALID_ARG;
-  if (r->q_stride_token < 0 || r->q_stride_head < 0 || r->out_stride_token < 0 ||
-      r->out_stride_head < 0)
+  const bool tokens = r->tokens > 1, heads = r->heads > 1;  // else the stride is never stepped over
+  if ((tokens && (r->q_stride_token < 0 || r->out_stride_token < 0)) ||
+      (heads && (r->q_stride_head < 0 || r->out_stride_head < 0)))
     return BITDELTA_ERR_INVALID_ARG;
   if (!aligned(r->q, 16) || !aligned(r->out, 8) || !aligned(r->lse, 4) ||
-      r->q_stride_token % 8 != 0 || r->q_stride_head % 8 != 0 || r->out_stride_token % 4 != 0 ||
-      r->out_stride_head % 4 != 0)
+      (tokens && (r->q_stride_token % 8 != 0 || r->out_stride_token % 4 != 0)) ||
+      (heads && (r->q_stride_head % 8 != 0 || r->out_stride_head % 4 != 0)))
     return BITDELTA_ERR_ALIGNMENT;
   return BITDELTA_OK;
 }

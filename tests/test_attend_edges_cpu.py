@@ -54,3 +54,20 @@ def test_refuses_scales_whose_product_is_no_number(call, scale, k_scale, status)
     ((0, 3, 2, 4), C.SHAPE), (tuple([0] * 66) + (4,), C.INVALID)])
 def test_segments_are_checked_without_prefixes(offs, status):
     assert C._shared(pt=None, pw=0, pl=None, offs=offs, ws_bytes=1000) == status
+
+
+ONE = [(dict(heads=2), dict(kv_heads=1, k_stride_head=3, v_stride_head=1)),
+       (dict(heads=1, q_stride_head=-1, out_stride_head=1), dict(kv_heads=1, k_stride_head=-3, v_stride_head=1)),
+       (dict(), dict(num_pages=1, k_stride_page=1, v_stride_page=-1)),
+       (dict(), dict(page_size=1, k_stride_token=1, v_stride_token=5)),
+       (dict(tokens=1, q_stride_token=1, out_stride_token=-1), dict())]
+
+
+@pytest.mark.parametrize("call", [C._shared, C._window])
+@pytest.mark.parametrize("case", range(len(ONE)))
+def test_strides_of_single_elements_may_be_anything(call, case):
+    """(a workspace too small is refused after them)"""
+    r, c = ONE[case]
+    n = r.get("tokens", 4)
+    kw = {"offs": (0, n), "pw": 4000} if call is C._shared else {"batch": n}
+    assert call(rows=C._rows(**r), cache=C._cache(**c), width=4000, ws_bytes=1000, **kw) == C.WORKSPACE

@@ -183,3 +183,17 @@ def test_segment_offsets_are_checked_without_prefixes():
     for offs in ([0, 1], [1, 2], [0, 3], [0, 2, 1, 2], [0], [0] * 66 + [2]):
         with pytest.raises(bd.BitDeltaError):
             bd.attend_shared(q, k, v, t, l, None, None, offs)
+
+
+@pytest.mark.parametrize("n,length", [(1, 7), (3, 2000)])
+def test_single_heads_with_any_stride(n, length):
+    """q, out and the cache of one head, whose head dimension has a stride of 1."""
+    rng = np.random.default_rng(71)
+    table, k, v, kf, vf, sc, q, qf, offs = setup(rng, [n], [length], 1, 1, 64)
+    lay = lambda x: x.squeeze(-2).contiguous().unsqueeze(-1).transpose(-1, -2)  # noqa: E731
+    q1, k1, v1 = lay(q), lay(k), lay(v)
+    out = lay(torch.empty_like(q))
+    assert q1.stride(-2) == k1.stride(-2) == out.stride(-2) == 1
+    _, lse = bd.attend_window(q1, k1, v1, A.i32(table), A.i32([length]), 1500, 2, q_offsets=offs, max_q_len=n,
+                              out=out, return_lse=True)
+    A.check(out, lse, A.window_ref(qf, kf, vf, 16, table, [length], [n], 1500, 2, sc, 64 ** -0.5))
