@@ -455,7 +455,8 @@ int64_t bitdelta_residency_used_bytes(bitdelta_residency* r);
  *
  * Limits (else UNSUPPORTED): head_dim 64 or 128, at most 64 query heads per kv head, 1024
  * sequences per call, 2^30 tokens per sequence, 2^30 query rows (tokens x heads), 2^21 (sequence, kv
- * head) pairs, page and token strides below 2^36 bytes.
+ * head) pairs, tables that hold fewer than 2^38 tokens together (a prefix's counted for each of its
+ * sequences; for a window no more than what it shows), page and token strides below 2^36 bytes.
  */
 #define BITDELTA_ATTEND_MAX_SEQS 1024
 #define BITDELTA_ATTEND_MAX_GROUP 64

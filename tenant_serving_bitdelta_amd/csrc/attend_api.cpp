@@ -287,6 +287,13 @@ bitdelta_status check_table(const void* table, int32_t width, const void* lens, 
   return BITDELTA_OK;
 }
 
+// Steps of all sequences are summed in 32 bits; the tables' capacity bounds them.  (The steps of prefixes
+// in row tiles then fit, too: they have half the keys, but a tile holds at least 4 sequences, or the last
+// ones of one of at most 65 segments.)
+bool steps_fit(int64_t sequences, int64_t keys) {
+  return sequences * ((keys + bd::kRowStep - 1) / bd::kRowStep) < int64_t(1) << 31;
+}
+
 bool shared_sizes_ok(int64_t tokens, int32_t heads, const bitdelta_kv_cache* cache, int32_t width,
                      int32_t pwidth, const int32_t* offs, int32_t nseg, bitdelta_status* s) {
   *s = check_cache(cache, heads);
@@ -294,7 +301,8 @@ bool shared_sizes_ok(int64_t tokens, int32_t heads, const bitdelta_kv_cache* cac
   if (*s == BITDELTA_OK) *s = check_segments(tokens, offs, nseg);
   if (*s == BITDELTA_OK && (tokens > BITDELTA_ATTEND_MAX_SEQS || tokens * heads > kMaxRows ||
                             tokens * cache->kv_heads > kMaxUnits ||
-                            ((int64_t)width + pwidth) * cache->page_size > kMaxKeys))
+                            ((int64_t)width + pwidth) * cache->page_size > kMaxKeys ||
+                            !steps_fit(tokens, ((int64_t)width + pwidth) * cache->page_size)))
     *s = BITDELTA_ERR_UNSUPPORTED;
   return *s == BITDELTA_OK;
 }
@@ -306,7 +314,8 @@ bitdelta_status check_window(int64_t tokens, int32_t heads, const bitdelta_kv_ca
   if (s != BITDELTA_OK) return s;
   if (batch < 0 || width < 0 || max_q < 1 || window < 1 || sinks < 0) return BITDELTA_ERR_INVALID_ARG;
   if (batch > BITDELTA_ATTEND_MAX_SEQS || (int64_t)width * cache->page_size > kMaxKeys ||
-      tokens * heads > kMaxRows || (int64_t)batch * cache->kv_heads > kMaxUnits)
+      tokens * heads > kMaxRows || (int64_t)batch * cache->kv_heads > kMaxUnits ||
+      !steps_fit(batch, std::min<int64_t>((int64_t)width * cache->page_size, (int64_t)window + max_q - 1 + sinks)))
     return BITDELTA_ERR_UNSUPPORTED;
   return BITDELTA_OK;
 }

@@ -71,3 +71,15 @@ def test_strides_of_single_elements_may_be_anything(call, case):
     n = r.get("tokens", 4)
     kw = {"offs": (0, n), "pw": 4000} if call is C._shared else {"batch": n}
     assert call(rows=C._rows(**r), cache=C._cache(**c), width=4000, ws_bytes=1000, **kw) == C.WORKSPACE
+
+
+@pytest.mark.parametrize("call,kw,status", [
+    (C._shared, dict(width=1 << 29, pw=4), C.UNSUPPORTED), (C._shared, dict(width=1 << 27, pw=4), C.WORKSPACE),
+    (C._shared, dict(width=4, pw=1 << 29), C.UNSUPPORTED), (C._shared, dict(width=4, pw=1 << 27), C.WORKSPACE),
+    (C._window, dict(width=1 << 29, window=1 << 30), C.UNSUPPORTED),
+    (C._window, dict(width=1 << 27, window=1 << 30), C.WORKSPACE),
+    (C._window, dict(width=1 << 29, window=1 << 20), C.WORKSPACE)])
+def test_refuses_tables_whose_steps_pass_32_bits(call, kw, status):
+    """1024 sequences of up to 2^29 tokens (a workspace too small is refused after them)"""
+    kw = dict(kw, **({"offs": (0, 1024)} if call is C._shared else {"batch": 1024}))
+    assert call(rows=C._rows(tokens=1024), cache=C._cache(page_size=1), ws_bytes=1000, **kw) == status
