@@ -243,7 +243,8 @@ def _empty(shape, dtype, device, stream, kept=True):
     current stream).  torch's caching allocator orders a block's uses by the stream it was allocated
     on: a block freed on the current stream may still be in use by that stream's queued work, which
     ``stream`` does not wait for.  So on another stream the tensor is allocated there, and, if the
-    caller gets it (``kept``), recorded as in use on the current one."""
+    caller gets it (``kept``), recorded as in use on the current one.  (Calls of some 10 us make their
+    results themselves where ``stream`` is None: through here one takes 2 us longer.)"""
     import torch
     if stream is None or device.type != "cuda":
         return torch.empty(shape, dtype=dtype, device=device)
@@ -720,7 +721,8 @@ def _attend_rows(q, cache, out, lse, return_lse, scale, stream):
         raise ValueError(f"q must be [tokens, heads, {dim}], not {tuple(shape)}")
     qs = q.stride()
     if out is None:
-        out = _empty(shape, q.dtype, q.device, stream)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None else \
+            _empty(shape, q.dtype, q.device, stream)
     elif not out.is_cuda or out.dtype is not torch.bfloat16:
         raise TypeError("out must be a torch.bfloat16 CUDA/HIP tensor")
     elif out.shape != shape:
@@ -733,7 +735,8 @@ def _attend_rows(q, cache, out, lse, return_lse, scale, stream):
         _check_shape(lse, shape[:2], "lse")
         lptr = _dev(lse, "torch.float32", "lse")
     elif return_lse:
-        lse = _empty(shape[:2], torch.float32, q.device, stream)
+        lse = torch.empty(shape[0], shape[1], dtype=torch.float32, device=q.device) if stream is None else \
+            _empty(shape[:2], torch.float32, q.device, stream)
         lptr = lse.data_ptr()
     return _AttendRows(q.data_ptr(), out.data_ptr(), lptr, shape[0], shape[1], qs[0], qs[1], os_[0],
                        os_[1], dim ** -0.5 if scale is None else scale), out, lse
@@ -880,9 +883,11 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=
 
     f32, i32 = torch.float32, torch.int32
     if out is None:
-        out = _empty(rows, i32, logits.device, stream)
+        out = torch.empty(rows, dtype=i32, device=logits.device) if stream is None else \
+            _empty(rows, i32, logits.device, stream)
     if logprob is None and return_logprob:
-        logprob = _empty(rows, f32, logits.device, stream)
+        logprob = torch.empty(rows, dtype=f32, device=logits.device) if stream is None else \
+            _empty(rows, f32, logits.device, stream)
     _check(_lib().bitdelta_sample(
         logits.data_ptr(), 0 if logits.dtype == torch.bfloat16 else 1, rows, vocab, stride,
         arg(u, f32, "u"), arg(temperature, f32, "temperature"), arg(top_k, i32, "top_k"),
