@@ -453,6 +453,9 @@ int64_t bitdelta_residency_used_bytes(bitdelta_residency* r);
  * is not in [0, num_pages) is absent (no query sees it).  What the cache holds outside the keys a
  * call's queries see (beyond the lengths, before the window) is never used, NaN included.
  *
+ * These entry points and bitdelta_sample came with ABI 7, without a new number: a program that may meet
+ * an older library looks them up by name.
+ *
  * Limits (else UNSUPPORTED): head_dim 64 or 128, at most 64 query heads per kv head, 1024
  * sequences per call, 2^30 tokens per sequence, 2^30 query rows (tokens x heads), 2^21 (sequence, kv
  * head) pairs, tables that hold fewer than 2^38 tokens together (a prefix's counted for each of its
@@ -501,7 +504,8 @@ typedef struct {
  * sequences share prefixes by segment: sequence b of segment g (seg_offsets as in
  * bitdelta_plan_segments: the requests of one variant share that variant's prompt) sees the
  * prefix_lens[g] prefix keys of row g of prefix_table, then its own lens[b] keys of row b of
- * table.  A segment's prefix is read once for all its sequences.
+ * table.  Where that saves 128 MiB of reading and more, going by prefix_width, a segment's prefix is
+ * read once for up to 256 query rows (sequences x heads per kv head); else each sequence reads it.
  *
  *   rows          q, out: tokens = the number of sequences, in segment order.
  *   table         [dev] int32 [tokens][table_width];  lens [dev] int32 [tokens].

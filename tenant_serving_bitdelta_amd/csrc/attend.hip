@@ -283,7 +283,9 @@ __device__ __forceinline__ int scan_find(const int* scan, int count, int x) {
 // fit took a second turn (145 against 120 us for the own keys of 256 sequences, bf16, dim 128).
 // Measured: 64 sequences x 8 kv heads of 6.9k keys, e4m3, dim 128, 902 MB in 187 us, 4.8 TB/s, what a
 // large copy reaches; the 448 MB of own keys of 256 sequences, bf16, in 121 us, 3.7 TB/s; one
-// sequence's 4.3 MB 9 us, which is latency.
+// sequence's 4.3 MB 9 us, which is latency.  Registers decide how many fit; at dim 128 some variants
+// spill: 8 for single tokens from e4m3 (36 bytes a lane), 23 to 87 with 2 and 4 column blocks from bf16,
+// up to 47 from e4m3.
 // ---------------------------------------------------------------------------------------------
 template <int D, bool FP8, int NC>
 struct RowLoop {
@@ -517,8 +519,8 @@ void attend_row_kernel(const AttendArgs a) {
           e[i] = exp2_fast(__builtin_fmaf(s[c][i >> 2][i & 3], a.c, -mb));
           w.l[c] += e[i];
         }
-        // weights enter the product as bf16 (relative error 2^-9 each, as the values they weigh);
-        // the sum l keeps them in fp32
+        // weights enter the product as bf16, the matrix instruction's operand type (off by at most 2^-8
+        // of themselves, as the values they weigh were when stored); the sum l keeps them in fp32
         p[c] = u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
                      pack_bf16(e[6], e[7])};
       }
@@ -632,12 +634,14 @@ void attend_row_kernel(const AttendArgs a) {
 //
 // Bound by the chain of a step within a wave: scores (32 matrix instructions), softmax, values (32),
 // about 2.2 us, with two waves a SIMD to fill each other's gaps; vector and matrix instructions each
-// are busy 44% of the time.  Measured, bf16, dim 128, 64 heads on 8: 8192 new tokens of 16384, window
+// are busy 44% of the time, so that neither is at its limit.  Measured, bf16, dim 128, 64 heads on 8: 8192 new tokens of 16384, window
 // 4096, 1.10 TFLOP in 1130 us, 970 TFLOP/s (a large matrix product reaches 1184); 4 requests of up to
-// 2048 tokens, window 1024, 108 GFLOP in 167 us, 650 TFLOP/s.  Prefixes of 256 sequences in 14 segments: 53 GFLOP on 300 MB in 110 us.
+// 2048 tokens, window 1024, 108 GFLOP in 168 us, 640 TFLOP/s; the same from an e4m3 cache 1156 and 172 us.
+// Plain causal attention of 8192 tokens 1143 us, 960 TFLOP/s.  Prefixes of 256 sequences in 14 segments:
+// 53 GFLOP on 300 MB in 110 us.  A unit's keys are not split: 16 tokens over 4096 keys, 8 units, take 88 us.
 // Tried and slower or no faster: the next step's scores under this step's softmax (1133 in the
-// compiler's order, 1171 to 1211 interleaved by hand: vector and matrix cycles add up to 88%, so little
-// is left to overlap), the second wave of each SIMD a third of a step late (4% slower),
+// compiler's order, 1171 to 1211 interleaved by hand), the second wave of each SIMD a third of a step
+// late (4% slower),
 // wave priorities around the products (1291 against 1225 us), a barrier every second step (1225
 // against 1220), values with infinities or NaN multiplied key by key (spills, 5 times slower).
 // ---------------------------------------------------------------------------------------------
@@ -1122,8 +1126,8 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
 #pragma unroll
           for (int i = 0; i < 8; ++i) e[i] = exp2_fast(__builtin_fmaf(sc[kb >> 1][8 * (kb & 1) + i], a.c, -mb));
           lp[kb] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-          // weights enter the product as bf16 (relative error 2^-9 each, as the values they
-          // weigh); the sum l keeps them in fp32
+          // weights enter the product as bf16, the matrix instruction's operand type (off by at most
+          // 2^-8 of themselves, as the values they weigh were when stored); the sum l keeps them in fp32
           p[kb] = u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
                         pack_bf16(e[6], e[7])};
         }
