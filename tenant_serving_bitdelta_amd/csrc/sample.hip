@@ -997,9 +997,10 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
       tau = lo <= to_key(kNegInf) ? kNegInf : from_key(lo);
     } else if (!greedy) {
       tau = kNegInf;
-      if (p >= 1.0 && minp > 0.0) {
-        // every token that min_p keeps (and a margin for the rounding of this bound)
-        const float t = (float)((double)top + log_f64(minp) / inv_t);
+      if (p >= 1.0 && minp > 0.0 && inv_t > 0.0) {
+        // every token that min_p keeps (and margins for the rounding of its weight and of this bound;
+        // where T is infinite, every token that is not masked)
+        const float t = (float)((double)top + (log_f64(minp) - 0x1p-52) / inv_t);
         tau = top < __builtin_inff() ? t - fabsf(t) * 1e-5f - 1e-30f : top;
       }
     }

@@ -94,3 +94,14 @@ def test_more_rows_than_one_launch_takes():
     want = 1 + torch.arange(rows, device="cuda", dtype=torch.int32) % 2
     want[-1] = 0
     assert torch.equal(tok, want) and not bool(lp.any())
+
+
+@pytest.mark.parametrize("vocab", [5, 1500, 9001])
+def test_min_p_of_one_at_an_infinite_temperature_keeps_every_token(vocab):
+    rng = np.random.default_rng(vocab)
+    x = rng.normal(size=(6, vocab)).astype(np.float32)
+    x[3:, ::3] = -np.inf
+    u = np.linspace(0.01, 0.99, 6)
+    check(torch.from_numpy(x).cuda(), u, np.full(6, np.inf), m=np.ones(6))
+    check(torch.from_numpy(x).cuda(), u, np.full(6, 3e38), m=np.ones(6))
+    check(torch.from_numpy(np.round(x)).cuda(), u, m=np.ones(6))
