@@ -239,6 +239,12 @@ __device__ __forceinline__ int wave_scan(int x) {
   x += lane_move<0x142, 0xA>(x, 0);
   return x + lane_move<0x143, 0xC>(x, 0);
 }
+__device__ __forceinline__ double last_lane(double x) {
+  const long long b = __double_as_longlong(x);
+  const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)b, 63);
+  const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(b >> 32), 63);
+  return __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
+}
 template <int kCtrl, int kRows>
 __device__ __forceinline__ float lane_move(float x) {  // where there is none: its own
   return __int_as_float(lane_move<kCtrl, kRows>(__float_as_int(x), __float_as_int(x)));
@@ -752,7 +758,8 @@ __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f,
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
       cnt1 += bins.count(t[i]);
-      m[i] = mass1 += e * bins.weight(t[i]);
+      // (what lies beyond the bins weighs less than e^-39.9 each, 4e-12 together: nothing, among sums)
+      m[i] = mass1 += kOwn * tid + i < kBins - 1 ? e * bins.weight(t[i]) : 0.0;
       e *= 0.98449643700540840596;  // e^(-1/64)
     }
     const Before b = block_prefix(cnt1, mass1);
@@ -770,6 +777,7 @@ __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f,
   mass0 = tid ? sh.bin_mass[kOwn * tid - 1] : 0.0;
   int keep = f.vocab;                         // tokens kept
   double zk = sh.bin_mass[kBins - 1], zn = zk;  // weight of the first k, of the tokens kept
+  int whole = kBins;  // the bins before this one are in zk and zn as tallied, this one token by token
   Answer r = {0, 0.0, false};
 #pragma unroll 1
   for (int stage = 0; stage < 4; ++stage) {
@@ -820,11 +828,20 @@ __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f,
     double sum = 0;   // their weight up to it
     uint64_t token = 0;
     const int limit = min(n, keep - before);  // tokens of the bin that a draw may take
+    // A target takes the bin's weight as its tokens have it, too: where they hold the row's weight, a
+    // border between equal tokens (half of them, say) is then exactly where the definition has it.  (Up
+    // to 64 tokens it is wave 0 that has them, and zn then: the wave that writes the answer.)
+    const double tallied = bin < whole ? sh.bin_mass[bin] - mass_before : 0.0;
+    auto own_target = [&](double weight) {
+      const double more = bin < whole ? weight - tallied : 0.0;
+      if (stage == 3) zn += more;
+      return (stage == 3 ? f.u * zn : f.p * (zk + more)) - mass_before;
+    };
     const bool few = n <= 64;
     if (few) {
       if (tid < 64) {
         const Few c = order_few(n, top, f.inv_t);
-        const double t = target - mass_before;
+        const double t = own_target(last_lane(c.cum));
         if (stage == 0) last = f.k - before <= n ? f.k - before - 1 : -1;
         else if (stage == 1) last = min(lanes_below(n, t, false, c), n - 1);
         else if (stage == 2) last = __popcll(__ballot(tid < n && c.w >= f.minp)) - 1;
@@ -844,7 +861,7 @@ __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f,
     } else {
       sort_candidates(n);
       weigh(n, top, f.inv_t);
-      const double t = target - mass_before;
+      const double t = own_target(sh.cum[n - 1]);
       if (stage == 0) last = f.k - before <= n ? f.k - before - 1 : -1;
       else if (stage == 1) last = min(count_below(n, t, false), n - 1);
       else if (stage == 2) last = count_heavy(n, f.minp, top, f.inv_t) - 1;
@@ -857,11 +874,13 @@ __device__ __forceinline__ Answer by_bins(const Row<F32>& row, const Filters& f,
       if (last >= 0) {  // (else fewer than k tokens are not masked: all of them)
         keep = f.k;
         zk = zn = sum;
+        whole = bin;
       }
     } else if (stage == 3) {
       if (last >= 0) r = Answer{token, zn, true};
     } else if (before + last + 1 < keep) {
       keep = max(before + last + 1, 1);
+      whole = bin;
       zn = stage == 2 ? fmax(sum, 1.0) : sum;
     }
     if (tid == 0) sh.found = kBins - 1;

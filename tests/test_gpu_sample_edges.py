@@ -105,3 +105,26 @@ def test_min_p_of_one_at_an_infinite_temperature_keeps_every_token(vocab):
     check(torch.from_numpy(x).cuda(), u, np.full(6, np.inf), m=np.ones(6))
     check(torch.from_numpy(x).cuda(), u, np.full(6, 3e38), m=np.ones(6))
     check(torch.from_numpy(np.round(x)).cuda(), u, m=np.ones(6))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("equal", [2, 6, 48, 64, 66, 1062, 2048, 4096])
+def test_borders_between_equal_tokens(equal, dtype):
+    """Half, a quarter and three quarters of the weight of n equal tokens are whole numbers of them; what
+    else the row holds weighs less than fp64 resolves, or is masked."""
+    rng = np.random.default_rng(equal)
+    vocab, rows = 5003, 9
+    x = np.full((rows, vocab), -60.0, np.float32)
+    x[3:6] = -np.inf
+    x[6:] = -1000.0 - 4.0 * rng.integers(0, 50, size=(3, vocab))
+    for r in range(rows):
+        x[r, rng.permutation(vocab)[:equal]] = (0.0, 3.0, -7.5)[r % 3]
+    x = torch.from_numpy(x).cuda().to(dtype)
+    share = np.tile([0.5, 0.25, 0.75], 3)
+    check(x, share)
+    check(x, np.full(rows, 1.0 - 2.0 ** -24), p=share)
+    check(x, share, p=share)
+    check(x, np.tile([0.25, 0.5, 0.5], 3), p=share, m=np.full(rows, 0.9))
+    check(x, share, k=np.full(rows, 4500))
+    check(x, np.full(rows, 1.0 - 2.0 ** -24), k=np.full(rows, 4500), p=share)
+    check(x, share, t=np.full(rows, 0.1), p=share)
