@@ -26,7 +26,7 @@
 // logits: greedy 8 us (6.5 of them the reading, the rate of one compute unit), top-k 50 11, top-k
 // 1000 27, top-p 0.9 29 (18 the reading with its tallies: vector instructions and LDS atomics), no
 // filter 50 (13 of them reading the row again for a bin of thousands).  256 such rows with mixed
-// settings, 134 MB: 63 us, 2.1 TB/s; 64 x 128000 bf16, top-k 50 with top-p: 16 us.
+// settings, 134 MB: 64 us, 2.1 TB/s; 64 x 128000 bf16, top-k 50 with top-p: 16 us.
 // Histograms by LDS atomics in the first reading without the maxima, every weight in fp64, took 158 us
 // a row and more.
 #include "bd_internal.h"
