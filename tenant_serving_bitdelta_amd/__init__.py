@@ -231,7 +231,8 @@ def _stream(stream):
 
 
 def _raw_stream(stream, tensor):
-    """The call's stream handle: ``stream``, or torch's current one on the tensor's device."""
+    """The call's stream handle: ``stream``, or torch's current one on the tensor's device (in 0.1 us;
+    through torch.cuda.current_stream and its object it takes 1.9 of a short call's 10)."""
     if stream is not None:
         return int(stream)
     import torch
