@@ -444,17 +444,18 @@ int64_t bitdelta_residency_used_bytes(bitdelta_residency* r);
  *     s_j = scale * k_scale * (q . k_j)           lse = ln sum_{j in J} exp(s_j)
  *     out = v_scale * sum_{j in J} exp(s_j - lse) * v_j
  *
- * An empty J gives out = 0 and lse = -inf.  Scores, maxima and sums are fp32; the weights enter
- * the product with the values as bf16; out is rounded to bf16 once.  Results do not depend on
- * timing: every sum is taken in a fixed order.
+ * (k_j and v_j as stored.)  An empty J gives out = 0 and lse = -inf.  Scores, maxima and sums are fp32;
+ * the weights enter the product with the values as bf16; out is rounded to bf16 once.  Results do not
+ * depend on timing: every sum is taken in a fixed order.
  *
  * Device tables cannot be checked before a kernel runs, so the kernels check them: a length below
  * 0 counts as 0 and one beyond its table row as the row's capacity, and a key whose table entry
  * is not in [0, num_pages) is absent (no query sees it).  What the cache holds outside the keys a
  * call's queries see (beyond the lengths, before the window) is never used, NaN included.
  *
- * These entry points and bitdelta_sample came with ABI 7, without a new number: a program that may meet
- * an older library looks them up by name.
+ * These entry points, bitdelta_sample, and later bitdelta_cache_write, bitdelta_cache_read and with them
+ * BITDELTA_KV_FP4 came with ABI 7, without a new number: a program that may meet an older library looks
+ * them up by name.
  *
  * Limits (else UNSUPPORTED): head_dim 64 or 128, at most 64 query heads per kv head, 1024
  * sequences per call, 2^30 tokens per sequence, 2^30 query rows (tokens x heads), 2^21 (sequence, kv
@@ -466,22 +467,33 @@ int64_t bitdelta_residency_used_bytes(bitdelta_residency* r);
 
 typedef enum {
   BITDELTA_KV_BF16 = 0,
-  BITDELTA_KV_FP8 = 1 /* OCP e4m3 */
+  BITDELTA_KV_FP8 = 1, /* OCP e4m3                                                              */
+  BITDELTA_KV_FP4 = 2  /* OCP e2m1 codes, one e8m0 scale byte per 32 values (below)             */
 } bitdelta_kv_dtype;
 
+/*
+ * BITDELTA_KV_FP4 (4.25 bits a value): two codes a byte, the lower four bits first, so that a row of
+ * head_dim values is head_dim / 2 bytes; the 32 values of a block (values 32 i .. 32 i + 31 of a row)
+ * have one scale byte b and stand for code * 2^(b - 127), b = 255 for 32 NaN.  The scale bytes of a
+ * row, head_dim / 32 of them, lie in an array that is an image of the pages at a 16th of the size: those
+ * of the row at k + o bytes at k_block_scales + o / 16, with the same page, token and head strides.
+ */
 typedef struct {
-  const void* k; /* [dev] keys, 16-byte aligned                                                 */
-  const void* v; /* [dev] values, 16-byte aligned                                               */
+  const void* k; /* [dev] keys, 16-byte aligned (bitdelta_cache_write writes here)              */
+  const void* v; /* [dev] values, 16-byte aligned (the same)                                    */
   int32_t dtype; /* bitdelta_kv_dtype                                                           */
   int32_t num_pages;
   int32_t page_size; /* tokens per page, any number >= 1                                        */
   int32_t kv_heads;
   int32_t head_dim;
-  /* strides in elements, each a multiple of 16 bytes (any value where the dimension is 1); the
-   * head_dim values of a row are contiguous */
+  /* strides in elements (of 4 bits with FP4), each a multiple of 16 bytes (FP4: of a row); any value
+   * where the dimension is 1; the head_dim values of a row are contiguous */
   int64_t k_stride_page, k_stride_token, k_stride_head;
   int64_t v_stride_page, v_stride_token, v_stride_head;
   float k_scale, v_scale; /* what a stored value is multiplied by; finite, > 0                  */
+  /* Read with BITDELTA_KV_FP4 only (a program built before these members came need not have them). */
+  const void* k_block_scales; /* [dev] scale bytes, 4-byte aligned                              */
+  const void* v_block_scales; /* [dev] the same                                                 */
 } bitdelta_kv_cache;
 
 /* Query and output rows: token t, head h at t * stride_token + h * stride_head (in elements; q's
@@ -559,6 +571,59 @@ size_t bitdelta_attend_window_workspace_bytes(int64_t tokens, int32_t heads,
                                               const bitdelta_kv_cache* cache, int32_t batch,
                                               int32_t table_width, int32_t max_q_len,
                                               int32_t window, int32_t sinks);
+
+/*
+ * ---- Writing and reading the paged cache ------------------------------------------------------
+ *
+ * Which token a row is, and so its place, goes by the tables that bitdelta_attend_window has: sequence
+ * b's rows are q_offsets[b] .. q_offsets[b + 1] - 1, and row q_offsets[b + 1] - 1 is the token at
+ * position lens[b] - 1 (the new tokens counted).  Without q_offsets each sequence has one row, its
+ * last token (then tokens = batch).  The token at position p is in slot p % page_size of page
+ * table[b][p / page_size].  It has no place where p is below 0 or beyond the table's row, or the entry
+ * is no page.
+ *
+ * Limits (else UNSUPPORTED): those of the cache above, BITDELTA_ATTEND_MAX_SEQS sequences, 2^16 kv heads,
+ * 2^30 rows (tokens x kv heads).
+ */
+
+/* Rows of keys and values: token t, kv head h at t * stride_token + h * stride_head (in elements,
+ * multiples of 8; any value for a single token or head), head_dim contiguous bf16 values, 16-byte
+ * aligned. */
+typedef struct {
+  void* k; /* [dev] bf16: read by bitdelta_cache_write, written by bitdelta_cache_read          */
+  void* v; /* [dev] bf16, the same                                                              */
+  int64_t tokens;
+  int64_t k_stride_token, k_stride_head, v_stride_token, v_stride_head;
+} bitdelta_kv_rows;
+
+/*
+ * bitdelta_cache_write — new keys and values into their pages, quantised on the way.  With y = x /
+ * k_scale (v_scale) in fp32, what is stored of a row's values x is
+ *   BF16  y rounded (x itself where the scale is 1);
+ *   FP8   y rounded, +-448 beyond; NaN for an infinity or NaN;
+ *   FP4   by blocks of 32: 2^e is the smallest power of two with max |y| <= 7 * 2^e, e in [-125, 125],
+ *         the scale byte e + 127, and a code is y / 2^e rounded, +-6 beyond.  No value below 7 * 2^125
+ *         is then off by more than half a step of its grid.  A block that holds an infinity or NaN
+ *         becomes NaN.
+ * Roundings are to nearest, ties to even.  A row without a place is not written, nor is anything else
+ * of the cache.  Two rows of a call with one place leave either's values there, or pieces of both.
+ * The rows must not overlap the cache.  tokens = 0 or batch = 0 is a no-op.  No workspace.
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT, UNSUPPORTED, HIP.
+ */
+bitdelta_status bitdelta_cache_write(const bitdelta_kv_rows* rows, const bitdelta_kv_cache* cache,
+                                     int32_t batch, const int32_t* table, int32_t table_width,
+                                     const int32_t* lens, const int32_t* q_offsets,
+                                     bitdelta_stream stream);
+
+/*
+ * bitdelta_cache_read — the same rows out of their pages: the stored values times k_scale (v_scale),
+ * one fp32 product rounded to bf16.  A row of a sequence without a place becomes zeros; rows of no
+ * sequence stay as they are.  Arguments and errors as bitdelta_cache_write.
+ */
+bitdelta_status bitdelta_cache_read(const bitdelta_kv_rows* rows, const bitdelta_kv_cache* cache,
+                                    int32_t batch, const int32_t* table, int32_t table_width,
+                                    const int32_t* lens, const int32_t* q_offsets,
+                                    bitdelta_stream stream);
 
 /*
  * bitdelta_sample — the next token of each row of logits from given uniform numbers.

@@ -23,6 +23,7 @@ __all__ = [
     "matmul_workspace_bytes", "sign_words_t128", "reconstruct", "upload_variant", "Residency",
     "matmul_grouped_noalloc", "NOALLOC_SCRATCH_BYTES", "attend_shared",
     "attend_shared_workspace_bytes", "attend_window", "attend_window_workspace_bytes", "sample",
+    "cache_write", "cache_read",
 ]
 
 ABI_VERSION = 7
@@ -68,6 +69,15 @@ class _KvCache(ctypes.Structure):
         ("k_stride_head", ctypes.c_int64), ("v_stride_page", ctypes.c_int64),
         ("v_stride_token", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
         ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+        ("k_block_scales", ctypes.c_void_p), ("v_block_scales", ctypes.c_void_p),
+    ]
+
+
+class _KvRows(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+        ("k_stride_token", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+        ("v_stride_token", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
     ]
 
 
@@ -97,7 +107,8 @@ def _lib():
         import torch  # noqa: F401
         L = ctypes.CDLL(LIB_PATH)
         # entry points that came without a new ABI version
-        for name in ("bitdelta_attend_shared", "bitdelta_attend_window", "bitdelta_sample"):
+        for name in ("bitdelta_attend_shared", "bitdelta_attend_window", "bitdelta_sample",
+                     "bitdelta_cache_write", "bitdelta_cache_read"):
             if not hasattr(L, name):
                 raise RuntimeError(f"{LIB_PATH} has no {name}: it is older than this package; run "
                                    "__graft_entry__.build() again")
@@ -203,6 +214,10 @@ def _lib():
         L.bitdelta_attend_window_workspace_bytes.argtypes = [
             ctypes.c_int64, ctypes.c_int32, cache_p, ctypes.c_int32, ctypes.c_int32,
             ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]
+        for f in (L.bitdelta_cache_write, L.bitdelta_cache_read):
+            f.restype = ctypes.c_int
+            f.argtypes = [ctypes.POINTER(_KvRows), cache_p, ctypes.c_int32, ctypes.c_void_p,
+                          ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
         L.bitdelta_sample.restype = ctypes.c_int
         L.bitdelta_sample.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                       ctypes.c_int64, ctypes.c_int64, *[ctypes.c_void_p] * 8]
@@ -685,28 +700,69 @@ def upload_variant(host_words, host_alpha, d_out: int, d_in: int, words=None, ti
 _KV_DTYPES = {}  # torch dtype -> bitdelta_kv_dtype
 
 
-def _kv_cache(k_pages, v_pages, k_scale, v_scale):
+def _block_scales(pages, scales, what):
+    """Address of a 4-bit cache's scale bytes: [pages, page_size, kv_heads, head_dim / 32] laid out as
+    the pages are, at a 16th of their byte offsets."""
+    import torch
+    if not isinstance(scales, torch.Tensor) or not scales.is_cuda:
+        raise TypeError(f"{what}_block_scales must be a CUDA/HIP torch tensor (4-bit pages have them)")
+    if scales.dtype is not torch.uint8:
+        raise TypeError(f"{what}_block_scales must be torch.uint8, got {scales.dtype}")
+    if scales.device != pages.device:
+        raise ValueError(f"{what}_block_scales are on {scales.device}, the pages on {pages.device}")
+    shape = pages.shape
+    if scales.shape != (shape[0], shape[1], shape[2], shape[3] // 16):
+        raise ValueError(f"{what}_block_scales have shape {tuple(scales.shape)}, need "
+                         f"{(*shape[:3], shape[3] // 16)}")
+    ps, ss = pages.stride(), scales.stride()
+    if ss[3] != 1 or any(n > 1 and p != 16 * b for n, p, b in zip(shape[:3], ps, ss)):
+        raise ValueError(f"{what}_block_scales must be laid out as the pages: strides of a 16th of theirs "
+                         f"({ps[:3]}), not {ss[:3]}, and contiguous rows")
+    return scales.data_ptr()
+
+
+def _kv_cache(k_pages, v_pages, k_scale, v_scale, k_block_scales=None, v_block_scales=None):
     """bitdelta_kv_cache of two [pages, page_size, kv_heads, head_dim] tensors (bf16 or
-    float8_e4m3fn), any strides but contiguous rows."""
+    float8_e4m3fn; uint8, two 4-bit codes each, [.., head_dim / 2]), any strides but contiguous rows."""
     import torch
     if not _KV_DTYPES:
-        _KV_DTYPES.update({torch.bfloat16: 0, torch.float8_e4m3fn: 1})
+        _KV_DTYPES.update({torch.bfloat16: 0, torch.float8_e4m3fn: 1, torch.uint8: 2})
     for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{what} must be a CUDA/HIP torch tensor")
     shape, dtype = k_pages.shape, k_pages.dtype
     code = _KV_DTYPES.get(dtype)
     if code is None or v_pages.dtype is not dtype:
-        raise TypeError("k_pages and v_pages must both be torch.bfloat16 or torch.float8_e4m3fn, "
-                        f"got {dtype} and {v_pages.dtype}")
+        raise TypeError("k_pages and v_pages must both be torch.bfloat16, torch.float8_e4m3fn or (4 bits) "
+                        f"torch.uint8, got {dtype} and {v_pages.dtype}")
     if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [pages, page_size, kv_heads, head_dim], "
                          "of one shape")
     ks, vs = k_pages.stride(), v_pages.stride()
     if shape[3] > 1 and (ks[3] != 1 or vs[3] != 1):
         raise ValueError("k_pages and v_pages must have contiguous rows")
+    if code != 2:
+        if k_block_scales is not None or v_block_scales is not None:
+            raise ValueError(f"pages of {dtype} have no block scales")
+        return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), code, shape[0], shape[1], shape[2],
+                        shape[3], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], k_scale, v_scale)
+    if v_pages.device != k_pages.device:
+        raise ValueError(f"v_pages are on {v_pages.device}, k_pages on {k_pages.device}")
     return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), code, shape[0], shape[1], shape[2],
-                    shape[3], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], k_scale, v_scale)
+                    2 * shape[3], 2 * ks[0], 2 * ks[1], 2 * ks[2], 2 * vs[0], 2 * vs[1], 2 * vs[2],
+                    k_scale, v_scale, _block_scales(k_pages, k_block_scales, "k"),
+                    _block_scales(v_pages, v_block_scales, "v"))
+
+
+def _cache_sizes(k_pages):
+    """The same for a query of workspace sizes: no scales are looked at."""
+    import torch
+    if k_pages.dtype is not torch.uint8:
+        return _kv_cache(k_pages, k_pages, 1.0, 1.0)
+    shape, ks = k_pages.shape, k_pages.stride()
+    p = k_pages.data_ptr()
+    return _KvCache(p, p, 2, shape[0], shape[1], shape[2], 2 * shape[3], *[2 * x for x in ks[:3]],
+                    *[2 * x for x in ks[:3]], 1.0, 1.0, p, p)
 
 
 def _attend_rows(q, cache, out, lse, return_lse, scale, stream):
@@ -762,7 +818,7 @@ def _host_i32(a):
 def attend_shared_workspace_bytes(k_pages, heads, table, prefix_table, seg_offsets) -> int:
     """Device workspace an attend_shared call with these tables needs (bytes, 0 if none)."""
     offs, offs_p = _host_i32(seg_offsets)
-    c = _kv_cache(k_pages, k_pages, 1.0, 1.0)
+    c = _cache_sizes(k_pages)
     pwidth = 0 if prefix_table is None else int(prefix_table.shape[1])
     return int(_lib().bitdelta_attend_shared_workspace_bytes(
         int(table.shape[0]), heads, ctypes.byref(c), int(table.shape[1]), pwidth, offs_p,
@@ -771,7 +827,7 @@ def attend_shared_workspace_bytes(k_pages, heads, table, prefix_table, seg_offse
 
 def attend_shared(q, k_pages, v_pages, table, lens, prefix_table, prefix_lens, seg_offsets,
                   scale=None, k_scale=1.0, v_scale=1.0, out=None, lse=None, return_lse=False,
-                  workspace=None, stream=None):
+                  workspace=None, stream=None, k_block_scales=None, v_block_scales=None):
     """Decode attention, one new token per sequence, over a paged cache whose prefixes are shared
     by segment: sequence b of segment g (``seg_offsets`` as plan_segments returns them) sees the
     first ``prefix_lens[g]`` tokens of ``prefix_table[g]``, then the first ``lens[b]`` of
@@ -779,13 +835,13 @@ def attend_shared(q, k_pages, v_pages, table, lens, prefix_table, prefix_lens, s
 
     ``q``: bf16 [batch, heads, head_dim]; ``k_pages`` / ``v_pages``: [pages, page_size, kv_heads,
     head_dim] bf16 or float8_e4m3fn (each stored value times ``k_scale`` / ``v_scale``), any
-    strides but contiguous rows; ``table`` int32 [batch, n], ``lens`` int32 [batch],
+    strides but contiguous rows, or 4-bit pages with their block scales (see cache_write); ``table`` int32 [batch, n], ``lens`` int32 [batch],
     ``prefix_table`` int32 [segments, m] and ``prefix_lens`` int32 [segments] (both None: no
     prefixes), on the device.  Returns bf16 ``out`` like q, and with ``return_lse`` (or ``lse``
     given) also the natural log of each row's softmax sum, float32 [batch, heads].  A sequence
     with no keys gives zeros and -inf."""
     offs, offs_p = _host_i32(seg_offsets)
-    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale)
+    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale, k_block_scales, v_block_scales)
     rows, out, lse = _attend_rows(q, cache, out, lse, return_lse, scale, stream)
     tptr, width, lptr = _table(table, lens, rows.tokens, "table")
     if offs.size < 1:
@@ -807,7 +863,7 @@ def attend_shared(q, k_pages, v_pages, table, lens, prefix_table, prefix_lens, s
 
 def attend_window_workspace_bytes(k_pages, heads, table, tokens, max_q_len, window, sinks) -> int:
     """Device workspace an attend_window call of these sizes needs (bytes, 0 if none)."""
-    c = _kv_cache(k_pages, k_pages, 1.0, 1.0)
+    c = _cache_sizes(k_pages)
     return int(_lib().bitdelta_attend_window_workspace_bytes(
         tokens, heads, ctypes.byref(c), int(table.shape[0]), int(table.shape[1]), max_q_len,
         window, sinks))
@@ -815,7 +871,7 @@ def attend_window_workspace_bytes(k_pages, heads, table, tokens, max_q_len, wind
 
 def attend_window(q, k_pages, v_pages, table, lens, window, sinks=0, q_offsets=None, max_q_len=None,
                   scale=None, k_scale=1.0, v_scale=1.0, out=None, lse=None, return_lse=False,
-                  workspace=None, stream=None):
+                  workspace=None, stream=None, k_block_scales=None, v_block_scales=None):
     """Causal attention of each sequence's last tokens over a paged cache, with a sliding window
     and first tokens that stay visible: the token at position p sees key j iff j <= p and
     (p - j < ``window`` or j < ``sinks``).  Sequence b holds ``lens[b]`` keys, its new tokens
@@ -826,7 +882,7 @@ def attend_window(q, k_pages, v_pages, table, lens, window, sinks=0, q_offsets=N
     longest chunk (None: 1 without q_offsets, else the number of tokens; the real length picks better
     kernels); a chunk's rows beyond its first ``max_q_len`` are not computed.  Cache, tables, scales
     and results as for attend_shared."""
-    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale)
+    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale, k_block_scales, v_block_scales)
     rows, out, lse = _attend_rows(q, cache, out, lse, return_lse, scale, stream)
     batch = lens.shape[0] if lens.dim() == 1 else -1
     tptr, width, lptr = _table(table, lens, batch, "table")
@@ -843,6 +899,98 @@ def attend_window(q, k_pages, v_pages, table, lens, window, sinks=0, q_offsets=N
         ctypes.byref(rows), ctypes.byref(cache), batch, tptr, width, lptr, optr, max_q_len, window,
         sinks, ws_ptr, ws_bytes, _raw_stream(stream, q)), "bitdelta_attend_window")
     return out if lse is None else (out, lse)
+
+
+# ---------------------------------------------------------------------------------------------
+# Writing and reading the paged cache
+# ---------------------------------------------------------------------------------------------
+
+def _kv_rows(k, v, cache, device):
+    """bitdelta_kv_rows of two bf16 [tokens, kv_heads, head_dim] tensors."""
+    import torch
+    for t, what in ((k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{what} must be a CUDA/HIP torch tensor")
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{what} must be torch.bfloat16, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{what} is on {t.device}, the pages on {device}")
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != cache.kv_heads or shape[2] != cache.head_dim or v.shape != shape:
+        raise ValueError(f"k and v must be [tokens, {cache.kv_heads}, {cache.head_dim}], not "
+                         f"{tuple(shape)} and {tuple(v.shape)}")
+    ks, vs = k.stride(), v.stride()
+    if shape[0] and (ks[2] != 1 or vs[2] != 1):
+        raise ValueError("k and v must have contiguous rows")
+    return _KvRows(k.data_ptr(), v.data_ptr(), shape[0], ks[0], ks[1], vs[0], vs[1])
+
+
+def _cache_places(table, lens, q_offsets, device):
+    """(batch, table pointer, width, lens pointer, q_offsets pointer)."""
+    import torch
+    batch = lens.shape[0] if lens.dim() == 1 else -1
+    tptr, width, lptr = _table(table, lens, batch, "table")
+    optr = None
+    if q_offsets is not None:
+        _check_shape(q_offsets, (batch + 1,), "q_offsets")
+        optr = _dev(q_offsets, "torch.int32", "q_offsets")
+    if table.device != device or lens.device != device or (optr and q_offsets.device != device):
+        raise ValueError(f"table, lens and q_offsets must be on {device}, as the pages")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the pages are on {device}, which is not the current device")
+    return batch, tptr, width, lptr, optr
+
+
+def cache_write(k, v, k_pages, v_pages, table, lens, q_offsets=None, k_scale=1.0, v_scale=1.0,
+                k_block_scales=None, v_block_scales=None, stream=None):
+    """New keys and values into their pages, quantised on the way.  Which token a row is goes by the
+    tables as attend_window has them: sequence b holds ``lens[b]`` tokens, its new ones among them as the
+    last ones, which are rows q_offsets[b] .. q_offsets[b + 1] (int32 [batch + 1] on the device; None: one
+    token per sequence).  Rows whose token has no page in the table are not written.
+
+    ``k`` / ``v``: bf16 [tokens, kv_heads, head_dim], contiguous rows.  ``k_pages`` / ``v_pages``:
+    [pages, page_size, kv_heads, head_dim] bf16 or float8_e4m3fn, which get each value divided by
+    ``k_scale`` / ``v_scale`` and rounded (float8: at most +-448), or, in 4 bits, uint8 [..., head_dim /
+    2] with ``k_block_scales`` / ``v_block_scales``, uint8 [..., head_dim / 32] of a 16th of the pages'
+    strides: each 32 values of a row share a power of two, byte - 127, such that the largest is at most 7
+    of them, and are rounded to 0, 0.5, 1, 1.5, 2, 3, 4 or 6 of them (lower four bits first).  Infinities
+    and NaN become NaN, in 4 bits with the 32 values around them.  Returns (k_pages, v_pages)."""
+    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale, k_block_scales, v_block_scales)
+    device = k_pages.device
+    rows = _kv_rows(k, v, cache, device)
+    batch, tptr, width, lptr, optr = _cache_places(table, lens, q_offsets, device)
+    _check(_lib().bitdelta_cache_write(ctypes.byref(rows), ctypes.byref(cache), batch, tptr, width, lptr,
+                                       optr, _raw_stream(stream, k_pages)), "bitdelta_cache_write")
+    return k_pages, v_pages
+
+
+def cache_read(k_pages, v_pages, table, lens, q_offsets=None, tokens=None, k_scale=1.0, v_scale=1.0,
+               k_block_scales=None, v_block_scales=None, k_out=None, v_out=None, stream=None):
+    """The rows cache_write wrote by these tables, read back: bf16 (k, v) [tokens, kv_heads, head_dim],
+    each stored value times ``k_scale`` / ``v_scale``.  With q_offsets, ``tokens`` (or ``k_out`` and
+    ``v_out``) says how many rows there are; q_offsets that begin at 0 and rise by ``lens`` read whole
+    sequences.  Tokens without a page are zeros; rows of no sequence stay as they are in k_out and v_out
+    (in results made here: anything)."""
+    import torch
+    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale, k_block_scales, v_block_scales)
+    device = k_pages.device
+    batch, tptr, width, lptr, optr = _cache_places(table, lens, q_offsets, device)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("give k_out and v_out, or neither")
+    if k_out is None:
+        if tokens is None:
+            if q_offsets is not None:
+                raise ValueError("with q_offsets, give tokens or k_out and v_out")
+            tokens = batch
+        shape = (tokens, cache.kv_heads, cache.head_dim)
+        k_out, v_out = (torch.empty(shape, dtype=torch.bfloat16, device=device) if stream is None else
+                        _empty(shape, torch.bfloat16, device, stream) for _ in "kv")
+    elif tokens is not None and k_out.shape[:1] != (tokens,):
+        raise ValueError(f"k_out has shape {tuple(k_out.shape)}, needs {tokens} tokens")
+    rows = _kv_rows(k_out, v_out, cache, device)
+    _check(_lib().bitdelta_cache_read(ctypes.byref(rows), ctypes.byref(cache), batch, tptr, width, lptr,
+                                      optr, _raw_stream(stream, k_pages)), "bitdelta_cache_read")
+    return k_out, v_out
 
 
 # ---------------------------------------------------------------------------------------------

@@ -41,6 +41,9 @@ struct PagedCache {
   int64_t k_head, v_head;       // bytes
   int32_t num_pages, page_size;
   PageDiv div;
+  // 4-bit cache: scale bytes, those of the row at byte o of k (v) at o / 16
+  const unsigned char* k_blocks;
+  const unsigned char* v_blocks;
 };
 
 // Where a key sits: page id and slot, id -1 when the table has no such page (entry out of range).

@@ -7,6 +7,7 @@
 
 #include "../../include/bitdelta.h"
 #include "attend.h"
+#include "cache.h"
 
 namespace bd {
 bitdelta_status status_of_hip(hipError_t e);
@@ -53,7 +54,7 @@ bool tiles_for_rows(int64_t rows, int64_t units) {
   return rows > 64 || (rows > 32 && units >= 64) || (rows > 16 && units >= 192);
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using bd::aligned;
 
 enum class Kind { kRows, kRowsSplit, kPrefixTiles, kTiles };
 
@@ -84,31 +85,6 @@ void lay_out(Plan* p, int64_t batch, int dim) {
     p->tile_ml = up256(slots * 8);
   }
   p->total = p->scan_bytes + p->row_o + p->row_ml + 2 * p->segs_bytes + p->tile_o + p->tile_ml;
-}
-
-bitdelta_status check_cache(const bitdelta_kv_cache* c, int32_t heads) {
-  if (!c) return BITDELTA_ERR_INVALID_ARG;
-  if (c->dtype != BITDELTA_KV_BF16 && c->dtype != BITDELTA_KV_FP8) return BITDELTA_ERR_INVALID_ARG;
-  if (!c->k || !c->v || c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || heads < 1)
-    return BITDELTA_ERR_INVALID_ARG;
-  if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || !isfinite(c->k_scale) || !isfinite(c->v_scale))
-    return BITDELTA_ERR_INVALID_ARG;
-  if (heads % c->kv_heads != 0) return BITDELTA_ERR_SHAPE;
-  if (c->head_dim != 64 && c->head_dim != 128) return BITDELTA_ERR_UNSUPPORTED;
-  if (heads / c->kv_heads > BITDELTA_ATTEND_MAX_GROUP) return BITDELTA_ERR_UNSUPPORTED;
-  const int64_t unit = c->dtype == BITDELTA_KV_FP8 ? 16 : 8;  // elements of 16 bytes
-  // strides of dimensions of one element are never stepped over: any value will do
-  const struct { int64_t stride; int32_t n; } steps[] = {
-      {c->k_stride_page, c->num_pages}, {c->k_stride_token, c->page_size}, {c->k_stride_head, c->kv_heads},
-      {c->v_stride_page, c->num_pages}, {c->v_stride_token, c->page_size}, {c->v_stride_head, c->kv_heads}};
-  for (const auto& s : steps) {
-    if (s.n == 1) continue;
-    if (s.stride < 0) return BITDELTA_ERR_INVALID_ARG;
-    if (s.stride % unit != 0) return BITDELTA_ERR_ALIGNMENT;
-    if (s.stride / unit > 0xFFFFFFFFll) return BITDELTA_ERR_UNSUPPORTED;
-  }
-  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return BITDELTA_ERR_ALIGNMENT;
-  return BITDELTA_OK;
 }
 
 // what scores are multiplied by to enter exp2
@@ -200,7 +176,6 @@ Plan plan_window(int32_t heads, const bitdelta_kv_cache& c, int32_t batch, int32
 }
 
 void fill(bd::AttendArgs* a, const bitdelta_attend_rows& r, const bitdelta_kv_cache& c) {
-  const int64_t es = c.dtype == BITDELTA_KV_FP8 ? 1 : 2;
   a->q = static_cast<const uint16_t*>(r.q);
   a->q_token = r.q_stride_token;
   a->q_head = r.q_stride_head;
@@ -208,17 +183,7 @@ void fill(bd::AttendArgs* a, const bitdelta_attend_rows& r, const bitdelta_kv_ca
   a->o_token = r.out_stride_token;
   a->o_head = r.out_stride_head;
   a->lse = r.lse;
-  a->cache.k = static_cast<const unsigned char*>(c.k);
-  a->cache.v = static_cast<const unsigned char*>(c.v);
-  a->cache.k_page = (uint32_t)(c.k_stride_page * es / 16);
-  a->cache.k_token = (uint32_t)(c.k_stride_token * es / 16);
-  a->cache.k_head = c.k_stride_head * es;
-  a->cache.v_page = (uint32_t)(c.v_stride_page * es / 16);
-  a->cache.v_token = (uint32_t)(c.v_stride_token * es / 16);
-  a->cache.v_head = c.v_stride_head * es;
-  a->cache.num_pages = c.num_pages;
-  a->cache.page_size = c.page_size;
-  a->cache.div = bd::make_page_div((uint32_t)c.page_size);
+  a->cache = bd::paged_cache(c);
   a->tokens = (int32_t)r.tokens;
   a->heads = r.heads;
   a->kv_heads = c.kv_heads;
@@ -296,7 +261,8 @@ bool steps_fit(int64_t sequences, int64_t keys) {
 
 bool shared_sizes_ok(int64_t tokens, int32_t heads, const bitdelta_kv_cache* cache, int32_t width,
                      int32_t pwidth, const int32_t* offs, int32_t nseg, bitdelta_status* s) {
-  *s = check_cache(cache, heads);
+  *s = bd::check_kv_cache(cache, heads);
+  if (*s == BITDELTA_OK && cache->dtype == BITDELTA_KV_FP4) *s = BITDELTA_ERR_UNSUPPORTED;
   if (*s == BITDELTA_OK && (width < 0 || pwidth < 0)) *s = BITDELTA_ERR_INVALID_ARG;
   if (*s == BITDELTA_OK) *s = check_segments(tokens, offs, nseg);
   if (*s == BITDELTA_OK && (tokens > BITDELTA_ATTEND_MAX_SEQS || tokens * heads > kMaxRows ||
@@ -310,7 +276,8 @@ bool shared_sizes_ok(int64_t tokens, int32_t heads, const bitdelta_kv_cache* cac
 bitdelta_status check_window(int64_t tokens, int32_t heads, const bitdelta_kv_cache* cache,
                              int32_t batch, int32_t width, int32_t max_q, int32_t window,
                              int32_t sinks) {
-  bitdelta_status s = check_cache(cache, heads);
+  bitdelta_status s = bd::check_kv_cache(cache, heads);
+  if (s == BITDELTA_OK && cache->dtype == BITDELTA_KV_FP4) s = BITDELTA_ERR_UNSUPPORTED;
   if (s != BITDELTA_OK) return s;
   if (batch < 0 || width < 0 || max_q < 1 || window < 1 || sinks < 0) return BITDELTA_ERR_INVALID_ARG;
   if (batch > BITDELTA_ATTEND_MAX_SEQS || (int64_t)width * cache->page_size > kMaxKeys ||

@@ -1,0 +1,287 @@
+// Writing new keys and values into a paged cache, quantised on the way, and reading tokens back.
+//
+// Mathematics, per value x of a row, y = x / scale in fp32:
+//   bf16  y rounded;   e4m3  min(max(y, -448), 448) rounded;
+//   4 bits, per 32 consecutive values: 2^e = the smallest power of two with max |y| <= 7 * 2^e (then
+//   every |y| / 2^e is at most half a step of {0, .5, 1, 1.5, 2, 3, 4, 6} away from it; 6.5 or more
+//   would be off by more with the usual choice, the largest power of two below max |y| / 4), code = the
+//   nearest one, ties to even, by the conversion instruction.
+// The quotient is a product where 1 / scale is exact, else a correctly rounded division.
+//
+// Bound by memory: 4 bytes of bf16 and 2 * 17/32 (4 bits) to 4 stored bytes per pair of a key and a
+// value.  A thread takes 8 values (16 bytes of bf16) of one row at a time, so that a wave's loads and
+// stores are whole lines, and 4 lanes hold a block of 32 (its largest value by two lane moves); each of
+// a workgroup's tokens is looked up once, by one thread.
+#include "bd_internal.h"
+#include "cache.h"
+
+namespace bd {
+namespace {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 64;  // of a workgroup at a time
+constexpr int kAhead = 4;       // loads of a thread in flight
+
+// Where a token's head 0 rows sit in the pages, byte offsets; k below 0: nowhere.  row: its sequence has
+// it (a place or not).
+struct TokenPlace {
+  int64_t k, v;
+  bool row;
+};
+
+// offsets: the call's q_offsets in LDS
+__device__ __forceinline__ TokenPlace token_place(const CacheArgs& a, const int* offsets, int t) {
+  TokenPlace at{-1, -1, false};
+  int b = t;
+  int64_t pos;
+  if (a.q_offsets) {
+    // the last sequence that begins at or before row t; empty ones end before it
+    int lo = 0, hi = a.batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (offsets[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    const int end = offsets[b + 1];
+    if (t < offsets[b] || t >= end) return at;
+    pos = (int64_t)a.lens[b] - ((int64_t)end - t);
+  } else {
+    pos = (int64_t)a.lens[b] - 1;
+  }
+  at.row = true;
+  if (pos < 0) return at;
+  const int page = page_quotient((int)pos, a.cache.div);
+  if (page >= a.width) return at;
+  const int id = page_id_checked(a.table[(int64_t)b * a.width + page], a.cache.num_pages);
+  if (id < 0) return at;
+  const int slot = (int)pos - page * a.cache.page_size;
+  at.k = page_row_bytes(id, slot, a.cache.k_page, a.cache.k_token);
+  at.v = page_row_bytes(id, slot, a.cache.v_page, a.cache.v_token);
+  return at;
+}
+
+__device__ __forceinline__ unsigned pack_bf16(float a, float b) {
+  f32x2 f;
+  f[0] = a;
+  f[1] = b;
+  return __builtin_bit_cast(unsigned, __builtin_convertvector(f, bf16x2));
+}
+
+__device__ __forceinline__ u16x2 max2(u16x2 a, u16x2 b) { return __builtin_elementwise_max(a, b); }
+// max over the 4 lanes of a block, in each
+__device__ __forceinline__ unsigned block_max(unsigned m) {
+  const unsigned x = max(m, (unsigned)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));
+  return max(x, (unsigned)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float quotient(float x, float scale, float inverse) {
+  return inverse != 0.f ? x * inverse : x / scale;
+}
+
+// 8 bf16 values -> what is stored of them, at unit `part` of row `to` (blocks: its scale bytes)
+template <int KV>
+__device__ __forceinline__ void store8(const u32x4& x, unsigned char* to, unsigned char* blocks, int part,
+                                       float scale, float inverse) {
+  if constexpr (KV == BITDELTA_KV_BF16) {
+    u32x4 r = x;
+    if (scale != 1.f) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[i] = pack_bf16(quotient(bf16lo_to_f32(x[i]), scale, inverse),
+                         quotient(bf16hi_to_f32(x[i]), scale, inverse));
+    }
+    *reinterpret_cast<u32x4*>(to + 16 * part) = r;
+  } else if constexpr (KV == BITDELTA_KV_FP8) {
+    u32x2 r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = e & 1 ? bf16hi_to_f32(x[2 * i + (e >> 1)]) : bf16lo_to_f32(x[2 * i + (e >> 1)]);
+        // (the comparison before the bounds, which would turn a NaN or an infinity into 448)
+        y[e] = __builtin_isfinite(f) ? fminf(fmaxf(quotient(f, scale, inverse), -448.f), 448.f)
+                                     : __builtin_nanf("");
+      }
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+      r[i] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+    }
+    *reinterpret_cast<u32x2*>(to + 8 * part) = r;
+  } else {
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max2(m, __builtin_bit_cast(u16x2, x[i] & 0x7FFF7FFFu));
+    const unsigned top = block_max(max((unsigned)m[0], (unsigned)m[1]));  // bf16 bits of max |x|
+    // division is monotonic: the quotient of the largest is the largest quotient
+    const float q = fminf(quotient(__uint_as_float(top << 16), scale, inverse), 3.402823466e38f);
+    // the exponent of q, one more where its fraction is above 1.75, two less
+    int byte = (int)((__float_as_uint(q) + 0x1FFFFFu) >> 23) - 2;
+    byte = min(max(byte, 2), 252);
+    const float step = __uint_as_float((unsigned)byte << 23);
+    unsigned r = 0;
+    if (top < 0x7F80u) {
+      auto lo = [&](int i) { return quotient(bf16lo_to_f32(x[i]), scale, inverse); };
+      auto hi = [&](int i) { return quotient(bf16hi_to_f32(x[i]), scale, inverse); };
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, lo(0), hi(0), step, 0);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, lo(1), hi(1), step, 1);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, lo(2), hi(2), step, 2);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, lo(3), hi(3), step, 3);
+    } else {
+      byte = 255;
+    }
+    *reinterpret_cast<unsigned*>(to + 4 * part) = r;
+    if ((part & 3) == 0) blocks[part >> 2] = (unsigned char)byte;
+  }
+}
+
+// what 8 values of a row are read as: the stored bytes, and with 4 bits the block's scale byte
+struct Stored {
+  u32x4 r;
+  unsigned byte;
+};
+template <int KV>
+__device__ __forceinline__ Stored load8(const unsigned char* from, const unsigned char* blocks, int part) {
+  Stored s{};
+  if constexpr (KV == BITDELTA_KV_BF16) {
+    s.r = *reinterpret_cast<const u32x4*>(from + 16 * part);
+  } else if constexpr (KV == BITDELTA_KV_FP8) {
+    const u32x2 x = *reinterpret_cast<const u32x2*>(from + 8 * part);
+    s.r[0] = x[0];
+    s.r[1] = x[1];
+  } else {
+    s.r[0] = *reinterpret_cast<const unsigned*>(from + 4 * part);
+    s.byte = blocks[part >> 2];
+  }
+  return s;
+}
+template <int KV>
+__device__ __forceinline__ u32x4 values8(const Stored& s, float scale) {
+  u32x4 r;
+  if constexpr (KV == BITDELTA_KV_BF16) {
+    r = s.r;
+  } else if constexpr (KV == BITDELTA_KV_FP8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[i] = i & 1 ? __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s.r[i >> 1], 1.0f, true))
+                   : __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s.r[i >> 1], 1.0f, false));
+  } else {
+    const float step = __uint_as_float(s.byte << 23);
+    r[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(s.r[0], step, 0));
+    r[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(s.r[0], step, 1));
+    r[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(s.r[0], step, 2));
+    r[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(s.r[0], step, 3));
+  }
+  if (scale != 1.f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = pack_bf16(bf16lo_to_f32(r[i]) * scale, bf16hi_to_f32(r[i]) * scale);
+  }
+  return r;
+}
+
+// One workgroup takes `per` tokens at a time; its threads go over the 8-value units of their rows: a
+// token's kv_heads key rows, then its value rows.
+template <int D, int KV, bool WRITE>
+__global__ __launch_bounds__(kThreads) void cache_kernel(const CacheArgs a, int per) {
+  constexpr int kUnits = D / 8;
+  __shared__ int offsets[kAttendMaxSeqs + 1];
+  __shared__ TokenPlace places[kMaxTokens];
+  const int tid = threadIdx.x;
+  if (a.q_offsets) {
+    for (int i = tid; i <= a.batch; i += kThreads) offsets[i] = a.q_offsets[i];
+    __syncthreads();
+  }
+  const int64_t stride = (int64_t)gridDim.x * per;
+  for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < a.tokens; t0 += stride) {
+    const int n = a.tokens - t0 < per ? (int)(a.tokens - t0) : per;
+    if (tid < n) places[tid] = token_place(a, offsets, (int)t0 + tid);
+    __syncthreads();
+    const int units = n * 2 * a.kv_heads * kUnits;
+    for (int base = 0; base < units; base += kThreads * kAhead) {
+      u32x4 x[kAhead];
+      Stored s[kAhead];
+      uint16_t* row[kAhead];
+      unsigned char* at[kAhead];
+      unsigned char* blocks[kAhead];
+      int part[kAhead], v[kAhead];
+      bool live[kAhead], placed[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int u = base + i * kThreads + tid;
+        const int r = u / kUnits;
+        const int tok = page_quotient(r, a.heads_div);
+        int h = r - tok * 2 * a.kv_heads;
+        v[i] = h >= a.kv_heads;
+        h -= v[i] ? a.kv_heads : 0;
+        part[i] = u & (kUnits - 1);
+        live[i] = u < units;
+        placed[i] = false;
+        if (!live[i]) continue;
+        const TokenPlace& p = places[tok];
+        const int64_t o = (v[i] ? p.v : p.k) + (int64_t)h * (v[i] ? a.cache.v_head : a.cache.k_head);
+        placed[i] = p.k >= 0;
+        live[i] = WRITE ? placed[i] : p.row;
+        at[i] = const_cast<unsigned char*>(v[i] ? a.cache.v : a.cache.k) + o;
+        blocks[i] = const_cast<unsigned char*>(v[i] ? a.cache.v_blocks : a.cache.k_blocks) + (o >> 4);
+        row[i] = a.rows[v[i]] + (t0 + tok) * a.row_token[v[i]] + (int64_t)h * a.row_head[v[i]] + 8 * part[i];
+        if constexpr (WRITE) {
+          if (placed[i]) x[i] = *reinterpret_cast<const u32x4*>(row[i]);
+        } else {
+          if (placed[i]) s[i] = load8<KV>(at[i], blocks[i], part[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (!live[i]) continue;
+        const float scale = v[i] ? a.scale[1] : a.scale[0];
+        if constexpr (WRITE)
+          store8<KV>(x[i], at[i], blocks[i], part[i], scale, v[i] ? a.inverse[1] : a.inverse[0]);
+        else
+          *reinterpret_cast<u32x4*>(row[i]) = placed[i] ? values8<KV>(s[i], scale) : u32x4{0, 0, 0, 0};
+      }
+    }
+    __syncthreads();  // the places are read
+  }
+}
+
+template <int D, int KV, bool WRITE>
+hipError_t launch(const CacheArgs& a, hipStream_t stream) {
+  // about 8 units a thread, fewer where that would leave compute units without a workgroup
+  int64_t per = 2048 / ((int64_t)a.kv_heads * (D / 4));
+  if (per > a.tokens / 512) per = a.tokens / 512;
+  per = per < 1 ? 1 : (per > kMaxTokens ? kMaxTokens : per);
+  int64_t blocks = (a.tokens + per - 1) / per;
+  if (blocks > (1 << 20)) blocks = 1 << 20;  // a launch holds fewer than 2^32 threads
+  clear_stale_error();
+  hipLaunchKernelGGL((cache_kernel<D, KV, WRITE>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a,
+                     (int)per);
+  return hipGetLastError();
+}
+
+template <bool WRITE>
+hipError_t launch_for(const CacheArgs& a, int dim, int dtype, hipStream_t stream) {
+  if (dim != 64 && dim != 128) return hipErrorInvalidValue;
+  if (dtype == BITDELTA_KV_BF16)
+    return dim == 64 ? launch<64, BITDELTA_KV_BF16, WRITE>(a, stream)
+                     : launch<128, BITDELTA_KV_BF16, WRITE>(a, stream);
+  if (dtype == BITDELTA_KV_FP8)
+    return dim == 64 ? launch<64, BITDELTA_KV_FP8, WRITE>(a, stream)
+                     : launch<128, BITDELTA_KV_FP8, WRITE>(a, stream);
+  if (dtype == BITDELTA_KV_FP4)
+    return dim == 64 ? launch<64, BITDELTA_KV_FP4, WRITE>(a, stream)
+                     : launch<128, BITDELTA_KV_FP4, WRITE>(a, stream);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_cache_write(const CacheArgs& a, int dim, int dtype, hipStream_t stream) {
+  return launch_for<true>(a, dim, dtype, stream);
+}
+hipError_t launch_cache_read(const CacheArgs& a, int dim, int dtype, hipStream_t stream) {
+  return launch_for<false>(a, dim, dtype, stream);
+}
+
+}  // namespace bd
