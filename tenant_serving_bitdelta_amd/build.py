@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbitdelta.so")
 
 SOURCES = ["compress.hip", "gemv.hip", "stream.hip", "split.hip", "prefill.hip", "reconstruct.hip",
-           "noalloc.hip", "attend.hip", "cache.hip", "sample.hip", "split_sched.cpp", "api.cpp", "residency.cpp", "attend_api.cpp", "cache_api.cpp",
+           "noalloc.hip", "attend.hip", "attend4.hip", "cache.hip", "sample.hip", "split_sched.cpp", "api.cpp", "residency.cpp", "attend_api.cpp", "cache_api.cpp",
            "sample_api.cpp"]
 ARCH = "gfx950"
 HIP_FLAGS = [

@@ -127,6 +127,10 @@ Plan plan_shared(int64_t batch, int32_t heads, const bitdelta_kv_cache& c, int32
                  int32_t pwidth, const int32_t* offs, int32_t nseg) {
   Plan p{};
   const int group = heads / c.kv_heads;
+  if (c.dtype == BITDELTA_KV_FP4) {
+    p.kind = Kind::kRows;
+    return p;
+  }
   p.row_rows = group;
   p.columns = columns_for(group);
   p.row_units = batch * c.kv_heads;
@@ -158,6 +162,10 @@ Plan plan_window(int32_t heads, const bitdelta_kv_cache& c, int32_t batch, int32
   Plan p{};
   const int group = heads / c.kv_heads;
   const int64_t rows = (int64_t)max_q * group;
+  if (c.dtype == BITDELTA_KV_FP4) {
+    p.kind = Kind::kRows;
+    return p;
+  }
   if (tiles_for_rows(rows, (int64_t)batch * c.kv_heads)) {
     p.kind = Kind::kTiles;
     return p;
@@ -197,6 +205,10 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
   const bool fp8 = c.dtype == BITDELTA_KV_FP8;
   hipStream_t st = static_cast<hipStream_t>(stream);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
+  if (c.dtype == BITDELTA_KV_FP4) {
+    a->row_prefix = a->nseg > 0;
+    return bd::status_of_hip(bd::launch_attend4(*a, c.head_dim, st));
+  }
   a->rows = p.row_rows;
   a->workers = (int)p.row_workers;
   a->tile_workers = (int)p.tile_workers;
@@ -262,7 +274,6 @@ bool steps_fit(int64_t sequences, int64_t keys) {
 bool shared_sizes_ok(int64_t tokens, int32_t heads, const bitdelta_kv_cache* cache, int32_t width,
                      int32_t pwidth, const int32_t* offs, int32_t nseg, bitdelta_status* s) {
   *s = bd::check_kv_cache(cache, heads);
-  if (*s == BITDELTA_OK && cache->dtype == BITDELTA_KV_FP4) *s = BITDELTA_ERR_UNSUPPORTED;
   if (*s == BITDELTA_OK && (width < 0 || pwidth < 0)) *s = BITDELTA_ERR_INVALID_ARG;
   if (*s == BITDELTA_OK) *s = check_segments(tokens, offs, nseg);
   if (*s == BITDELTA_OK && (tokens > BITDELTA_ATTEND_MAX_SEQS || tokens * heads > kMaxRows ||
@@ -277,7 +288,6 @@ bitdelta_status check_window(int64_t tokens, int32_t heads, const bitdelta_kv_ca
                              int32_t batch, int32_t width, int32_t max_q, int32_t window,
                              int32_t sinks) {
   bitdelta_status s = bd::check_kv_cache(cache, heads);
-  if (s == BITDELTA_OK && cache->dtype == BITDELTA_KV_FP4) s = BITDELTA_ERR_UNSUPPORTED;
   if (s != BITDELTA_OK) return s;
   if (batch < 0 || width < 0 || max_q < 1 || window < 1 || sinks < 0) return BITDELTA_ERR_INVALID_ARG;
   if (batch > BITDELTA_ATTEND_MAX_SEQS || (int64_t)width * cache->page_size > kMaxKeys ||
