@@ -24,6 +24,7 @@ constexpr int64_t kMaxUnits = int64_t(1) << 21;  // sequences x kv heads
 // Workgroups of a split launch: as many as the 256 compute units hold at a time (more would start
 // when the first have ended, and take as long again), which their registers decide.
 int row_workers(int columns, int64_t max_q, const bitdelta_kv_cache& c) {
+  if (c.dtype == BITDELTA_KV_FP4) return columns == 1 ? 768 : (columns == 2 ? 512 : 256);
   if (columns == 1 && max_q == 1 && (c.dtype == BITDELTA_KV_FP8 || c.head_dim == 64)) return 768;
   return columns <= 2 ? 512 : 256;
 }
@@ -127,10 +128,6 @@ Plan plan_shared(int64_t batch, int32_t heads, const bitdelta_kv_cache& c, int32
                  int32_t pwidth, const int32_t* offs, int32_t nseg) {
   Plan p{};
   const int group = heads / c.kv_heads;
-  if (c.dtype == BITDELTA_KV_FP4) {
-    p.kind = Kind::kRows;
-    return p;
-  }
   p.row_rows = group;
   p.columns = columns_for(group);
   p.row_units = batch * c.kv_heads;
@@ -140,7 +137,7 @@ Plan plan_shared(int64_t batch, int32_t heads, const bitdelta_kv_cache& c, int32
   const int64_t row_bytes = 2 * (int64_t)c.head_dim * (c.dtype == BITDELTA_KV_FP8 ? 1 : 2);
   if (own + pre <= (int64_t)direct_steps(p.row_units) * bd::kRowStep) {
     p.kind = Kind::kRows;
-  } else if ((batch - used) * pre * c.kv_heads * row_bytes < kShareBytes) {
+  } else if (c.dtype == BITDELTA_KV_FP4 || (batch - used) * pre * c.kv_heads * row_bytes < kShareBytes) {
     p.kind = Kind::kRowsSplit;
   } else {
     p.kind = Kind::kPrefixTiles;
@@ -162,10 +159,6 @@ Plan plan_window(int32_t heads, const bitdelta_kv_cache& c, int32_t batch, int32
   Plan p{};
   const int group = heads / c.kv_heads;
   const int64_t rows = (int64_t)max_q * group;
-  if (c.dtype == BITDELTA_KV_FP4) {
-    p.kind = Kind::kRows;
-    return p;
-  }
   if (tiles_for_rows(rows, (int64_t)batch * c.kv_heads)) {
     p.kind = Kind::kTiles;
     return p;
@@ -205,10 +198,6 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
   const bool fp8 = c.dtype == BITDELTA_KV_FP8;
   hipStream_t st = static_cast<hipStream_t>(stream);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  if (c.dtype == BITDELTA_KV_FP4) {
-    a->row_prefix = a->nseg > 0;
-    return bd::status_of_hip(bd::launch_attend4(*a, c.head_dim, st));
-  }
   a->rows = p.row_rows;
   a->workers = (int)p.row_workers;
   a->tile_workers = (int)p.tile_workers;
@@ -228,6 +217,7 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
   a->tile_o = reinterpret_cast<float*>(take(p.tile_o));
   a->tile_ml = reinterpret_cast<float*>(take(p.tile_ml));
   if (p.kind == Kind::kTiles) {
+    if (c.dtype == BITDELTA_KV_FP4) return bd::status_of_hip(bd::launch_attend4(*a, c.head_dim, st));
     const int tpt = bd::kTileRows / a->group;
     // each sequence rounds its tokens up to whole tiles
     const int64_t tiles = std::min<int64_t>(a->tokens / tpt + a->batch,
@@ -244,7 +234,8 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
   }
   const int blocks = (int)(p.kind == Kind::kRows ? p.row_units : p.row_workers);
   bitdelta_status s = bd::status_of_hip(
-      bd::launch_attend_rows(*a, c.head_dim, fp8, p.columns, blocks, st));
+      c.dtype == BITDELTA_KV_FP4 ? bd::launch_attend4_rows(*a, c.head_dim, p.columns, blocks, st)
+                                 : bd::launch_attend_rows(*a, c.head_dim, fp8, p.columns, blocks, st));
   if (s != BITDELTA_OK || p.kind == Kind::kRows) return s;
   return bd::status_of_hip(bd::launch_attend_combine(*a, c.head_dim, st));
 }
