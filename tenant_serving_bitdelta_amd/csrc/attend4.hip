@@ -473,107 +473,465 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
   }
 }
 
-// One wave per query row: a lane takes a key of 64 at a time, its whole score; then the wave goes through
-// the 64 values, a lane two dims.
+// ---------------------------------------------------------------------------------------------
+// Tile kernel: 256 query rows (tokens x the heads of one kv head) against a key list in 64-key steps.  8
+// waves of 32 rows; K codes and scale bytes in LDS as they are, V widened to bf16 on the way there, each a
+// step ahead in two buffers.
+// ---------------------------------------------------------------------------------------------
+// Byte offset of 16-byte unit u (32 dims) of row r in a K tile: a wave's reads take one unit of 32 rows
 template <int D>
-__global__ __launch_bounds__(64) void attend4_plain_kernel(const AttendArgs a) {
-  __shared__ float qs[D];
-  const int lane = threadIdx.x;
-  const int64_t rows = (int64_t)a.tokens * a.heads;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const int t = (int)(r / a.heads), hh = (int)(r - (int64_t)t * a.heads), h = hh / a.group;
-    // the row's sequence and keys
-    KeyList kl{};
-    bool found = false;
-    if (a.nseg > 0) {
-      const RowUnit u = row_unit(a, t);
-      kl = u.keys;
-      found = true;
+__device__ __forceinline__ unsigned k4_unit(int r, int u) {
+  return D == 128 ? (unsigned)(r * 64 + ((u ^ ((r >> 2) & 3)) << 4)) : (unsigned)(r * 32 + (u << 4));
+}
+
+__device__ __forceinline__ f32x16 mfma_k32(const u32x4& k, int k_bytes, bool odd_step, const i32x8& q, int q_bytes,
+                                           bool low, const f32x16& c) {
+  const i32x8 a = {(int)k[0], (int)k[1], (int)k[2], (int)k[3], 0, 0, 0, 0};
+  if (odd_step)
+    return low ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, q, c, 4, 0, 2, k_bytes, 1, q_bytes)
+               : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, q, c, 4, 0, 2, k_bytes, 0, q_bytes);
+  return low ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, q, c, 4, 0, 0, k_bytes, 1, q_bytes)
+             : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, q, c, 4, 0, 0, k_bytes, 0, q_bytes);
+}
+
+// Byte offsets of a key's rows; bit 0 of k: there is no such key (offsets 0).
+struct Row4Place {
+  int64_t k, v;
+};
+// Where the lane's key sits: its table entry (null: no such key), and the rows' offsets from it.
+struct Key4Lookup {
+  const int32_t* entry;
+  int slot;
+  __device__ __forceinline__ Key4Lookup(const PagedCache& c, const KeyList& kl, int vp) {
+    const int kp = key_position(kl, vp);
+    const int page = page_quotient(kp < 0 ? 0 : kp, c.div);
+    const int at = key_table_index(kl, vp, page);
+    slot = kp - page * c.page_size;
+    entry = at >= 0 ? (vp < kl.na ? kl.ta : kl.tb) + at : nullptr;
+  }
+  __device__ __forceinline__ Row4Place place(const PagedCache& c, int id) const {
+    const bool ok = entry && page_id_checked(id, c.num_pages) >= 0;
+    const int p = ok ? id : 0, t = ok ? slot : 0;
+    return Row4Place{page_row_bytes(p, t, c.k_page, c.k_token) | (ok ? 0 : 1),
+                     page_row_bytes(p, t, c.v_page, c.v_token)};
+  }
+};
+
+// What a thread moves of a step: an eighth of a key's rows, D / 16 bytes each of K and V, the scale byte
+// its values go by, and for the first eighth the key's K scale bytes.
+template <int D>
+struct Tile4Stage {
+  static constexpr int kBytes = D / 16;
+  u32x2 k, v;
+  unsigned vb, kb;
+  bool ok;
+
+  __device__ __forceinline__ void fetch(const AttendArgs& a, int64_t k_head, int64_t v_head,
+                                        const Row4Place* places, int tid) {
+    const Row4Place at = places[tid >> 3];
+    const int part = tid & 7;
+    // absent keys read page 0; their values are cleared before they are stored, their scores masked
+    ok = (at.k & 1) == 0;
+    const int64_t ko = (at.k & ~15ll) + k_head, vo = at.v + v_head;
+    const unsigned char* kp = a.cache.k + ko + kBytes * part;
+    const unsigned char* vp = a.cache.v + vo + kBytes * part;
+    if constexpr (D == 128) {
+      k = *reinterpret_cast<const u32x2*>(kp);
+      v = *reinterpret_cast<const u32x2*>(vp);
     } else {
-      for (int b0 = 0; b0 < a.batch && !found; b0 += 64) {
-        const int b = b0 + lane;
-        RowUnit u{};
-        if (b < a.batch) u = row_unit(a, b);
-        const uint64_t mine = __ballot(b < a.batch && t >= u.t0 && t < u.t0 + u.nq);
-        if (!mine) continue;
-        const int bb = b0 + __builtin_ctzll(mine);
-        u = row_unit(a, bb);
-        const int pos = u.p0 + t - u.t0;
-        kl = window_keys(a.table + (int64_t)bb * a.width, a.width, pos < 0 ? 0 : pos + 1, pos, a.window, a.sinks);
-        found = true;
+      k[0] = *reinterpret_cast<const unsigned*>(kp);
+      v[0] = *reinterpret_cast<const unsigned*>(vp);
+    }
+    vb = a.cache.v_blocks[(vo >> 4) + part * (D / 8) / 32];
+    if (part == 0) {
+      if constexpr (D == 128) kb = *reinterpret_cast<const unsigned*>(a.cache.k_blocks + (ko >> 4));
+      else kb = *reinterpret_cast<const uint16_t*>(a.cache.k_blocks + (ko >> 4));
+    }
+  }
+  // state: per key, bit 0: it exists; bit 1 (edge steps, where some row does not see some key): a block of
+  // its values is NaN.  Those are stored as zeros, since their product with a zero weight would be NaN, and
+  // added later for the rows that see them.
+  __device__ __forceinline__ void store(unsigned char* kt, unsigned* kbt, unsigned char* vt, int* state, bool edge,
+                                        int tid) {
+    const int r = tid >> 3, part = tid & 7;
+    int bits = ok;
+    if (!ok) {
+      v = u32x2{0, 0};
+      vb = 127;
+    }
+    if (edge) {
+      const bool f = vb == 255;
+      if (f) {
+        v = u32x2{0, 0};
+        vb = 127;
+      }
+      const uint64_t m = __ballot(f) >> (tid & 56);  // of this key's eighths
+      if (m & 0xFF) bits |= 2;
+    }
+    const float step = block_step(vb);
+    if constexpr (D == 128) {
+      *reinterpret_cast<u32x2*>(kt + k4_unit<D>(r, part >> 1) + 8 * (part & 1)) = k;
+      *reinterpret_cast<u32x4*>(vt + v_unit<D>(r, 2 * part)) = fp4x8_to_bf16(v[0], step);
+      *reinterpret_cast<u32x4*>(vt + v_unit<D>(r, 2 * part + 1)) = fp4x8_to_bf16(v[1], step);
+    } else {
+      *reinterpret_cast<unsigned*>(kt + k4_unit<D>(r, part >> 2) + 4 * (part & 3)) = k[0];
+      *reinterpret_cast<u32x4*>(vt + v_unit<D>(r, part)) = fp4x8_to_bf16(v[0], step);
+    }
+    if (part == 0) {
+      kbt[r] = kb;
+      state[r] = bits;
+    }
+  }
+};
+
+__device__ __forceinline__ int prefix_steps(const AttendArgs& a, int sg) {
+  const int len = clamp_len(a.prefix_lens[sg], a.pwidth, a.cache.page_size);
+  return (len + kTileKeys - 1) / kTileKeys;
+}
+
+template <int D, bool PREFIX>
+__global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a) {
+  constexpr int kTile = kTileKeys * D * 2;   // bytes of a V tile
+  constexpr int kTileK = kTileKeys * D / 2;
+  constexpr int kSteps = D / 64;   // matrix steps over D of a score tile
+  constexpr int kOut = D / 32;     // 32-row tiles of O^T
+  __shared__ __attribute__((aligned(16))) unsigned char kbuf[2][kTileK];
+  __shared__ __attribute__((aligned(16))) unsigned char vbuf[2][kTile];
+  __shared__ unsigned kbytes[2][kTileKeys];
+  __shared__ int state[2][kTileKeys];
+  __shared__ Row4Place places[4][kTileKeys];
+  __shared__ int entries[8][kTileKeys];
+  __shared__ int scan[kAttendMaxSeqs + 1];
+  __shared__ int segs[PREFIX ? kAttendMaxSegments + 1 : 1];
+  __shared__ int wave_sum[8];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane & 31, hf = lane >> 5;
+  const int tpt = kTileRows / a.group;  // tokens per tile
+  const unsigned entries_at = __builtin_amdgcn_readfirstlane(lds_address(entries));
+
+  // ---- work: prefix: a share of all (segment, row tile, kv head) units' steps; window: one unit
+  int64_t x = 0, x_end = 1, total = 1;
+  int w_id = blockIdx.x;
+  if constexpr (PREFIX) {
+    // workgroups go round robin over the 8 XCDs: give each XCD one run of the work, so that the
+    // row tiles and heads that read the same pages share its L2
+    auto tiles_of = [&](int s) { return (a.seg_offsets[s + 1] - a.seg_offsets[s] + tpt - 1) / tpt; };
+    block_scan<512>(segs, wave_sum, a.nseg, tiles_of);
+    block_scan<512>(scan, wave_sum, a.nseg, [&](int s) { return tiles_of(s) * prefix_steps(a, s); });
+    if (blockIdx.x == 0)  // for the joining kernel
+      for (int i = tid; i <= a.nseg; i += 512) {
+        a.tile_segs[i] = segs[i];
+        a.tile_scan[i] = scan[i];
+      }
+    total = (int64_t)scan[a.nseg] * a.kv_heads;
+    const int workers = split_workers(total, a.tile_workers);
+    const int per = (workers + 7) / 8;
+    w_id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || w_id >= workers) return;
+    x = split_begin(w_id, total, workers);
+    x_end = split_begin(w_id + 1, total, workers);
+  } else {
+    block_scan<512>(scan, wave_sum, a.batch, [&](int b) {
+      const RowUnit u = row_unit(a, b);
+      return (u.nq + tpt - 1) / tpt;
+    });
+  }
+
+  while (x < x_end) {
+    KeyList kl;
+    int t0, nt, p0 = 0, h, s_begin, s_end;
+    int64_t slot = 0;
+    if constexpr (PREFIX) {
+      const int sg = scan_find(scan, a.nseg, (int)(x / a.kv_heads));
+      const int n0 = a.seg_offsets[sg], n = a.seg_offsets[sg + 1] - n0;
+      const int len = clamp_len(a.prefix_lens[sg], a.pwidth, a.cache.page_size);
+      const int steps = prefix_steps(a, sg);
+      const int tiles = (n + tpt - 1) / tpt;
+      int64_t r = x - (int64_t)scan[sg] * a.kv_heads;  // units: kv head major, then row tile
+      h = (int)(r / ((int64_t)tiles * steps));
+      r -= (int64_t)h * tiles * steps;
+      const int rt = (int)(r / steps);
+      s_begin = (int)(r - (int64_t)rt * steps);
+      s_end = (int)(x_end - x < steps - s_begin ? s_begin + (x_end - x) : steps);
+      x += s_end - s_begin;
+      t0 = n0 + rt * tpt;
+      nt = n - rt * tpt < tpt ? n - rt * tpt : tpt;
+      slot = w_id + (int64_t)segs[sg] * a.kv_heads + h * tiles + rt;
+      const int32_t* row = a.prefix_table + (int64_t)sg * a.pwidth;
+      kl = KeyList{row, row, a.pwidth, a.pwidth, 0, 0, len};
+    } else {
+      // heads fastest: with a multiple of 8 kv heads each XCD serves its own heads.  Later tiles
+      // see more keys: they start first.
+      const int tiles = scan[a.batch];
+      const int ti = tiles - 1 - (int)blockIdx.x / a.kv_heads;
+      if (ti < 0) return;
+      h = (int)blockIdx.x % a.kv_heads;
+      const int b = scan_find(scan, a.batch, ti);
+      const RowUnit u = row_unit(a, b);
+      const int rt = ti - scan[b];
+      t0 = u.t0 + rt * tpt;
+      nt = u.nq - rt * tpt < tpt ? u.nq - rt * tpt : tpt;
+      p0 = u.p0 + rt * tpt;
+      // keys up to the tile's last token
+      const int len = p0 + nt < 0 ? 0 : p0 + nt;
+      kl = window_keys(a.table + (int64_t)b * a.width, a.width, len, p0, a.window, a.sinks);
+      s_begin = 0;
+      s_end = (kl.n + kTileKeys - 1) / kTileKeys;
+    }
+
+    // ---- this lane's query row: 32 * wave + q of the tile
+    const int row = 32 * wave + q;
+    const int t = row / a.group, hh = h * a.group + row - t * a.group;
+    const bool live = t < nt;
+    const int pq = p0 + t;
+    // positions of the wave's first and last live token
+    const int wt0 = 32 * wave / a.group;
+    const int wt1 = (32 * wave + 31) / a.group < nt ? (32 * wave + 31) / a.group : nt - 1;
+    const bool wave_live = wt0 < nt;
+    // the lane's dims of step d: 64 d + 16 hf .. + 15 and 64 d + 32 + 16 hf .. + 15
+    i32x8 q_hi[kSteps], q_lo[kSteps];
+    int q_scales;
+    {
+      const uint16_t* qp = a.q + (int64_t)(t0 + t) * a.q_token + (int64_t)hh * a.q_head + 16 * hf;
+      u32x4 x4[2 * kSteps][2];
+      unsigned top = 0;
+#pragma unroll
+      for (int s = 0; s < 2 * kSteps; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          x4[s][i] = live ? *reinterpret_cast<const u32x4*>(qp + 32 * s + 8 * i) : u32x4{0, 0, 0, 0};
+          top = max(top, top_bits(x4[s][i]));
+        }
+      top = __float_as_uint(half_max(__uint_as_float(top << 16))) >> 16;
+      q_scales = (int)query_scales(top);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        int hi[8], lo[8];
+        split_query(x4[2 * s], (unsigned)q_scales, hi, lo);
+        split_query(x4[2 * s + 1], (unsigned)q_scales, hi + 4, lo + 4);
+        q_hi[s] = i32x8{hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]};
+        q_lo[s] = i32x8{lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]};
       }
     }
-    if (!found) continue;
-    const uint16_t* qp = a.q + (int64_t)t * a.q_token + (int64_t)hh * a.q_head;
-    __syncthreads();
-    for (int d = lane; d < D; d += 64) qs[d] = __uint_as_float((unsigned)qp[d] << 16);
-    __syncthreads();
-    float m = kNegInf, l = 0.f, o0 = 0.f, o1 = 0.f;
-    for (int base = 0; base < kl.n; base += 64) {
-      const int vp = base + lane;
-      const int kp = key_position(kl, vp);
-      const int page = page_quotient(kp < 0 ? 0 : kp, a.cache.div);
-      const int at = key_table_index(kl, vp, page);
-      const int id = at >= 0 ? page_id_checked((vp < kl.na ? kl.ta : kl.tb)[at], a.cache.num_pages) : -1;
-      float s = kNegInf;
-      int64_t vo = -1;
-      if (id >= 0) {
-        const int slot = kp - page * a.cache.page_size;
-        vo = page_row_bytes(id, slot, a.cache.v_page, a.cache.v_token) + (int64_t)h * a.cache.v_head;
-        const int64_t ko = page_row_bytes(id, slot, a.cache.k_page, a.cache.k_token) + (int64_t)h * a.cache.k_head;
-        s = 0.f;
-        for (int i = 0; i < D / 32; ++i) {
-          const u32x4 x = *reinterpret_cast<const u32x4*>(a.cache.k + ko + 16 * i);
-          const float step = __uint_as_float((unsigned)a.cache.k_blocks[(ko >> 4) + i] << 23);
+    f32x16 o[kOut];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const float* qd = qs + 32 * i + 8 * w;
-            auto add = [&](unsigned pair, int d) {
-              s = __builtin_fmaf(bf16lo_to_f32(pair), qd[d], s);
-              s = __builtin_fmaf(bf16hi_to_f32(pair), qd[d + 1], s);
-            };
-            add(__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x[w], step, 0)), 0);
-            add(__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x[w], step, 1)), 2);
-            add(__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x[w], step, 2)), 4);
-            add(__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x[w], step, 3)), 6);
+    for (int i = 0; i < kOut; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
+    float m = kNegInf, l = 0.f;
+
+    // The pipeline: the keys of step t are looked up by one wave (wave t mod 8, one lane a key).
+    // Table entries are copied into LDS, so that no register waits for them; two steps later the
+    // rows' offsets are worked out, and a step later the rows' loads begin.
+    constexpr int kAhead = 2;  // steps from the loads to the step they are for
+    auto look_begin = [&](int s) {
+      if (((s - s_begin) & 7) == wave) {
+        const Key4Lookup look(a.cache, kl, s * kTileKeys + lane);
+        if (look.entry) copy4(look.entry, entries_at + wave * kTileKeys * 4);
+      }
+    };
+    auto look_end = [&](int s) {
+      if (((s - s_begin) & 7) == wave) {
+        const Key4Lookup look(a.cache, kl, s * kTileKeys + lane);
+        places[(s - s_begin) & 3][lane] = look.place(a.cache, entries[wave][lane]);
+      }
+    };
+    // edge step: some row of the tile does not see some key of it (the same for all waves)
+    auto hides = [&](int base) {
+      if constexpr (PREFIX) return false;
+      const int f = key_position(kl, base), last = key_position(kl, base + kTileKeys - 1);
+      return base < kl.na || last > p0 || p0 + nt - 1 - f >= a.window;
+    };
+    const int64_t k_head = (int64_t)h * a.cache.k_head, v_head = (int64_t)h * a.cache.v_head;
+    Tile4Stage<D> st;
+    for (int i = 0; i < kAhead + 3; ++i) look_begin(s_begin + i);
+    wait_copies<0>();
+    __syncthreads();  // the last unit's tiles and notes are no longer read
+    for (int i = 0; i <= kAhead; ++i) look_end(s_begin + i);
+    __syncthreads();
+    st.fetch(a, k_head, v_head, places[0], tid);
+    st.store(kbuf[0], kbytes[0], vbuf[0], state[0], hides(s_begin * kTileKeys), tid);
+    st.fetch(a, k_head, v_head, places[1], tid);
+    __syncthreads();
+
+    // O^T += V^T P^T of step s: of 16 keys the lane's 8 are 4 hf .. + 3 and 8 + 4 hf .. + 3
+    u32x4 p[4];
+    const int l16 = lane & 15;
+    const int v_row = 4 * hf + (l16 >> 2), v_un = 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1);
+    const int v_b = 8 * (l16 & 1);
+    u32x4 vf[2][kOut];
+    auto read_values = [&](int buf, int kb) {
+      const unsigned char* vt = vbuf[buf];
+#pragma unroll
+      for (int i = 0; i < kOut; ++i) {
+        const u32x2 lo = lds_read_tr(vt + v_unit<D>(16 * kb + v_row, 4 * i + v_un) + v_b);
+        const u32x2 hi = lds_read_tr(vt + v_unit<D>(16 * kb + 8 + v_row, 4 * i + v_un) + v_b);
+        vf[kb & 1][i] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
+    };
+    for (int s = s_begin; s < s_end; ++s) {
+      const int buf = (s - s_begin) & 1;
+      const int base = s * kTileKeys;
+      const int key_state = state[buf][lane];
+      const uint64_t valid = __ballot(key_state & 1);
+      uint64_t odd = PREFIX ? 0 : __ballot(key_state & 2);  // keys whose values were taken out
+      // does the wave see anything, does every row see everything?
+      bool any = wave_live && valid != 0, all = valid == ~0ull;
+      if constexpr (!PREFIX) {
+        const int f = key_position(kl, base), last = key_position(kl, base + kTileKeys - 1);
+        const bool in_main = base >= kl.na;
+        any = any && f <= p0 + wt1 && (f < a.sinks || p0 + wt0 - last < a.window);
+        all = all && in_main && last <= p0 + wt0 && p0 + wt1 - f < a.window;
+      }
+      f32x16 sc[2];
+      if (any) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sc[i][e] = 0.f;
+        u32x4 kf[2][kSteps];
+        int kb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // the lane's scale bytes: of block hf in byte 0, of block 2 + hf in byte 2
+          kb[i] = (int)(kbytes[buf][32 * i + q] >> (8 * hf));
+#pragma unroll
+          for (int d = 0; d < kSteps; ++d)
+            kf[i][d] = *reinterpret_cast<const u32x4*>(kbuf[buf] + k4_unit<D>(32 * i + q, 2 * d + hf));
+        }
+#pragma unroll
+        for (int d = 0; d < kSteps; ++d) {
+          sc[0] = mfma_k32(kf[0][d], kb[0], d == 1, q_hi[d], q_scales, false, sc[0]);
+          sc[1] = mfma_k32(kf[1][d], kb[1], d == 1, q_hi[d], q_scales, false, sc[1]);
+          sc[0] = mfma_k32(kf[0][d], kb[0], d == 1, q_lo[d], q_scales, true, sc[0]);
+          sc[1] = mfma_k32(kf[1][d], kb[1], d == 1, q_lo[d], q_scales, true, sc[1]);
+        }
+      }
+      // ---- the next step's tiles; these buffers were last read before the barrier that began
+      // this step
+      if (s + 1 < s_end) {
+        st.store(kbuf[buf ^ 1], kbytes[buf ^ 1], vbuf[buf ^ 1], state[buf ^ 1], hides(base + kTileKeys), tid);
+        st.fetch(a, k_head, v_head, places[(s + 2 - s_begin) & 3], tid);
+        // (the loads that st.store waited for are newer than the entries')
+        look_end(s + 3);
+        look_begin(s + 5);
+      }
+      if (any) {
+        // lane (q, hf) holds keys 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
+        if (!all) {
+          const uint64_t mine = valid >> (4 * hf);
+          const Sight at = sight(kl, pq, a.sinks, base + 4 * hf);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const unsigned bits = (unsigned)(mine >> (32 * i));
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int key = 8 * (e >> 2) + (e & 3);  // + 32 i + 4 hf
+              bool seen = (bits >> key) & 1u;
+              if constexpr (!PREFIX) seen = seen & at.sees(32 * i + key, a.window);
+              const float v = sc[i][e];
+              sc[i][e] = seen ? v : kNegInf;
+            }
           }
         }
-        s *= a.c;
-      }
-      float t0 = s;
+        // the first values are on their way while the weights are worked out
+        read_values(buf, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        // (elementwise maximum: a NaN among a row's scores passes, the row is NaN then)
+        float tp[4];
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) t0 = __builtin_elementwise_maximum(t0, __shfl_xor(t0, d, 64));
-      const float mn = __builtin_elementwise_maximum(m, t0);
-      const float mb = mn == kNegInf ? 0.f : mn;
-      const float f = m == kNegInf ? 0.f : exp2_fast(m - mb);
-      m = mn;
-      const float p = exp2_fast(s - mb);
-      float sum = p;
+        for (int e = 0; e < 4; ++e) {
+          tp[e] = sc[0][e];
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
-      l = l * f + sum;
-      o0 *= f;
-      o1 *= f;
-      for (uint64_t left = __ballot(id >= 0); left; left &= left - 1) {
-        const int j = __builtin_ctzll(left);
-        const float w = __shfl(p, j, 64);
-        const int64_t off = __shfl(vo, j, 64);
-        if (2 * lane < D) {
-          const unsigned x = a.cache.v[off + lane];
-          const float step = __uint_as_float((unsigned)a.cache.v_blocks[(off >> 4) + lane / 16] << 23);
-          const unsigned pair = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, step, 0));
-          o0 = __builtin_fmaf(w, bf16lo_to_f32(pair), o0);
-          o1 = __builtin_fmaf(w, bf16hi_to_f32(pair), o1);
+          for (int i = 4; i < 32; i += 4) tp[e] = __builtin_elementwise_maximum(tp[e], (float)sc[(i + e) >> 4][(i + e) & 15]);
+        }
+        float tm = __builtin_elementwise_maximum(__builtin_elementwise_maximum(tp[0], tp[1]),
+                                                 __builtin_elementwise_maximum(tp[2], tp[3]));
+        tm = half_max(tm) * a.c;
+        if (__any(tm > m + kRescale)) {
+          const float mn = fmaxf(m, tm);
+          const float f = mn == kNegInf ? 1.f : exp2_fast(m - mn);
+          m = mn;
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < kOut; ++i) o[i] *= f;
+        }
+        const float mb = m == kNegInf ? 0.f : m;
+        float lp[4];
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          float e[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) e[i] = exp2_fast(__builtin_fmaf(sc[kb >> 1][8 * (kb & 1) + i], a.c, -mb));
+          lp[kb] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+          // weights enter the product as bf16, the matrix instruction's operand type (off by at most
+          // 2^-8 of themselves); the sum l keeps them in fp32
+          p[kb] = u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
+                        pack_bf16(e[6], e[7])};
+        }
+        l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          if (kb < 3) read_values(buf, kb + 1);
+#pragma unroll
+          for (int i = 0; i < kOut; ++i) o[i] = mfma32(vf[kb & 1][i], p[kb], o[i]);
+        }
+        if constexpr (!PREFIX) {
+          // (also where this wave's rows see all keys: the values were taken out for the whole tile)
+          for (; odd; odd &= odd - 1) {
+            const int vp = base + __builtin_ctzll(odd);
+            const unsigned char* row_v = value_row(a.cache, kl, vp, h);
+            if (!row_v) continue;
+            const unsigned char* blocks = a.cache.v_blocks + ((row_v - a.cache.v) >> 4);
+            const bool seen = sees(kl, pq, a.window, a.sinks, vp);
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) {
+              const float odd_one = seen ? odd_block(blocks, 32 * i) : 0.f;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[i][e] = o[i][e] + odd_one;
+            }
+          }
         }
       }
+      __syncthreads();
     }
-    const float inv = l > 0.f ? a.v_scale / l : (l == 0.f ? 0.f : l);
-    if (2 * lane < D) {
-      uint16_t* op = a.out + (int64_t)t * a.o_token + (int64_t)hh * a.o_head + 2 * lane;
-      *reinterpret_cast<unsigned*>(op) = pack_bf16(o0 * inv, o1 * inv);
+    // no copy into LDS outlives its use: the next unit, or workgroup, has these buffers
+    wait_copies<0>();
+
+    // ---- epilogue: lane (q, hf) holds dims 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
+    l = half_sum(l);
+    if (live) {
+      if constexpr (PREFIX) {
+        const int64_t at = slot * kTileRows + row;
+        float* op = a.tile_o + at * D + 4 * hf;
+#pragma unroll
+        for (int i = 0; i < kOut; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<f32x4*>(op + 32 * i + 8 * e) =
+                f32x4{o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
+        if (hf == 0) {
+          a.tile_ml[at * 2] = m;
+          a.tile_ml[at * 2 + 1] = l;
+        }
+      } else {
+        const float inv = l > 0.f ? a.v_scale / l : (l == 0.f ? 0.f : l);
+        uint16_t* op = a.out + (int64_t)(t0 + t) * a.o_token + (int64_t)hh * a.o_head + 4 * hf;
+#pragma unroll
+        for (int i = 0; i < kOut; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<u32x2*>(op + 32 * i + 8 * e) =
+                u32x2{pack_bf16(o[i][4 * e] * inv, o[i][4 * e + 1] * inv),
+                      pack_bf16(o[i][4 * e + 2] * inv, o[i][4 * e + 3] * inv)};
+        if (a.lse && hf == 0)
+          a.lse[(int64_t)(t0 + t) * a.heads + hh] =
+              l == 0.f ? kNegInf : (m + __builtin_log2f(l)) * kLn2;
+      }
     }
-    if (a.lse && lane == 0)
-      a.lse[(int64_t)t * a.heads + hh] = l == 0.f ? kNegInf : (m + __builtin_log2f(l)) * kLn2;
+    if constexpr (!PREFIX) break;
   }
 }
 
@@ -601,12 +959,13 @@ hipError_t launch_attend4_rows(const AttendArgs& a, int dim, int columns, int bl
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_attend4(const AttendArgs& a, int dim, hipStream_t stream) {
-  const int64_t rows = (int64_t)a.tokens * a.heads;
-  const dim3 grid((unsigned)(rows < (1 << 22) ? rows : (1 << 22)));
+hipError_t launch_attend4_tiles(const AttendArgs& a, int dim, bool prefix, int blocks, hipStream_t stream) {
+  if (blocks < 1 || a.batch > kAttendMaxSeqs || a.nseg > kAttendMaxSegments) return hipErrorInvalidValue;
   clear_stale_error();
-  if (dim == 64) hipLaunchKernelGGL(attend4_plain_kernel<64>, grid, dim3(64), 0, stream, a);
-  else if (dim == 128) hipLaunchKernelGGL(attend4_plain_kernel<128>, grid, dim3(64), 0, stream, a);
+  if (dim == 64 && prefix) hipLaunchKernelGGL((attend4_tile_kernel<64, true>), dim3(blocks), dim3(512), 0, stream, a);
+  else if (dim == 64) hipLaunchKernelGGL((attend4_tile_kernel<64, false>), dim3(blocks), dim3(512), 0, stream, a);
+  else if (dim == 128 && prefix) hipLaunchKernelGGL((attend4_tile_kernel<128, true>), dim3(blocks), dim3(512), 0, stream, a);
+  else if (dim == 128) hipLaunchKernelGGL((attend4_tile_kernel<128, false>), dim3(blocks), dim3(512), 0, stream, a);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }

@@ -134,10 +134,11 @@ Plan plan_shared(int64_t batch, int32_t heads, const bitdelta_kv_cache& c, int32
   const int64_t own = (int64_t)width * c.page_size, pre = (int64_t)pwidth * c.page_size;
   int used = 0;  // segments with sequences
   for (int i = 0; i < nseg; ++i) used += offs[i + 1] > offs[i];
-  const int64_t row_bytes = 2 * (int64_t)c.head_dim * (c.dtype == BITDELTA_KV_FP8 ? 1 : 2);
+  const int64_t row_bytes = c.dtype == BITDELTA_KV_FP4 ? c.head_dim + c.head_dim / 16
+                                                       : 2 * (int64_t)c.head_dim * (c.dtype == BITDELTA_KV_FP8 ? 1 : 2);
   if (own + pre <= (int64_t)direct_steps(p.row_units) * bd::kRowStep) {
     p.kind = Kind::kRows;
-  } else if (c.dtype == BITDELTA_KV_FP4 || (batch - used) * pre * c.kv_heads * row_bytes < kShareBytes) {
+  } else if ((batch - used) * pre * c.kv_heads * row_bytes < kShareBytes) {
     p.kind = Kind::kRowsSplit;
   } else {
     p.kind = Kind::kPrefixTiles;
@@ -195,13 +196,13 @@ void fill(bd::AttendArgs* a, const bitdelta_attend_rows& r, const bitdelta_kv_ca
 
 bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c, void* workspace,
                     bitdelta_stream stream) {
-  const bool fp8 = c.dtype == BITDELTA_KV_FP8;
+  const bool fp8 = c.dtype == BITDELTA_KV_FP8, fp4 = c.dtype == BITDELTA_KV_FP4;
   hipStream_t st = static_cast<hipStream_t>(stream);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a->rows = p.row_rows;
   a->workers = (int)p.row_workers;
   a->tile_workers = (int)p.tile_workers;
-  a->halves = !fp8;
+  a->halves = !fp8 && !fp4;
   a->direct = p.kind == Kind::kRows;
   a->row_prefix = a->nseg > 0 && p.kind != Kind::kPrefixTiles;
   auto take = [&](size_t bytes) {
@@ -217,25 +218,26 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
   a->tile_o = reinterpret_cast<float*>(take(p.tile_o));
   a->tile_ml = reinterpret_cast<float*>(take(p.tile_ml));
   if (p.kind == Kind::kTiles) {
-    if (c.dtype == BITDELTA_KV_FP4) return bd::status_of_hip(bd::launch_attend4(*a, c.head_dim, st));
     const int tpt = bd::kTileRows / a->group;
     // each sequence rounds its tokens up to whole tiles
     const int64_t tiles = std::min<int64_t>(a->tokens / tpt + a->batch,
                                             a->batch * (((int64_t)a->max_q + tpt - 1) / tpt));
-    return bd::status_of_hip(bd::launch_attend_tiles(*a, c.head_dim, fp8, false,
-                                                     (int)(tiles * a->kv_heads), st));
+    const int blocks = (int)(tiles * a->kv_heads);
+    return bd::status_of_hip(fp4 ? bd::launch_attend4_tiles(*a, c.head_dim, false, blocks, st)
+                                 : bd::launch_attend_tiles(*a, c.head_dim, fp8, false, blocks, st));
   }
   if (p.kind == Kind::kPrefixTiles) {
     // the grid holds whole runs of tile_workers / 8 per XCD
     const int per = (a->tile_workers + 7) / 8;
     const bitdelta_status s = bd::status_of_hip(
-        bd::launch_attend_tiles(*a, c.head_dim, fp8, true, per * 8, st));
+        fp4 ? bd::launch_attend4_tiles(*a, c.head_dim, true, per * 8, st)
+            : bd::launch_attend_tiles(*a, c.head_dim, fp8, true, per * 8, st));
     if (s != BITDELTA_OK) return s;
   }
   const int blocks = (int)(p.kind == Kind::kRows ? p.row_units : p.row_workers);
   bitdelta_status s = bd::status_of_hip(
-      c.dtype == BITDELTA_KV_FP4 ? bd::launch_attend4_rows(*a, c.head_dim, p.columns, blocks, st)
-                                 : bd::launch_attend_rows(*a, c.head_dim, fp8, p.columns, blocks, st));
+      fp4 ? bd::launch_attend4_rows(*a, c.head_dim, p.columns, blocks, st)
+          : bd::launch_attend_rows(*a, c.head_dim, fp8, p.columns, blocks, st));
   if (s != BITDELTA_OK || p.kind == Kind::kRows) return s;
   return bd::status_of_hip(bd::launch_attend_combine(*a, c.head_dim, st));
 }
