@@ -28,9 +28,9 @@ struct CacheArgs {
   const int32_t* lens;                   // [batch]
   const int32_t* q_offsets;              // [batch + 1] or null: row t is the last token of sequence t
   int32_t width, batch, tokens, kv_heads;
-  PageDiv heads_div;                     // by 2 kv_heads
   float scale[2];
   float inverse[2];                      // 1 / scale where that is exact, else 0
+  float near[2];                         // 1 / scale rounded where a division by it may start from that, else 0
 };
 
 hipError_t launch_cache_write(const CacheArgs& a, int dim, int dtype, hipStream_t stream);

@@ -98,6 +98,14 @@ float exact_inverse(float scale) {
   return frexpf(scale, &e) == 0.5f && isnormal(scale) && isnormal(inv) ? inv : 0.0f;
 }
 
+// 1 / scale rounded, if Markstein's theorem holds with it (a fraction of scale that is not all ones) for
+// quotients from 2^-20 to 2^9 without an underflow of what is left over (products 2^-48 of the value)
+float near_inverse(float scale) {
+  int e;
+  const float f = frexpf(scale, &e);
+  return e > -60 && e < 60 && f < 0.99999994f ? 1.0f / scale : 0.0f;
+}
+
 bitdelta_status run(bool write, const bitdelta_kv_rows* r, const bitdelta_kv_cache* c, int32_t batch,
                     const int32_t* table, int32_t width, const int32_t* lens,
                     const int32_t* q_offsets, bitdelta_stream stream) {
@@ -121,11 +129,12 @@ bitdelta_status run(bool write, const bitdelta_kv_rows* r, const bitdelta_kv_cac
   a.batch = batch;
   a.tokens = (int32_t)r->tokens;
   a.kv_heads = c->kv_heads;
-  a.heads_div = make_page_div((uint32_t)(2 * c->kv_heads));
   a.scale[0] = c->k_scale;
   a.scale[1] = c->v_scale;
   a.inverse[0] = exact_inverse(c->k_scale);
   a.inverse[1] = exact_inverse(c->v_scale);
+  a.near[0] = near_inverse(c->k_scale);
+  a.near[1] = near_inverse(c->v_scale);
   hipStream_t st = static_cast<hipStream_t>(stream);
   return status_of_hip(write ? launch_cache_write(a, c->head_dim, c->dtype, st)
                              : launch_cache_read(a, c->head_dim, c->dtype, st));
