@@ -169,6 +169,7 @@ hipError_t launch_attend_tiles(const AttendArgs& a, int dim, bool fp8, bool pref
 // the same for a 4-bit cache
 hipError_t launch_attend4_rows(const AttendArgs& a, int dim, int columns, int blocks, hipStream_t stream);
 hipError_t launch_attend4_tiles(const AttendArgs& a, int dim, bool prefix, int blocks, hipStream_t stream);
-hipError_t launch_attend_combine(const AttendArgs& a, int dim, hipStream_t stream);
+// many: rows of so many pieces that a workgroup's waves share one's
+hipError_t launch_attend_combine(const AttendArgs& a, int dim, bool many, hipStream_t stream);
 
 }  // namespace bd

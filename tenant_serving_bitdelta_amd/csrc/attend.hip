@@ -943,20 +943,21 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
 // Combine: one wave per query row adds the row's partials of both kernels, in a fixed order: lanes of
 // 4 dims each, 64 / (dim / 4) pieces side by side, four loads each in flight.  Bound by finding the
 // pieces (divisions) and the loads' latency: 16384 rows of 3 to 5 pieces 18 us, 64 rows of 96 4 us.  Two
-// rows a wave took 15.6 us for the former, but 6.1 for the latter.
+// rows a wave took 15.6 us for the former, but 6.1 for the latter.  W = 4: a workgroup's waves take one
+// row's pieces between them.
 // ---------------------------------------------------------------------------------------------
-template <int D>
+template <int D, int W>
 __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a) {
   const int tpt = kTileRows / a.group;
-  constexpr int kQ = D / 4, kWays = 64 / kQ;  // lanes of a row, pieces side by side
+  constexpr int kQ = D / 4, kWays = W * (64 / kQ);  // lanes of a row, pieces side by side
   const int lane = threadIdx.x & 63;
-  const int rest = blockIdx.x * 4 + (threadIdx.x >> 6), b = blockIdx.y;
+  const int rest = W == 1 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x, b = blockIdx.y;
   if (rest >= a.max_q * a.heads) return;
   const int tq = rest / a.heads, hh = rest - tq * a.heads;
   const int h = hh / a.group;
   const RowUnit u = row_unit(a, b);
   if (tq >= u.nq) return;
-  const int d4 = lane % kQ, way = lane / kQ;
+  const int d4 = lane % kQ, way = lane / kQ + (W == 1 ? 0 : (threadIdx.x >> 6) * (64 / kQ));
 
   float mx = kNegInf, lt = 0.f;
   f32x4 ot = {0.f, 0.f, 0.f, 0.f};
@@ -1037,6 +1038,19 @@ __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a)
     ot = ot * f0 + oo * f1;
     mx = mn;
   }
+  if constexpr (W > 1) {  // the waves' sums
+    __shared__ f32x4 wave_o[W][kQ];
+    __shared__ float wave_ml[W][2];
+    const int wave = threadIdx.x >> 6;
+    if (lane < kQ) wave_o[wave][lane] = ot;
+    if (lane == 0) {
+      wave_ml[wave][0] = mx;
+      wave_ml[wave][1] = lt;
+    }
+    __syncthreads();
+    if (way == 0)
+      for (int v = 1; v < W; ++v) add(wave_ml[v][0], wave_ml[v][1], wave_o[v][d4]);
+  }
   if (way == 0) {
     const float inv = lt > 0.f ? a.v_scale / lt : (lt == 0.f ? 0.f : lt);
     const int64_t tok = u.t0 + tq;
@@ -1103,15 +1117,15 @@ hipError_t launch_attend_tiles(const AttendArgs& a, int dim, bool fp8, bool pref
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_attend_combine(const AttendArgs& a, int dim, hipStream_t stream) {
-  const dim3 grid((a.max_q * a.heads + 3) / 4, a.batch);  // at most 64 rows per kv head
+hipError_t launch_attend_combine(const AttendArgs& a, int dim, bool many, hipStream_t stream) {
+  const unsigned rows = (unsigned)a.max_q * a.heads;  // at most 64 per kv head
+  const dim3 grid(many ? rows : (rows + 3) / 4, a.batch);
   clear_stale_error();
-  if (dim == 64)
-    hipLaunchKernelGGL(attend_combine_kernel<64>, grid, dim3(256), 0, stream, a);
-  else if (dim == 128)
-    hipLaunchKernelGGL(attend_combine_kernel<128>, grid, dim3(256), 0, stream, a);
-  else
-    return hipErrorInvalidValue;
+  if (dim == 64 && many) hipLaunchKernelGGL((attend_combine_kernel<64, 4>), grid, dim3(256), 0, stream, a);
+  else if (dim == 64) hipLaunchKernelGGL((attend_combine_kernel<64, 1>), grid, dim3(256), 0, stream, a);
+  else if (dim == 128 && many) hipLaunchKernelGGL((attend_combine_kernel<128, 4>), grid, dim3(256), 0, stream, a);
+  else if (dim == 128) hipLaunchKernelGGL((attend_combine_kernel<128, 1>), grid, dim3(256), 0, stream, a);
+  else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 

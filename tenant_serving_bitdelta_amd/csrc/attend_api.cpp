@@ -239,7 +239,9 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
       fp4 ? bd::launch_attend4_rows(*a, c.head_dim, p.columns, blocks, st)
           : bd::launch_attend_rows(*a, c.head_dim, fp8, p.columns, blocks, st));
   if (s != BITDELTA_OK || p.kind == Kind::kRows) return s;
-  return bd::status_of_hip(bd::launch_attend_combine(*a, c.head_dim, st));
+  // pieces of a unit: MANY
+  const bool many = fp4 && p.row_workers >= 32 * p.row_units;
+  return bd::status_of_hip(bd::launch_attend_combine(*a, c.head_dim, many, st));
 }
 
 bitdelta_status check_workspace(const Plan& p, const void* ws, size_t bytes) {
