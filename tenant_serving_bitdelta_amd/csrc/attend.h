@@ -44,6 +44,7 @@ struct PagedCache {
   // 4-bit cache: scale bytes, those of the row at byte o of k (v) at o / 16
   const unsigned char* k_blocks;
   const unsigned char* v_blocks;
+  int32_t alike;  // keys and values have the same strides
 };
 
 // Where a key sits: page id and slot, id -1 when the table has no such page (entry out of range).

@@ -20,6 +20,7 @@ __device__ __forceinline__ u32x4 fp4x8_to_bf16(unsigned v, float step) {
                __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, step, 2)),
                __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, step, 3))};
 }
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ float block_step(unsigned byte) { return __uint_as_float(byte << 23); }
 
 // ---------------------------------------------------------------------------------------------
@@ -82,6 +83,15 @@ __device__ __forceinline__ float odd_block(const unsigned char* blocks, int d) {
 // first two lane groups, another, 16 keys on, in the last two; each is met by a query operand that is zero
 // in the other half).  V rows are widened to bf16 into 8 KiB of the wave's LDS, and read transposed.
 // ---------------------------------------------------------------------------------------------
+// The aligned word with the scale bytes of the row at byte o of the scale bytes (dim 64: a row has two, at
+// bits 0 or 16; the word's other half is a neighbour's, or behind the array's end in the same word, and is
+// not looked at).
+template <int D>
+__device__ __forceinline__ unsigned block_word(const unsigned char* blocks, int64_t o, int* at) {
+  *at = D == 128 ? 0 : 8 * (int)(o & 2);
+  return *reinterpret_cast<const unsigned*>(blocks + (D == 128 ? o : o & ~3ll));
+}
+
 template <int D, int NC>
 struct Row4Loop {
   static constexpr int kLoads = D / 64;   // keys a lane has a block of, per step
@@ -94,7 +104,8 @@ struct Row4Loop {
   float m[NC], l[NC];
   int pos[NC];   // the column's token position (window op with several tokens)
   u32x4 kr[kLoads], vr[kLoads];
-  int kb[kLoads], vb[kLoads];  // scale bytes
+  unsigned kb[kLoads], vb[kLoads];  // words that hold the rows' scale bytes
+  int kat[kLoads], vat[kLoads];     // (dim 64) where in them this row's begin, bits
   int id[kLoads], slot[kLoads];
   bool ok[kLoads];
 
@@ -121,11 +132,15 @@ struct Row4Loop {
       ok[i] = page_id_checked(id[i], a.cache.num_pages) >= 0;
       const int page = ok[i] ? id[i] : 0, at = ok[i] ? slot[i] : 0;
       const int64_t ko = page_row_bytes(page, at, a.cache.k_page, a.cache.k_token) + (int64_t)h * a.cache.k_head;
-      const int64_t vo = page_row_bytes(page, at, a.cache.v_page, a.cache.v_token) + (int64_t)h * a.cache.v_head;
+      // (most caches lay keys and values out alike: then their offsets are worked out once)
+      int64_t vo = ko;
+      if (!a.cache.alike)
+        vo = page_row_bytes(page, at, a.cache.v_page, a.cache.v_token) + (int64_t)h * a.cache.v_head;
       kr[i] = *reinterpret_cast<const u32x4*>(a.cache.k + ko + 16 * block(g));
       vr[i] = *reinterpret_cast<const u32x4*>(a.cache.v + vo + 16 * block(g));
-      kb[i] = a.cache.k_blocks[(ko >> 4) + block(g)];
-      vb[i] = a.cache.v_blocks[(vo >> 4) + block(g)];
+      // (whole words: the compiler widens a loaded byte at once, and waits for it there)
+      kb[i] = block_word<D>(a.cache.k_blocks, ko >> 4, &kat[i]);
+      vb[i] = block_word<D>(a.cache.v_blocks, vo >> 4, &vat[i]);
     }
   }
   // keys of the step that exist, bit (key)
@@ -143,20 +158,25 @@ struct Row4Loop {
     for (int i = 0; i < kLoads; ++i)
       if (!ok[i]) {
         vr[i] = u32x4{0, 0, 0, 0};
-        vb[i] = 127;
+        vb[i] = 0;
       }
   }
+  // the lane's blocks' scale bytes, K's in the low byte
+  __device__ __forceinline__ int k_byte(int i, int g) const { return (int)(kb[i] >> (kat[i] + 8 * block(g))); }
+  __device__ __forceinline__ unsigned v_byte(int i, int g) const {
+    return __builtin_amdgcn_ubfe(vb[i], vat[i] + 8 * block(g), 8);
+  }
   // keys with a block of NaN among their values, bit (key); those blocks become zeros
-  __device__ __forceinline__ unsigned clear_odd_blocks() {
+  __device__ __forceinline__ unsigned clear_odd_blocks(int g) {
     unsigned odd = 0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const bool f = vb[i] == 255;
+      const bool f = v_byte(i, g) == 255;
       uint64_t m = __ballot(f);
       if (m) {
         if (f) {
           vr[i] = u32x4{0, 0, 0, 0};
-          vb[i] = 127;
+          vb[i] = 0;
         }
         m |= m >> 16;  // lane groups 0, 1 and 2, 3
         if constexpr (D == 128) odd |= (unsigned)((m | (m >> 32)) & 0xFFFFull) << (16 * i);
@@ -167,9 +187,9 @@ struct Row4Loop {
   }
   // dim 64: a product has two keys in it, one met by zeros, which a block of NaN would pass through: such
   // blocks become zeros.  Returns their keys, bit (key), whose scores are NaN.
-  __device__ __forceinline__ unsigned clear_odd_keys() {
+  __device__ __forceinline__ unsigned clear_odd_keys(int g) {
     if constexpr (D == 128) return 0;
-    const bool f = kb[0] == 255;
+    const bool f = (k_byte(0, g) & 255) == 255;
     uint64_t m = __ballot(f);
     if (!m) return 0;
     if (f) kb[0] = 0, kr[0] = u32x4{0, 0, 0, 0};
@@ -195,15 +215,15 @@ struct Row4Loop {
     for (int h = 0; h < kHalves; ++h) split_query(x[h], (unsigned)scales[c], hi[c] + 4 * h, lo[c] + 4 * h);
   }
   // scores of the keys 16 r .. 16 r + 15 (lane (j, g): keys 4 g .. + 3) with block c's queries
-  __device__ __forceinline__ f32x4 scores(int c, int r) const {
+  __device__ __forceinline__ f32x4 scores(int c, int r, int g) const {
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     auto operand = [&](const int* w) {
       if constexpr (D == 128) return i32x8{w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
       else return r == 0 ? i32x8{w[0], w[1], w[2], w[3], 0, 0, 0, 0} : i32x8{0, 0, 0, 0, w[0], w[1], w[2], w[3]};
     };
-    const int i = D == 128 ? r : 0;
-    s = mfma_k16(kr[i], kb[i], operand(hi[c]), scales[c], false, s);
-    return mfma_k16(kr[i], kb[i], operand(lo[c]), scales[c], true, s);
+    const int i = D == 128 ? r : 0, byte = k_byte(i, g);
+    s = mfma_k16(kr[i], byte, operand(hi[c]), scales[c], false, s);
+    return mfma_k16(kr[i], byte, operand(lo[c]), scales[c], true, s);
   }
 };
 
@@ -288,7 +308,9 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
       lens[b] = a.lens[b];
       return row_steps(row_unit(a, b, lens[b]));
     });
-    total = (int64_t)scan[a.batch] * a.kv_heads;
+    // (values from LDS are the same for all lanes, which the compiler does not know: told so, it keeps what
+    // comes of them, the key list above all, in scalar registers)
+    total = (int64_t)uniform(scan[a.batch]) * a.kv_heads;
     if (blockIdx.x == 0)
       for (int i = tid; i <= a.batch; i += 256) a.scan[i] = scan[i];
     const int workers = split_workers(total, a.workers);
@@ -308,10 +330,10 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
       s_end = row_steps(u);
       x = x_end;
     } else {
-      b = scan_find(scan, a.batch, (int)(x / a.kv_heads));
-      u = row_unit(a, b, lens[b]);
+      b = uniform(scan_find(scan, a.batch, (int)(x / a.kv_heads)));
+      u = row_unit(a, b, uniform(lens[b]));
       const int s = row_steps(u);
-      const int64_t x0 = (int64_t)scan[b] * a.kv_heads;
+      const int64_t x0 = (int64_t)uniform(scan[b]) * a.kv_heads;
       h = (int)((x - x0) / s);
       s_begin = (int)(x - x0 - (int64_t)h * s);
       s_end = (int)(x_end - x < s - s_begin ? s_begin + (x_end - x) : s);
@@ -345,22 +367,22 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
       // keys whose values are not all numbers: those values are taken out here and added below for the
       // tokens that see them, since their product with a zero weight would be NaN
       unsigned odd = 0;
-      if constexpr (MULTI) odd = w.clear_odd_blocks();
+      if constexpr (MULTI) odd = w.clear_odd_blocks(g);
       // ---- V into LDS, scores from K
 #pragma unroll
       for (int i = 0; i < Loop::kLoads; ++i) {
-        const float step = block_step(w.vb[i]);
+        const float step = block_step(w.v_byte(i, g));
         const int row = Loop::key(i, j, g), unit = 4 * Loop::block(g);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           *reinterpret_cast<u32x4*>(vl + v_unit<D>(row, unit + e)) = fp4x8_to_bf16(w.vr[i][e], step);
       }
-      const unsigned odd_keys = w.clear_odd_keys();
+      const unsigned odd_keys = w.clear_odd_keys(g);
       f32x4 s[NC][2];
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) s[c][r] = w.scores(c, r);
+        for (int c = 0; c < NC; ++c) s[c][r] = w.scores(c, r, g);
       if (D == 64 && odd_keys) {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
@@ -370,12 +392,28 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
             for (int i = 0; i < 4; ++i)
               if ((odd_keys >> (16 * r + 4 * g + i)) & 1u) s[c][r][i] = __builtin_nanf("");
       }
-      // ---- the next tile's rows are on their way while this one is worked on
+      // ---- the next tile's rows are on their way while this one is worked on (not before the products have
+      // their operands: the compiler would keep those in copies)
+      __builtin_amdgcn_sched_barrier(0);
       if (base + kRowStep < end) {
         w.fetch(a, h, g);
         if (base + 2 * kRowStep < end) w.lookup(a, kl, base + 2 * kRowStep, j, g);
       }
 
+      // ---- V^T from LDS, the first half on its way while the weights are worked out: the lane's 8 keys are
+      // 4g .. 4g + 3 and 16 + 4g .. 16 + 4g + 3
+      u32x4 vt[Loop::kTiles];
+      const int vr0 = 4 * g + (j >> 2), vu = (j & 3) >> 1, vb = 8 * (j & 1);
+      auto read_values = [&](int i0) {
+#pragma unroll
+        for (int i = i0; i < i0 + Loop::kTiles / 2; ++i) {
+          const u32x2 lo = lds_read_tr(vl + v_unit<D>(vr0, 2 * i + vu) + vb);
+          const u32x2 hi = lds_read_tr(vl + v_unit<D>(16 + vr0, 2 * i + vu) + vb);
+          vt[i] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        }
+      };
+      read_values(0);
+      __builtin_amdgcn_sched_barrier(0);
       // ---- mask: lane (j, g) holds keys 4g + i (s[.][0]) and 16 + 4g + i (s[.][1]) of column j
       u32x4 p[NC];
 #pragma unroll
@@ -420,16 +458,13 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
                      pack_bf16(e[6], e[7])};
       }
 
-      // ---- O^T += V^T P^T: the lane's 8 keys are 4g .. 4g + 3 and 16 + 4g .. 16 + 4g + 3
-      const int vr0 = 4 * g + (j >> 2), vu = (j & 3) >> 1, vb = 8 * (j & 1);
+      // ---- O^T += V^T P^T
+      read_values(Loop::kTiles / 2);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < Loop::kTiles; ++i) {
-        const u32x2 lo = lds_read_tr(vl + v_unit<D>(vr0, 2 * i + vu) + vb);
-        const u32x2 hi = lds_read_tr(vl + v_unit<D>(16 + vr0, 2 * i + vu) + vb);
-        const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
+      for (int i = 0; i < Loop::kTiles; ++i)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) w.o[c][i] = mfma16(v, p[c], w.o[c][i]);
-      }
+        for (int c = 0; c < NC; ++c) w.o[c][i] = mfma16(vt[i], p[c], w.o[c][i]);
       if constexpr (MULTI) {
         for (; odd; odd &= odd - 1) {
           const int vp = base + __builtin_ctz(odd);
@@ -517,13 +552,14 @@ struct Key4Lookup {
   }
 };
 
-// What a thread moves of a step: an eighth of a key's rows, D / 16 bytes each of K and V, the scale byte
-// its values go by, and for the first eighth the key's K scale bytes.
+// What a thread moves of a step: an eighth of a key's rows, D / 16 bytes each of K and V, and the key's scale
+// bytes.
 template <int D>
 struct Tile4Stage {
   static constexpr int kBytes = D / 16;
   u32x2 k, v;
-  unsigned vb, kb;
+  unsigned vb, kb;  // words that hold the rows' scale bytes
+  int vat, kat;     // (dim 64) where in them, bits
   bool ok;
 
   __device__ __forceinline__ void fetch(const AttendArgs& a, int64_t k_head, int64_t v_head,
@@ -542,11 +578,8 @@ struct Tile4Stage {
       k[0] = *reinterpret_cast<const unsigned*>(kp);
       v[0] = *reinterpret_cast<const unsigned*>(vp);
     }
-    vb = a.cache.v_blocks[(vo >> 4) + part * (D / 8) / 32];
-    if (part == 0) {
-      if constexpr (D == 128) kb = *reinterpret_cast<const unsigned*>(a.cache.k_blocks + (ko >> 4));
-      else kb = *reinterpret_cast<const uint16_t*>(a.cache.k_blocks + (ko >> 4));
-    }
+    vb = block_word<D>(a.cache.v_blocks, vo >> 4, &vat);
+    kb = block_word<D>(a.cache.k_blocks, ko >> 4, &kat);
   }
   // state: per key, bit 0: it exists; bit 1 (edge steps, where some row does not see some key): a block of
   // its values is NaN.  Those are stored as zeros, since their product with a zero weight would be NaN, and
@@ -555,20 +588,21 @@ struct Tile4Stage {
                                         int tid) {
     const int r = tid >> 3, part = tid & 7;
     int bits = ok;
+    unsigned byte = __builtin_amdgcn_ubfe(vb, vat + 8 * (part * (D / 8) / 32), 8);
     if (!ok) {
       v = u32x2{0, 0};
-      vb = 127;
+      byte = 0;
     }
     if (edge) {
-      const bool f = vb == 255;
+      const bool f = byte == 255;
       if (f) {
         v = u32x2{0, 0};
-        vb = 127;
+        byte = 0;
       }
       const uint64_t m = __ballot(f) >> (tid & 56);  // of this key's eighths
       if (m & 0xFF) bits |= 2;
     }
-    const float step = block_step(vb);
+    const float step = block_step(byte);
     if constexpr (D == 128) {
       *reinterpret_cast<u32x2*>(kt + k4_unit<D>(r, part >> 1) + 8 * (part & 1)) = k;
       *reinterpret_cast<u32x4*>(vt + v_unit<D>(r, 2 * part)) = fp4x8_to_bf16(v[0], step);
@@ -578,7 +612,7 @@ struct Tile4Stage {
       *reinterpret_cast<u32x4*>(vt + v_unit<D>(r, part)) = fp4x8_to_bf16(v[0], step);
     }
     if (part == 0) {
-      kbt[r] = kb;
+      kbt[r] = kb >> kat;
       state[r] = bits;
     }
   }

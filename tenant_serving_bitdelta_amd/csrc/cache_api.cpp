@@ -55,6 +55,7 @@ PagedCache paged_cache(const bitdelta_kv_cache& c) {
   p.v_page = (uint32_t)(bytes(c.v_stride_page, c.num_pages) / 16);
   p.v_token = (uint32_t)(bytes(c.v_stride_token, c.page_size) / 16);
   p.v_head = bytes(c.v_stride_head, c.kv_heads);
+  p.alike = p.k_page == p.v_page && p.k_token == p.v_token && p.k_head == p.v_head;
   p.num_pages = c.num_pages;
   p.page_size = c.page_size;
   p.div = make_page_div((uint32_t)c.page_size);
