@@ -147,7 +147,8 @@ struct AttendArgs {
   float c;                      // scale * k_scale * log2(e): scores enter exp2
   float v_scale;
   int32_t workers;              // row kernel workgroups
-  int32_t tile_workers;         // tile kernel workgroups that split the prefixes
+  int32_t tile_workers;         // tile kernel workgroups that split the prefixes (4 bits: or a window's rest)
+  int32_t tile_parts;           // 4 bits, window: parts that a unit's keys are split into, at most
   int32_t halves;               // tile kernel: units of up to 128 rows take two key tiles a step
   int32_t row_prefix;           // row kernel: 1 = a sequence's keys start with its prefix
   int32_t direct;               // row kernel: one workgroup per unit, written without partials
@@ -170,6 +171,8 @@ hipError_t launch_attend_tiles(const AttendArgs& a, int dim, bool fp8, bool pref
 // the same for a 4-bit cache
 hipError_t launch_attend4_rows(const AttendArgs& a, int dim, int columns, int blocks, hipStream_t stream);
 hipError_t launch_attend4_tiles(const AttendArgs& a, int dim, bool prefix, int blocks, hipStream_t stream);
+// joins the parts of at most `units` split units
+hipError_t launch_attend4_join(const AttendArgs& a, int dim, int units, hipStream_t stream);
 // many: rows of so many pieces that a workgroup's waves share one's
 hipError_t launch_attend_combine(const AttendArgs& a, int dim, bool many, hipStream_t stream);
 

@@ -552,6 +552,26 @@ struct Key4Lookup {
   }
 };
 
+// Work of a tile launch over `units` (sequence, row tile, kv head) on `workers` compute units: as many whole
+// units as fill them a number of times, then the rest's keys cut into as many parts as fill them once more
+// (at most `most`): few units use the whole machine, and many end together (the last 8 of 1288 units, left
+// whole, kept 8 compute units busy for a sixth of the time).
+struct TileWork {
+  int unit;  // -1: none
+  int part, parts;
+  int slot;  // of the part's sums
+};
+__device__ __forceinline__ TileWork tile_work(int units, int workers, int most, int w) {
+  const int rest = most > 1 ? units % workers : 0, whole = units - rest;
+  if (w < whole) return TileWork{w, 0, 1, 0};
+  const int j = w - whole;
+  if (rest == 0) return TileWork{-1, 0, 1, 0};
+  const int parts = min(workers / rest, most);
+  if (j >= rest * parts) return TileWork{-1, 0, 1, 0};
+  const int part = j / rest, unit = j - part * rest;
+  return TileWork{whole + unit, part, parts, unit * parts + part};
+}
+
 // What a thread moves of a step: an eighth of a key's rows, D / 16 bytes each of K and V, and the key's scale
 // bytes.
 template <int D>
@@ -671,12 +691,15 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
       const RowUnit u = row_unit(a, b);
       return (u.nq + tpt - 1) / tpt;
     });
+    if (blockIdx.x == 0 && a.tile_parts > 1)  // for the joining kernel
+      for (int i = tid; i <= a.batch; i += 512) a.scan[i] = scan[i];
   }
 
   while (x < x_end) {
     KeyList kl;
     int t0, nt, p0 = 0, h, s_begin, s_end;
     int64_t slot = 0;
+    int parts = 1;  // that the unit's keys are split into
     if constexpr (PREFIX) {
       const int sg = scan_find(scan, a.nseg, (int)(x / a.kv_heads));
       const int n0 = a.seg_offsets[sg], n = a.seg_offsets[sg + 1] - n0;
@@ -698,10 +721,12 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
     } else {
       // heads fastest: with a multiple of 8 kv heads each XCD serves its own heads.  Later tiles
       // see more keys: they start first.
-      const int tiles = scan[a.batch];
-      const int ti = tiles - 1 - (int)blockIdx.x / a.kv_heads;
-      if (ti < 0) return;
-      h = (int)blockIdx.x % a.kv_heads;
+      const TileWork w = tile_work(uniform(scan[a.batch]) * a.kv_heads, a.tile_workers, a.tile_parts, blockIdx.x);
+      if (w.unit < 0) return;
+      const int ti = uniform(scan[a.batch]) - 1 - w.unit / a.kv_heads;
+      h = w.unit % a.kv_heads;
+      parts = w.parts;
+      slot = w.slot;
       const int b = scan_find(scan, a.batch, ti);
       const RowUnit u = row_unit(a, b);
       const int rt = ti - scan[b];
@@ -711,8 +736,9 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
       // keys up to the tile's last token
       const int len = p0 + nt < 0 ? 0 : p0 + nt;
       kl = window_keys(a.table + (int64_t)b * a.width, a.width, len, p0, a.window, a.sinks);
-      s_begin = 0;
-      s_end = (kl.n + kTileKeys - 1) / kTileKeys;
+      const int steps = (kl.n + kTileKeys - 1) / kTileKeys;
+      s_begin = (int)((int64_t)steps * w.part / parts);
+      s_end = (int)((int64_t)steps * (w.part + 1) / parts);
     }
 
     // ---- this lane's query row: 32 * wave + q of the tile
@@ -937,7 +963,7 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
     // ---- epilogue: lane (q, hf) holds dims 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
     l = half_sum(l);
     if (live) {
-      if constexpr (PREFIX) {
+      if (PREFIX || parts > 1) {
         const int64_t at = slot * kTileRows + row;
         float* op = a.tile_o + at * D + 4 * hf;
 #pragma unroll
@@ -966,6 +992,68 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
       }
     }
     if constexpr (!PREFIX) break;
+  }
+}
+
+// Joins the parts of split units: a wave per query row, lanes of 4 dims, 64 / (D / 4) parts side by side,
+// four loads each in flight, in a fixed order.
+template <int D>
+__global__ __launch_bounds__(256) void attend4_join_kernel(const AttendArgs a) {
+  constexpr int kQ = D / 4, kWays = 64 / kQ;
+  const int lane = threadIdx.x & 63;
+  const int i = blockIdx.x / (kTileRows / 4);  // of the split units
+  const int row = (blockIdx.x % (kTileRows / 4)) * 4 + (threadIdx.x >> 6);
+  const int tpt = kTileRows / a.group;
+  const int tiles = a.scan[a.batch], units = tiles * a.kv_heads;
+  const int rest = units % a.tile_workers, whole = units - rest;
+  if (i >= rest) return;
+  const int parts = min(a.tile_workers / rest, a.tile_parts);
+  if (parts == 1) return;
+  const int unit = whole + i, h = unit % a.kv_heads;
+  const int ti = tiles - 1 - unit / a.kv_heads;
+  const int b = scan_find(a.scan, a.batch, ti);
+  const RowUnit u = row_unit(a, b);
+  const int t = (ti - a.scan[b]) * tpt + row / a.group, hh = h * a.group + row % a.group;
+  if (row >= tpt * a.group || t >= u.nq) return;
+  const int d4 = lane % kQ, way = lane / kQ;
+  float mx = kNegInf, lt = 0.f;
+  f32x4 ot = {0.f, 0.f, 0.f, 0.f};
+  auto add = [&](float pm, float pl, const f32x4& po) {
+    const float mn = fmaxf(mx, pm);
+    const float mb = mn == kNegInf ? 0.f : mn;
+    const float f0 = exp2_fast(mx - mb), f1 = exp2_fast(pm - mb);
+    lt = lt * f0 + pl * f1;
+    ot = ot * f0 + po * f1;
+    mx = mn;
+  };
+  for (int p0 = way; p0 < parts; p0 += 4 * kWays) {
+    f32x2 pm[4];
+    f32x4 po[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = (int64_t)(i * parts + min(p0 + k * kWays, parts - 1)) * kTileRows + row;
+      pm[k] = *reinterpret_cast<const f32x2*>(a.tile_ml + at * 2);
+      po[k] = *reinterpret_cast<const f32x4*>(a.tile_o + at * D + 4 * d4);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (p0 + k * kWays < parts) add(pm[k][0], pm[k][1], po[k]);
+  }
+#pragma unroll
+  for (int d = kQ; d < 64; d <<= 1) {
+    const float om = __shfl_xor(mx, d, 64), ol = __shfl_xor(lt, d, 64);
+    f32x4 oo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) oo[e] = __shfl_xor(ot[e], d, 64);
+    add(om, ol, oo);
+  }
+  if (way == 0) {
+    const float inv = lt > 0.f ? a.v_scale / lt : (lt == 0.f ? 0.f : lt);
+    const int64_t tok = u.t0 + t;
+    *reinterpret_cast<u32x2*>(a.out + tok * a.o_token + (int64_t)hh * a.o_head + 4 * d4) =
+        u32x2{pack_bf16(ot[0] * inv, ot[1] * inv), pack_bf16(ot[2] * inv, ot[3] * inv)};
+    if (a.lse && d4 == 0)
+      a.lse[tok * a.heads + hh] = lt == 0.f ? kNegInf : (mx + __builtin_log2f(lt)) * kLn2;
   }
 }
 
@@ -1000,6 +1088,16 @@ hipError_t launch_attend4_tiles(const AttendArgs& a, int dim, bool prefix, int b
   else if (dim == 64) hipLaunchKernelGGL((attend4_tile_kernel<64, false>), dim3(blocks), dim3(512), 0, stream, a);
   else if (dim == 128 && prefix) hipLaunchKernelGGL((attend4_tile_kernel<128, true>), dim3(blocks), dim3(512), 0, stream, a);
   else if (dim == 128) hipLaunchKernelGGL((attend4_tile_kernel<128, false>), dim3(blocks), dim3(512), 0, stream, a);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+hipError_t launch_attend4_join(const AttendArgs& a, int dim, int units, hipStream_t stream) {
+  if (units < 1 || units > a.tile_workers) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)units * (kTileRows / 4));
+  clear_stale_error();
+  if (dim == 64) hipLaunchKernelGGL(attend4_join_kernel<64>, grid, dim3(256), 0, stream, a);
+  else if (dim == 128) hipLaunchKernelGGL(attend4_join_kernel<128>, grid, dim3(256), 0, stream, a);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }

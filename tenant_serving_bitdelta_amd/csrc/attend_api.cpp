@@ -29,6 +29,8 @@ int row_workers(int columns, int64_t max_q, const bitdelta_kv_cache& c) {
   return columns <= 2 ? 512 : 256;
 }
 constexpr int kTileWorkers = 256;
+// Steps of 64 keys that a part of a split unit has at least: it begins with three dependent readings.
+constexpr int kPartSteps = 4;
 
 // A unit (sequence, kv head) whose key list is at most this many 128-key steps long is done by one
 // workgroup, without partials and the launch that joins them.  Few units: a step takes such a
@@ -65,6 +67,7 @@ struct Plan {
   int row_rows;        // rows of a row unit
   int64_t row_units, row_workers;
   int64_t tile_units, tile_workers;
+  int tile_parts;      // 4 bits, window
   size_t scan_bytes, row_o, row_ml, segs_bytes, tile_o, tile_ml;
   size_t total;
 };
@@ -78,6 +81,12 @@ void lay_out(Plan* p, int64_t batch, int dim) {
     p->scan_bytes = up256((size_t)(batch + 1) * 4);
     p->row_o = up256(slots * dim * 4);
     p->row_ml = up256(slots * 8);
+  }
+  if (p->kind == Kind::kTiles && p->tile_parts > 1) {
+    p->scan_bytes = up256((size_t)(batch + 1) * 4);
+    const size_t slots = (size_t)p->tile_workers * bd::kTileRows;
+    p->tile_o = up256(slots * dim * 4);
+    p->tile_ml = up256(slots * 8);
   }
   if (p->kind == Kind::kPrefixTiles) {
     const size_t slots = (size_t)(p->tile_units + p->tile_workers) * bd::kTileRows;
@@ -162,6 +171,13 @@ Plan plan_window(int32_t heads, const bitdelta_kv_cache& c, int32_t batch, int32
   const int64_t rows = (int64_t)max_q * group;
   if (tiles_for_rows(rows, (int64_t)batch * c.kv_heads)) {
     p.kind = Kind::kTiles;
+    if (c.dtype == BITDELTA_KV_FP4) {
+      const int64_t keys = std::min<int64_t>((int64_t)width * c.page_size,
+                                             (int64_t)window + bd::kTileRows / group - 1 + sinks);
+      p.tile_workers = kTileWorkers;
+      p.tile_parts = (int)std::min<int64_t>(kTileWorkers, keys / (kPartSteps * bd::kTileKeys));
+      lay_out(&p, batch, c.head_dim);
+    }
     return p;
   }
   p.row_rows = (int)rows;
@@ -202,6 +218,7 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
   a->rows = p.row_rows;
   a->workers = (int)p.row_workers;
   a->tile_workers = (int)p.tile_workers;
+  a->tile_parts = p.tile_parts;
   a->halves = !fp8 && !fp4;
   a->direct = p.kind == Kind::kRows;
   a->row_prefix = a->nseg > 0 && p.kind != Kind::kPrefixTiles;
@@ -222,9 +239,14 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
     // each sequence rounds its tokens up to whole tiles
     const int64_t tiles = std::min<int64_t>(a->tokens / tpt + a->batch,
                                             a->batch * (((int64_t)a->max_q + tpt - 1) / tpt));
-    const int blocks = (int)(tiles * a->kv_heads);
-    return bd::status_of_hip(fp4 ? bd::launch_attend4_tiles(*a, c.head_dim, false, blocks, st)
-                                 : bd::launch_attend_tiles(*a, c.head_dim, fp8, false, blocks, st));
+    const int units = (int)(tiles * a->kv_heads);
+    if (!fp4) return bd::status_of_hip(bd::launch_attend_tiles(*a, c.head_dim, fp8, false, units, st));
+    if (p.tile_parts < 2) return bd::status_of_hip(bd::launch_attend4_tiles(*a, c.head_dim, false, units, st));
+    // of the units, at most these, the rest that does not fill the machine is split: to once its workgroups
+    const int blocks = (units / kTileWorkers + 1) * kTileWorkers;
+    const bitdelta_status s = bd::status_of_hip(bd::launch_attend4_tiles(*a, c.head_dim, false, blocks, st));
+    if (s != BITDELTA_OK) return s;
+    return bd::status_of_hip(bd::launch_attend4_join(*a, c.head_dim, std::min(units, kTileWorkers), st));
   }
   if (p.kind == Kind::kPrefixTiles) {
     // the grid holds whole runs of tile_workers / 8 per XCD

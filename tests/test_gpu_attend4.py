@@ -191,6 +191,42 @@ def test_window(case):
     check(out, lse, window_ref(qf, c, page, table, lens, q_lens, window, sinks, sc, dim ** -0.5))
 
 
+# chunks whose units' keys are split into parts: new tokens, tokens with them, heads, kv heads, dim, window,
+# sinks, table pages beyond need, and rows to look at (None: all)
+SPLIT = [
+    ([100], [3000], 8, 2, 128, 5000, 0, 0, None),
+    ([33, 70, 0, 1], [5000, 2000, 40, 1], 12, 4, 64, 3000, 5, 9, None),
+    ([9, 40], [700, 30], 16, 1, 128, 1200, 2, 500, None),  # parts without keys
+    ([1056], [2600], 64, 4, 128, 1400, 4, 0, 61),          # 264 units: 8 of them split
+    ([700, 400], [700, 900], 32, 8, 64, 4096, 0, 0, 41),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SPLIT)))
+def test_chunks_split_over_workgroups(case):
+    q_lens, lens, heads, hk, dim, window, sinks, extra, some = SPLIT[case]
+    rng = np.random.default_rng(300 + case)
+    table, c, q, qf, offs = _setup(rng, q_lens, lens, heads, hk, dim, extra=extra)
+    out, lse = bd.attend_window(q, c.k, c.v, i32(table), i32(lens), window, sinks, q_offsets=offs,
+                                max_q_len=max(q_lens), return_lse=True, **c.kw())
+    assert bd.attend_window_workspace_bytes(c.k, heads, i32(table), sum(q_lens), max(q_lens), window, sinks) > 0
+    n = sum(q_lens)
+    pick = range(n) if some is None else sorted({0, 1, n - 1, *range(0, n, n // some)})
+    at, ref = 0, {}
+    for b, m in enumerate(q_lens):
+        length = lens[b]
+        k, p = rows(c.kf, table[b], length, 16, 1.0)
+        v, _ = rows(c.vf, table[b], length, 16, 1.0)
+        j = np.arange(length)
+        for t in pick:
+            if at <= t < at + m:
+                pos = length - m + t - at
+                ref[t] = attend(qf[t], k, v, p & (j <= pos) & ((pos - j < window) | (j < sinks)), dim ** -0.5)
+        at += m
+    pick = list(pick)
+    check(out[pick], lse[pick], [ref[t] for t in pick])
+
+
 def _setup(rng, q_lens, lens, heads=8, hk=2, dim=128, page=16, extra=0):
     need = sum(-(-x // page) for x in lens) + 1
     free = list(rng.permutation(need))
