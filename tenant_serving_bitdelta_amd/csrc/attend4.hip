@@ -516,7 +516,7 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
 // Byte offset of 16-byte unit u (32 dims) of row r in a K tile: a wave's reads take one unit of 32 rows
 template <int D>
 __device__ __forceinline__ unsigned k4_unit(int r, int u) {
-  return D == 128 ? (unsigned)(r * 64 + ((u ^ ((r >> 2) & 3)) << 4)) : (unsigned)(r * 32 + (u << 4));
+  return D == 128 ? (unsigned)(r * 64 + ((u ^ ((r >> 1) & 3)) << 4)) : (unsigned)(r * 32 + (u << 4));
 }
 
 __device__ __forceinline__ f32x16 mfma_k32(const u32x4& k, int k_bytes, bool odd_step, const i32x8& q, int q_bytes,
@@ -638,10 +638,9 @@ struct Tile4Stage {
   }
 };
 
-__device__ __forceinline__ int prefix_steps(const AttendArgs& a, int sg) {
-  const int len = clamp_len(a.prefix_lens[sg], a.pwidth, a.cache.page_size);
-  return (len + kTileKeys - 1) / kTileKeys;
-}
+// prefixes may take two key tiles a step
+constexpr int tile4_buffers(bool prefix) { return prefix ? 4 : 2; }
+constexpr int tile4_lds(int D, bool prefix) { return tile4_buffers(prefix) * kTileKeys * (D * 2 + D / 2); }
 
 template <int D, bool PREFIX>
 __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a) {
@@ -649,10 +648,11 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
   constexpr int kTileK = kTileKeys * D / 2;
   constexpr int kSteps = D / 64;   // matrix steps over D of a score tile
   constexpr int kOut = D / 32;     // 32-row tiles of O^T
-  __shared__ __attribute__((aligned(16))) unsigned char kbuf[2][kTileK];
-  __shared__ __attribute__((aligned(16))) unsigned char vbuf[2][kTile];
-  __shared__ unsigned kbytes[2][kTileKeys];
-  __shared__ int state[2][kTileKeys];
+  constexpr int kBuffers = tile4_buffers(PREFIX);
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // K tiles, then V tiles
+  unsigned char* const vbuf = smem + kBuffers * kTileK;
+  __shared__ unsigned kbytes[kBuffers][kTileKeys];
+  __shared__ int state[kBuffers][kTileKeys];
   __shared__ Row4Place places[4][kTileKeys];
   __shared__ int entries[8][kTileKeys];
   __shared__ int scan[kAttendMaxSeqs + 1];
@@ -700,12 +700,14 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
     int t0, nt, p0 = 0, h, s_begin, s_end;
     int64_t slot = 0;
     int parts = 1;  // that the unit's keys are split into
+    bool half = false;  // the unit's rows fill at most half the waves: the others take a second key tile
     if constexpr (PREFIX) {
       const int sg = scan_find(scan, a.nseg, (int)(x / a.kv_heads));
       const int n0 = a.seg_offsets[sg], n = a.seg_offsets[sg + 1] - n0;
       const int len = clamp_len(a.prefix_lens[sg], a.pwidth, a.cache.page_size);
       const int steps = prefix_steps(a, sg);
       const int tiles = (n + tpt - 1) / tpt;
+      half = halved(a, sg);
       int64_t r = x - (int64_t)scan[sg] * a.kv_heads;  // units: kv head major, then row tile
       h = (int)(r / ((int64_t)tiles * steps));
       r -= (int64_t)h * tiles * steps;
@@ -713,6 +715,10 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
       s_begin = (int)(r - (int64_t)rt * steps);
       s_end = (int)(x_end - x < steps - s_begin ? s_begin + (x_end - x) : steps);
       x += s_end - s_begin;
+      if (half) {
+        s_begin *= 2;
+        s_end = min(2 * s_end, (len + kTileKeys - 1) / kTileKeys);
+      }
       t0 = n0 + rt * tpt;
       nt = n - rt * tpt < tpt ? n - rt * tpt : tpt;
       slot = w_id + (int64_t)segs[sg] * a.kv_heads + h * tiles + rt;
@@ -741,14 +747,15 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
       s_end = (int)((int64_t)steps * (w.part + 1) / parts);
     }
 
-    // ---- this lane's query row: 32 * wave + q of the tile
-    const int row = 32 * wave + q;
+    // ---- this lane's query row: 32 * (wave's rows) + q of the tile
+    const int wave_rows = half ? wave & 3 : wave;
+    const int row = 32 * wave_rows + q;
     const int t = row / a.group, hh = h * a.group + row - t * a.group;
     const bool live = t < nt;
     const int pq = p0 + t;
     // positions of the wave's first and last live token
-    const int wt0 = 32 * wave / a.group;
-    const int wt1 = (32 * wave + 31) / a.group < nt ? (32 * wave + 31) / a.group : nt - 1;
+    const int wt0 = 32 * wave_rows / a.group;
+    const int wt1 = (32 * wave_rows + 31) / a.group < nt ? (32 * wave_rows + 31) / a.group : nt - 1;
     const bool wave_live = wt0 < nt;
     // the lane's dims of step d: 64 d + 16 hf .. + 15 and 64 d + 32 + 16 hf .. + 15
     i32x8 q_hi[kSteps], q_lo[kSteps];
@@ -785,7 +792,6 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
     // The pipeline: the keys of step t are looked up by one wave (wave t mod 8, one lane a key).
     // Table entries are copied into LDS, so that no register waits for them; two steps later the
     // rows' offsets are worked out, and a step later the rows' loads begin.
-    constexpr int kAhead = 2;  // steps from the loads to the step they are for
     auto look_begin = [&](int s) {
       if (((s - s_begin) & 7) == wave) {
         const Key4Lookup look(a.cache, kl, s * kTileKeys + lane);
@@ -805,16 +811,34 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
       return base < kl.na || last > p0 || p0 + nt - 1 - f >= a.window;
     };
     const int64_t k_head = (int64_t)h * a.cache.k_head, v_head = (int64_t)h * a.cache.v_head;
-    Tile4Stage<D> st;
-    for (int i = 0; i < kAhead + 3; ++i) look_begin(s_begin + i);
+    Tile4Stage<D> st[PREFIX ? 2 : 1];
+    auto fetch = [&](int s) {
+      st[0].fetch(a, k_head, v_head, places[(s - s_begin) & 3], tid);
+      if (PREFIX && half) st[PREFIX].fetch(a, k_head, v_head, places[(s + 1 - s_begin) & 3], tid);
+    };
+    auto store_one = [&](Tile4Stage<D>& t, int s) {
+      const int buf = (s - s_begin) & (kBuffers - 1);
+      t.store(smem + buf * kTileK, kbytes[buf], vbuf + buf * kTile, state[buf], hides(s * kTileKeys), tid);
+    };
+    auto store = [&](int s) {
+      store_one(st[0], s);
+      if (PREFIX && half) store_one(st[PREFIX], s + 1);
+    };
+    const int take = PREFIX && half ? 2 : 1;  // key tiles a step
+    for (int i = 0; i < (take == 2 ? 8 : 5); ++i) look_begin(s_begin + i);
     wait_copies<0>();
     __syncthreads();  // the last unit's tiles and notes are no longer read
-    for (int i = 0; i <= kAhead; ++i) look_end(s_begin + i);
+    for (int i = 0; i < (take == 2 ? 4 : 3); ++i) look_end(s_begin + i);
     __syncthreads();
-    st.fetch(a, k_head, v_head, places[0], tid);
-    st.store(kbuf[0], kbytes[0], vbuf[0], state[0], hides(s_begin * kTileKeys), tid);
-    st.fetch(a, k_head, v_head, places[1], tid);
+    fetch(s_begin);
+    store(s_begin);
+    fetch(s_begin + take);
     __syncthreads();
+    if (take == 2) {
+      for (int i = 4; i < 6; ++i) look_end(s_begin + i);
+      for (int i = 8; i < 10; ++i) look_begin(s_begin + i);
+      lds_barrier();
+    }
 
     // O^T += V^T P^T of step s: of 16 keys the lane's 8 are 4 hf .. + 3 and 8 + 4 hf .. + 3
     u32x4 p[4];
@@ -823,7 +847,7 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
     const int v_b = 8 * (l16 & 1);
     u32x4 vf[2][kOut];
     auto read_values = [&](int buf, int kb) {
-      const unsigned char* vt = vbuf[buf];
+      const unsigned char* vt = vbuf + buf * kTile;
 #pragma unroll
       for (int i = 0; i < kOut; ++i) {
         const u32x2 lo = lds_read_tr(vt + v_unit<D>(16 * kb + v_row, 4 * i + v_un) + v_b);
@@ -831,11 +855,13 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
         vf[kb & 1][i] = u32x4{lo[0], lo[1], hi[0], hi[1]};
       }
     };
-    for (int s = s_begin; s < s_end; ++s) {
-      const int buf = (s - s_begin) & 1;
+    for (int s0 = s_begin; s0 < s_end; s0 += take) {
+      const int s = s0 + (half ? wave >> 2 : 0);  // this wave's tile
+      const int buf = (s - s_begin) & (kBuffers - 1);
       const int base = s * kTileKeys;
       const int key_state = state[buf][lane];
-      const uint64_t valid = __ballot(key_state & 1);
+      uint64_t valid = __ballot(key_state & 1);
+      if (PREFIX && s >= s_end) valid = 0;
       uint64_t odd = PREFIX ? 0 : __ballot(key_state & 2);  // keys whose values were taken out
       // does the wave see anything, does every row see everything?
       bool any = wave_live && valid != 0, all = valid == ~0ull;
@@ -859,7 +885,7 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
           kb[i] = (int)(kbytes[buf][32 * i + q] >> (8 * hf));
 #pragma unroll
           for (int d = 0; d < kSteps; ++d)
-            kf[i][d] = *reinterpret_cast<const u32x4*>(kbuf[buf] + k4_unit<D>(32 * i + q, 2 * d + hf));
+            kf[i][d] = *reinterpret_cast<const u32x4*>(smem + buf * kTileK + k4_unit<D>(32 * i + q, 2 * d + hf));
         }
 #pragma unroll
         for (int d = 0; d < kSteps; ++d) {
@@ -871,12 +897,12 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
       }
       // ---- the next step's tiles; these buffers were last read before the barrier that began
       // this step
-      if (s + 1 < s_end) {
-        st.store(kbuf[buf ^ 1], kbytes[buf ^ 1], vbuf[buf ^ 1], state[buf ^ 1], hides(base + kTileKeys), tid);
-        st.fetch(a, k_head, v_head, places[(s + 2 - s_begin) & 3], tid);
-        // (the loads that st.store waited for are newer than the entries')
-        look_end(s + 3);
-        look_begin(s + 5);
+      if (s0 + take < s_end) {
+        store(s0 + take);
+        fetch(s0 + 2 * take);
+        // (the loads that the store waited for are newer than the entries')
+        for (int i = 0; i < take; ++i) look_end(s0 + 3 * take + i);
+        for (int i = 0; i < take; ++i) look_begin(s0 + 5 * take + i);
       }
       if (any) {
         // lane (q, hf) holds keys 32 i + 8 (e / 4) + 4 hf + e % 4 of its row
@@ -964,7 +990,7 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
     l = half_sum(l);
     if (live) {
       if (PREFIX || parts > 1) {
-        const int64_t at = slot * kTileRows + row;
+        const int64_t at = slot * kTileRows + row + (half ? (wave >> 2) * (kTileRows / 2) : 0);
         float* op = a.tile_o + at * D + 4 * hf;
 #pragma unroll
         for (int i = 0; i < kOut; ++i)
@@ -1072,6 +1098,18 @@ hipError_t rows_for(const AttendArgs& a, int columns, int blocks, hipStream_t st
   return hipGetLastError();
 }
 
+template <int D, bool PREFIX>
+hipError_t tiles_for(const AttendArgs& a, int blocks, hipStream_t stream) {
+  constexpr int lds = tile4_lds(D, PREFIX);
+  static DeviceOnce once;
+  const hipError_t e =
+      set_dynamic_lds_once(once, reinterpret_cast<const void*>(&attend4_tile_kernel<D, PREFIX>), lds);
+  if (e != hipSuccess) return e;
+  clear_stale_error();
+  hipLaunchKernelGGL((attend4_tile_kernel<D, PREFIX>), dim3(blocks), dim3(512), lds, stream, a);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_attend4_rows(const AttendArgs& a, int dim, int columns, int blocks, hipStream_t stream) {
@@ -1083,13 +1121,9 @@ hipError_t launch_attend4_rows(const AttendArgs& a, int dim, int columns, int bl
 
 hipError_t launch_attend4_tiles(const AttendArgs& a, int dim, bool prefix, int blocks, hipStream_t stream) {
   if (blocks < 1 || a.batch > kAttendMaxSeqs || a.nseg > kAttendMaxSegments) return hipErrorInvalidValue;
-  clear_stale_error();
-  if (dim == 64 && prefix) hipLaunchKernelGGL((attend4_tile_kernel<64, true>), dim3(blocks), dim3(512), 0, stream, a);
-  else if (dim == 64) hipLaunchKernelGGL((attend4_tile_kernel<64, false>), dim3(blocks), dim3(512), 0, stream, a);
-  else if (dim == 128 && prefix) hipLaunchKernelGGL((attend4_tile_kernel<128, true>), dim3(blocks), dim3(512), 0, stream, a);
-  else if (dim == 128) hipLaunchKernelGGL((attend4_tile_kernel<128, false>), dim3(blocks), dim3(512), 0, stream, a);
-  else return hipErrorInvalidValue;
-  return hipGetLastError();
+  if (dim == 64) return prefix ? tiles_for<64, true>(a, blocks, stream) : tiles_for<64, false>(a, blocks, stream);
+  if (dim == 128) return prefix ? tiles_for<128, true>(a, blocks, stream) : tiles_for<128, false>(a, blocks, stream);
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_attend4_join(const AttendArgs& a, int dim, int units, hipStream_t stream) {

@@ -219,7 +219,7 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
   a->workers = (int)p.row_workers;
   a->tile_workers = (int)p.tile_workers;
   a->tile_parts = p.tile_parts;
-  a->halves = !fp8 && !fp4;
+  a->halves = !fp8;
   a->direct = p.kind == Kind::kRows;
   a->row_prefix = a->nseg > 0 && p.kind != Kind::kPrefixTiles;
   auto take = [&](size_t bytes) {

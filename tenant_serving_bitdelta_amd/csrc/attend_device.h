@@ -263,5 +263,15 @@ __device__ __forceinline__ int scan_find(const int* scan, int count, int x) {
   return lo;
 }
 
+// segments whose rows fit half a tile: their units take two 64-key tiles a step
+__device__ __forceinline__ bool halved(const AttendArgs& a, int sg) {
+  return a.halves && (a.seg_offsets[sg + 1] - a.seg_offsets[sg]) * a.group <= kTileRows / 2;
+}
+__device__ __forceinline__ int prefix_steps(const AttendArgs& a, int sg) {
+  const int len = clamp_len(a.prefix_lens[sg], a.pwidth, a.cache.page_size);
+  const int keys = halved(a, sg) ? 2 * kTileKeys : kTileKeys;
+  return (len + keys - 1) / keys;
+}
+
 }  // namespace
 }  // namespace bd
