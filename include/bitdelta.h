@@ -516,7 +516,7 @@ typedef struct {
  * sequences share prefixes by segment: sequence b of segment g (seg_offsets as in
  * bitdelta_plan_segments: the requests of one variant share that variant's prompt) sees the
  * prefix_lens[g] prefix keys of row g of prefix_table, then its own lens[b] keys of row b of
- * table.  Where that saves 128 MiB of reading and more, going by prefix_width, a segment's prefix is
+ * table.  Where that saves 128 MiB (FP4: 400) of reading and more, going by prefix_width, a segment's prefix is
  * read once for up to 256 query rows (sequences x heads per kv head); else each sequence reads it.
  *
  *   rows          q, out: tokens = the number of sequences, in segment order.

@@ -1087,13 +1087,12 @@ template <int D>
 hipError_t rows_for(const AttendArgs& a, int columns, int blocks, hipStream_t stream) {
   clear_stale_error();
   const dim3 grid(blocks), block(256);
-  const bool multi = a.max_q > 1;
+  const bool multi = a.max_q > 1;  // (with more than 32 rows: the tile kernel)
   if (columns == 1 && !multi) hipLaunchKernelGGL((attend4_row_kernel<D, 1, false>), grid, block, 0, stream, a);
   else if (columns == 2 && !multi) hipLaunchKernelGGL((attend4_row_kernel<D, 2, false>), grid, block, 0, stream, a);
   else if (columns == 4 && !multi) hipLaunchKernelGGL((attend4_row_kernel<D, 4, false>), grid, block, 0, stream, a);
   else if (columns == 1) hipLaunchKernelGGL((attend4_row_kernel<D, 1, true>), grid, block, 0, stream, a);
   else if (columns == 2) hipLaunchKernelGGL((attend4_row_kernel<D, 2, true>), grid, block, 0, stream, a);
-  else if (columns == 4) hipLaunchKernelGGL((attend4_row_kernel<D, 4, true>), grid, block, 0, stream, a);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }

@@ -24,7 +24,7 @@ constexpr int64_t kMaxUnits = int64_t(1) << 21;  // sequences x kv heads
 // Workgroups of a split launch: as many as the 256 compute units hold at a time (more would start
 // when the first have ended, and take as long again), which their registers decide.
 int row_workers(int columns, int64_t max_q, const bitdelta_kv_cache& c) {
-  if (c.dtype == BITDELTA_KV_FP4) return columns == 1 ? 768 : (columns == 2 ? 512 : 256);
+  if (columns == 1 && c.dtype == BITDELTA_KV_FP4) return 768;
   if (columns == 1 && max_q == 1 && (c.dtype == BITDELTA_KV_FP8 || c.head_dim == 64)) return 768;
   return columns <= 2 ? 512 : 256;
 }
@@ -38,7 +38,13 @@ constexpr int kPartSteps = 4;
 // one sequence: 6 steps 18.0 against 20.7 us, 12 steps 30.6 against 21.0).  As many units as
 // workgroups at a time fill the machine unsplit (64 sequences: 12 steps 77 against 84 us); beyond
 // 12 steps one long list among short ones would be waited for.
-int direct_steps(int64_t units) { return units >= 512 ? 12 : 6; }
+// From 4 bits (64 sequences of up to the given length, 8 kv heads, one workgroup a unit against split and
+// joined): 2000 keys 28 against 37 us, 4000 46 against 50, 6000 66 against 63; 256 of up to 3000 108 against
+// 135.
+int direct_steps(int64_t units, int32_t dtype) {
+  if (units < 512) return 6;
+  return dtype == BITDELTA_KV_FP4 ? 32 : 12;
+}
 
 // Are prefixes worth a launch of their own?  Reading a prefix once per segment instead of once per
 // sequence saves this many bytes, most of which the caches would have served; the tile launch and its
@@ -46,6 +52,10 @@ int direct_steps(int64_t units) { return units >= 512 ? 12 : 6; }
 // against the row kernel: saving 67 MB 36.4 against 34.1 us, 101 MB 34.8 against 33.1, 201 MB 39.7
 // against 47.9, 503 MB 61.3 against 92.8.
 constexpr int64_t kShareBytes = int64_t(128) << 20;
+// From 4 bits, whose row kernel reads 3.8 times the keys in that time, rows against tiles: saving 111 MB 42
+// against 55 us, 134 MB 37 against 46, 267 MB 52 against 52, 446 MB 86 against 87, 508 MB 94 against 87,
+// 561 MB 115 against 91, 1.0 GB 147 against 115.
+constexpr int64_t kShareBytes4 = int64_t(400) << 20;
 
 // Does a call with several rows a unit go to the tile kernel?  Beyond 64 rows always.  Below, a tile
 // workgroup has idle rows, but reads a unit's keys at the same speed whatever its rows are, one unit a
@@ -53,7 +63,11 @@ constexpr int64_t kShareBytes = int64_t(128) << 20;
 // Rows x units at 4096 keys, bf16, head_dim 128, row against tile kernel: 64 x 8 39 against 86 us,
 // 64 x 64 84 against 85, 64 x 256 286 against 100, 32 x 64 47 against 81, 32 x 256 136 against 100,
 // 16 x 256 108 against 99.
-bool tiles_for_rows(int64_t rows, int64_t units) {
+// From 4 bits the tile kernel widens a tile's values once for its 8 waves and splits a unit's keys where
+// units are few: row against tile kernel, with what joins them, 64 x 8 29 against 20 us, 64 x 64 47 against
+// 40, 64 x 256 117 against 101, 32 x 8 20 against 18, 32 x 64 32 against 38, 32 x 256 80 against 97.
+bool tiles_for_rows(int64_t rows, int64_t units, int32_t dtype) {
+  if (dtype == BITDELTA_KV_FP4) return rows > 32;
   return rows > 64 || (rows > 32 && units >= 64) || (rows > 16 && units >= 192);
 }
 
@@ -145,9 +159,10 @@ Plan plan_shared(int64_t batch, int32_t heads, const bitdelta_kv_cache& c, int32
   for (int i = 0; i < nseg; ++i) used += offs[i + 1] > offs[i];
   const int64_t row_bytes = c.dtype == BITDELTA_KV_FP4 ? c.head_dim + c.head_dim / 16
                                                        : 2 * (int64_t)c.head_dim * (c.dtype == BITDELTA_KV_FP8 ? 1 : 2);
-  if (own + pre <= (int64_t)direct_steps(p.row_units) * bd::kRowStep) {
+  if (own + pre <= (int64_t)direct_steps(p.row_units, c.dtype) * bd::kRowStep) {
     p.kind = Kind::kRows;
-  } else if ((batch - used) * pre * c.kv_heads * row_bytes < kShareBytes) {
+  } else if ((batch - used) * pre * c.kv_heads * row_bytes <
+             (c.dtype == BITDELTA_KV_FP4 ? kShareBytes4 : kShareBytes)) {
     p.kind = Kind::kRowsSplit;
   } else {
     p.kind = Kind::kPrefixTiles;
@@ -169,7 +184,7 @@ Plan plan_window(int32_t heads, const bitdelta_kv_cache& c, int32_t batch, int32
   Plan p{};
   const int group = heads / c.kv_heads;
   const int64_t rows = (int64_t)max_q * group;
-  if (tiles_for_rows(rows, (int64_t)batch * c.kv_heads)) {
+  if (tiles_for_rows(rows, (int64_t)batch * c.kv_heads, c.dtype)) {
     p.kind = Kind::kTiles;
     if (c.dtype == BITDELTA_KV_FP4) {
       const int64_t keys = std::min<int64_t>((int64_t)width * c.page_size,
@@ -186,7 +201,7 @@ Plan plan_window(int32_t heads, const bitdelta_kv_cache& c, int32_t batch, int32
   const int64_t keys = std::min<int64_t>((int64_t)width * c.page_size,
                                          (int64_t)window + max_q - 1 + sinks);
   const int64_t steps = (keys + bd::kRowStep - 1) / bd::kRowStep;
-  p.kind = steps <= direct_steps(p.row_units) ? Kind::kRows : Kind::kRowsSplit;
+  p.kind = steps <= direct_steps(p.row_units, c.dtype) ? Kind::kRows : Kind::kRowsSplit;
   p.row_workers = std::min<int64_t>(row_workers(p.columns, max_q, c),
                                     std::max<int64_t>(1, p.row_units * steps));
   lay_out(&p, batch, c.head_dim);
@@ -261,7 +276,7 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
       fp4 ? bd::launch_attend4_rows(*a, c.head_dim, p.columns, blocks, st)
           : bd::launch_attend_rows(*a, c.head_dim, fp8, p.columns, blocks, st));
   if (s != BITDELTA_OK || p.kind == Kind::kRows) return s;
-  // pieces of a unit: MANY
+  // units of 32 pieces and more are few (64 rows of 96 pieces 5 us instead of 11)
   const bool many = fp4 && p.row_workers >= 32 * p.row_units;
   return bd::status_of_hip(bd::launch_attend_combine(*a, c.head_dim, many, st));
 }
