@@ -6,12 +6,16 @@
 //   s_j = c * (q . k_j),  c = scale * k_scale * log2(e)
 //   m = max_j s_j,  l = sum_j 2^(s_j - m),  o = v_scale / l * sum_j 2^(s_j - m) v_j
 // in one pass over the keys, with a running maximum and sum.
+#include <type_traits>
+
 #include "attend_device.h"
 
 namespace bd {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x6 __attribute__((ext_vector_type(6)));
+typedef float f32x32 __attribute__((ext_vector_type(32)));
 
 // 8 codes -> 8 bf16, times a power of two; exact
 __device__ __forceinline__ u32x4 fp4x8_to_bf16(unsigned v, float step) {
@@ -24,51 +28,83 @@ __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirs
 __device__ __forceinline__ float block_step(unsigned byte) { return __uint_as_float(byte << 23); }
 
 // ---------------------------------------------------------------------------------------------
-// Queries.  The scaled matrix instruction takes K's codes and scale bytes as they lie in memory; its
-// other operand is 8 bits wide, so a query row q goes in as two e4m3 rows of 4 significant bits each:
-// q / 2^e = hi + lo / 16, hi = q / 2^e rounded, lo what is left of it, times 16, rounded, with 2^e such
-// that the row's largest |q| / 2^e is in [128, 256).  A bf16 value has 8 bits: values down to 2^-9 of the
-// largest are exact, smaller ones off by at most 2^-20 of it.  A row with an infinity or NaN has the scale
-// byte 255, which makes its scores NaN.
+// Queries.  The scaled matrix instruction takes K's codes and scale bytes as they lie in memory, against
+// another operand of at most 8 bits a value, so a query goes in as four rows of e2m3 (4 significant bits, or
+// steps of 1/8 below 2): by blocks of 32 dims, q / 2^e = x0 + 2^-4 x1 + 2^-9 x2 + 2^-14 x3, where 2^e is the
+// smallest power of two with max |q| <= 7.5 * 2^e, and each x is what those before it leave, in its unit,
+// rounded.  x0 leaves at most 2^-2 (2^-4 of values below 2), x1 2^-8, x2 2^-13, x3 2^-18: a bf16 value's 8
+// bits are exact down to 2^-10, and smaller values off by at most 2^-19 of the block's largest: log-sums come
+// out 4e-8 off, as from a bf16 cache (two rows of e4m3, which take the same time, left those over few keys
+// 5e-6 off, three of e2m3 3e-6 in 98% of the time).  A block with an infinity or NaN has scale bytes 255,
+// which make its row's scores NaN.
 // ---------------------------------------------------------------------------------------------
-// 16 values (x: bf16 pairs) of a row -> their bytes of both parts; scales: bytes of e + 127 and e - 4 + 127
-__device__ __forceinline__ void split_query(const u32x4* x, unsigned scales, int* hi, int* lo) {
-  typedef short s16x2 __attribute__((ext_vector_type(2)));
-  const float step = block_step(scales & 0xFF), fine = block_step((scales >> 8) & 0xFF);
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {  // 4 values a word
-    s16x2 h = {0, 0}, l = {0, 0};
-    const unsigned a = x[w >> 1][2 * (w & 1)], b = x[w >> 1][2 * (w & 1) + 1];
-    const float f0 = bf16lo_to_f32(a), f1 = bf16hi_to_f32(a), f2 = bf16lo_to_f32(b), f3 = bf16hi_to_f32(b);
-    h = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(h, f0, f1, step, false);
-    h = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(h, f2, f3, step, true);
-    hi[w] = __builtin_bit_cast(int, h);
-    const f32x2 u = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi[w], step, false);
-    const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi[w], step, true);
-    l = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(l, f0 - u[0], f1 - u[1], fine, false);
-    l = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(l, f2 - v[0], f3 - v[1], fine, true);
-    lo[w] = __builtin_bit_cast(int, l);
-  }
+constexpr int kParts = 4;
+__device__ constexpr int part_shift(int k) { return k == 0 ? 0 : 5 * k - 1; }  // 0, 4, 9, 14
+struct Query {
+  i32x6 part[kParts];
+  int scales;  // bytes: e - part_shift(k) + 127
+};
+// 32 values / scale as e2m3 codes, to nearest even, at most 7.5: code 2 i from even[i], 2 i + 1 from odd[i].
+// (In assembly: the compiler gives its builtin's result registers that overlap the sources.)
+__device__ __forceinline__ i32x6 to_e2m3(const f32x16& even, const f32x16& odd, float scale) {
+  i32x6 r;
+  asm("v_cvt_scalef32_2xpk16_fp6_f32 %0, %1, %2, %3" : "=&v"(r) : "v"(even), "v"(odd), "v"(scale));
+  return r;
 }
-// largest |x| of 8 bf16 values, as its bits
-__device__ __forceinline__ unsigned top_bits(const u32x4& x) {
+__device__ __forceinline__ f32x32 e2m3_values(const i32x6& codes, float scale) {
+  f32x32 r;
+  asm("v_cvt_scalef32_pk32_f32_fp6 %0, %1, %2" : "=&v"(r) : "v"(codes), "v"(scale));
+  return r;
+}
+// x: 32 bf16 values
+__device__ __forceinline__ Query split_query(const u32x4* x) {
   u16x2 m = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[i] & 0x7FFF7FFFu));
-  return max((unsigned)m[0], (unsigned)m[1]);
-}
-// scale bytes of the two parts of a row whose largest value has these bits
-__device__ __forceinline__ unsigned query_scales(unsigned top) {
-  const int p = (int)(top >> 7);
-  const int hi = p == 255 ? 255 : max(p - 7, 5);
-  return (unsigned)hi | (unsigned)(p == 255 ? 255 : hi - 4) << 8;
+  for (int i = 0; i < 16; ++i)
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[i >> 2][i & 3] & 0x7FFF7FFFu));
+  const int top = max((int)m[0], (int)m[1]);  // bits of the largest |value|
+  const int exponent = top >> 7;
+  // (larger than need be where all values are below 2^-110, so that all scales are numbers)
+  const int e = max(exponent - 2 + ((top & 0x7F) > 0x70 ? 1 : 0), part_shift(kParts - 1) + 1);
+  Query q;
+  q.scales = 0;
+#pragma unroll
+  for (int k = 0; k < kParts; ++k) q.scales |= (exponent == 255 ? 255 : e - part_shift(k)) << (8 * k);
+  f32x16 even, odd;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    even[i] = bf16lo_to_f32(x[i >> 2][i & 3]);
+    odd[i] = bf16hi_to_f32(x[i >> 2][i & 3]);
+  }
+#pragma unroll
+  for (int k = 0; k < kParts; ++k) {
+    const float scale = block_step((unsigned)(e - part_shift(k)));
+    q.part[k] = to_e2m3(even, odd, scale);
+    if (k == kParts - 1) break;
+    const f32x32 v = e2m3_values(q.part[k], scale);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      even[i] -= v[2 * i];
+      odd[i] -= v[2 * i + 1];
+    }
+  }
+  return q;
 }
 
-__device__ __forceinline__ f32x4 mfma_k16(const u32x4& k, int k_byte, const i32x8& q, int q_bytes, bool low,
-                                          const f32x4& c) {
+// Part SEL of the queries against 16 (32) keys: c + K q, K's scale byte in byte BYTE of k_bytes
+template <int SEL>
+__device__ __forceinline__ f32x4 mfma_k16(const u32x4& k, int k_byte, const Query& q, const f32x4& c) {
   const i32x8 a = {(int)k[0], (int)k[1], (int)k[2], (int)k[3], 0, 0, 0, 0};
-  return low ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, q, c, 4, 0, 0, k_byte, 1, q_bytes)
-             : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, q, c, 4, 0, 0, k_byte, 0, q_bytes);
+  const i32x6& p = q.part[SEL];
+  const i32x8 b = {p[0], p[1], p[2], p[3], p[4], p[5], 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 2, 0, k_byte, SEL, q.scales);
+}
+template <int SEL, int BYTE>
+__device__ __forceinline__ f32x16 mfma_k32(const u32x4& k, int k_bytes, const Query& q, const f32x16& c) {
+  const i32x8 a = {(int)k[0], (int)k[1], (int)k[2], (int)k[3], 0, 0, 0, 0};
+  const i32x6& p = q.part[SEL];
+  const i32x8 b = {p[0], p[1], p[2], p[3], p[4], p[5], 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 2, BYTE, k_bytes, SEL, q.scales);
 }
 
 // NaN if the block of dim d of a value row is NaN, else 0; blocks: the row's scale bytes
@@ -80,8 +116,8 @@ __device__ __forceinline__ float odd_block(const unsigned char* blocks, int d) {
 // Row kernel: up to 16 * NC query rows (the heads of one kv head, for one or a few tokens) against a key
 // list, each of a workgroup's 4 waves 32 keys of a 128-key step on its own.  A lane's 16 bytes of a K row
 // are one block of 32 dims, as the scaled matrix instruction wants its operand (dim 64: one row in the
-// first two lane groups, another, 16 keys on, in the last two; each is met by a query operand that is zero
-// in the other half).  V rows are widened to bf16 into 8 KiB of the wave's LDS, and read transposed.
+// first two lane groups, another, 16 keys on, in the last two, whose queries are zeros; for the others' turn
+// the halves change places).  V rows are widened to bf16 into 8 KiB of the wave's LDS, and read transposed.
 // ---------------------------------------------------------------------------------------------
 // The aligned word with the scale bytes of the row at byte o of the scale bytes (dim 64: a row has two, at
 // bits 0 or 16; the word's other half is a neighbour's, or behind the array's end in the same word, and is
@@ -96,10 +132,8 @@ template <int D, int NC>
 struct Row4Loop {
   static constexpr int kLoads = D / 64;   // keys a lane has a block of, per step
   static constexpr int kTiles = D / 16;   // 16-row tiles of O^T
-  static constexpr int kWords = D / 16;   // dwords of a query operand (dim 64: its half that is not zero)
 
-  int hi[NC][kWords], lo[NC][kWords];
-  int scales[NC];
+  Query q[NC];
   f32x4 o[NC][kTiles];
   float m[NC], l[NC];
   int pos[NC];   // the column's token position (window op with several tokens)
@@ -198,32 +232,30 @@ struct Row4Loop {
   }
   // column j of block c is query row 16 c + j; row: this lane's, or null
   __device__ __forceinline__ void load_query(int c, const uint16_t* row, int g) {
-    constexpr int kHalves = D / 64;
-    u32x4 x[kHalves][2];
-    unsigned top = 0;
+    u32x4 x[4];
+    const bool live = row && (D == 128 || g < 2);
 #pragma unroll
-    for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x[h][i] = row ? *reinterpret_cast<const u32x4*>(row + 64 * h + 16 * g + 8 * i) : u32x4{0, 0, 0, 0};
-        top = max(top, top_bits(x[h][i]));
-      }
-    // (bits of values that are not negative order as they do)
-    top = __float_as_uint(half_max(row_max(__uint_as_float(top << 16)))) >> 16;
-    scales[c] = (int)query_scales(top);
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h) split_query(x[h], (unsigned)scales[c], hi[c] + 4 * h, lo[c] + 4 * h);
+    for (int i = 0; i < 4; ++i)
+      x[i] = live ? *reinterpret_cast<const u32x4*>(row + 32 * block(g) + 8 * i) : u32x4{0, 0, 0, 0};
+    q[c] = split_query(x);
   }
-  // scores of the keys 16 r .. 16 r + 15 (lane (j, g): keys 4 g .. + 3) with block c's queries
-  __device__ __forceinline__ f32x4 scores(int c, int r, int g) const {
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    auto operand = [&](const int* w) {
-      if constexpr (D == 128) return i32x8{w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
-      else return r == 0 ? i32x8{w[0], w[1], w[2], w[3], 0, 0, 0, 0} : i32x8{0, 0, 0, 0, w[0], w[1], w[2], w[3]};
-    };
-    const int i = D == 128 ? r : 0, byte = k_byte(i, g);
-    s = mfma_k16(kr[i], byte, operand(hi[c]), scales[c], false, s);
-    return mfma_k16(kr[i], byte, operand(lo[c]), scales[c], true, s);
+  // scores of the keys 16 r .. 16 r + 15 (lane (j, g): keys 4 g .. + 3) with all queries
+  __device__ __forceinline__ void scores(int r, int g, f32x4 (*s)[2]) const {
+    u32x4 k = kr[D == 128 ? r : 0];
+    int byte = k_byte(D == 128 ? r : 0, g);
+    if (D == 64 && r == 1) {  // the last two lane groups' keys to the first two, which have the queries
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k[i] = __builtin_amdgcn_permlane32_swap(k[i], k[i], false, false)[1];
+      byte = (int)__builtin_amdgcn_permlane32_swap((unsigned)byte, (unsigned)byte, false, false)[1];
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      f32x4 x = {0.f, 0.f, 0.f, 0.f};
+      x = mfma_k16<0>(k, byte, q[c], x);
+      x = mfma_k16<1>(k, byte, q[c], x);
+      x = mfma_k16<2>(k, byte, q[c], x);
+      s[c][r] = mfma_k16<3>(k, byte, q[c], x);
+    }
   }
 };
 
@@ -380,9 +412,7 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
       const unsigned odd_keys = w.clear_odd_keys(g);
       f32x4 s[NC][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) s[c][r] = w.scores(c, r, g);
+      for (int r = 0; r < 2; ++r) w.scores(r, g, s);
       if (D == 64 && odd_keys) {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
@@ -517,16 +547,6 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
 template <int D>
 __device__ __forceinline__ unsigned k4_unit(int r, int u) {
   return D == 128 ? (unsigned)(r * 64 + ((u ^ ((r >> 1) & 3)) << 4)) : (unsigned)(r * 32 + (u << 4));
-}
-
-__device__ __forceinline__ f32x16 mfma_k32(const u32x4& k, int k_bytes, bool odd_step, const i32x8& q, int q_bytes,
-                                           bool low, const f32x16& c) {
-  const i32x8 a = {(int)k[0], (int)k[1], (int)k[2], (int)k[3], 0, 0, 0, 0};
-  if (odd_step)
-    return low ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, q, c, 4, 0, 2, k_bytes, 1, q_bytes)
-               : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, q, c, 4, 0, 2, k_bytes, 0, q_bytes);
-  return low ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, q, c, 4, 0, 0, k_bytes, 1, q_bytes)
-             : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, q, c, 4, 0, 0, k_bytes, 0, q_bytes);
 }
 
 // Byte offsets of a key's rows; bit 0 of k: there is no such key (offsets 0).
@@ -757,29 +777,16 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
     const int wt0 = 32 * wave_rows / a.group;
     const int wt1 = (32 * wave_rows + 31) / a.group < nt ? (32 * wave_rows + 31) / a.group : nt - 1;
     const bool wave_live = wt0 < nt;
-    // the lane's dims of step d: 64 d + 16 hf .. + 15 and 64 d + 32 + 16 hf .. + 15
-    i32x8 q_hi[kSteps], q_lo[kSteps];
-    int q_scales;
+    Query qs[kSteps];  // of step d: the lane's dims 64 d + 32 hf .. + 31
     {
-      const uint16_t* qp = a.q + (int64_t)(t0 + t) * a.q_token + (int64_t)hh * a.q_head + 16 * hf;
-      u32x4 x4[2 * kSteps][2];
-      unsigned top = 0;
+      const uint16_t* qp = a.q + (int64_t)(t0 + t) * a.q_token + (int64_t)hh * a.q_head + 32 * hf;
 #pragma unroll
-      for (int s = 0; s < 2 * kSteps; ++s)
+      for (int d = 0; d < kSteps; ++d) {
+        u32x4 x4[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          x4[s][i] = live ? *reinterpret_cast<const u32x4*>(qp + 32 * s + 8 * i) : u32x4{0, 0, 0, 0};
-          top = max(top, top_bits(x4[s][i]));
-        }
-      top = __float_as_uint(half_max(__uint_as_float(top << 16))) >> 16;
-      q_scales = (int)query_scales(top);
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        int hi[8], lo[8];
-        split_query(x4[2 * s], (unsigned)q_scales, hi, lo);
-        split_query(x4[2 * s + 1], (unsigned)q_scales, hi + 4, lo + 4);
-        q_hi[s] = i32x8{hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]};
-        q_lo[s] = i32x8{lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]};
+        for (int i = 0; i < 4; ++i)
+          x4[i] = live ? *reinterpret_cast<const u32x4*>(qp + 64 * d + 8 * i) : u32x4{0, 0, 0, 0};
+        qs[d] = split_query(x4);
       }
     }
     f32x16 o[kOut];
@@ -887,13 +894,19 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
           for (int d = 0; d < kSteps; ++d)
             kf[i][d] = *reinterpret_cast<const u32x4*>(smem + buf * kTileK + k4_unit<D>(32 * i + q, 2 * d + hf));
         }
-#pragma unroll
-        for (int d = 0; d < kSteps; ++d) {
-          sc[0] = mfma_k32(kf[0][d], kb[0], d == 1, q_hi[d], q_scales, false, sc[0]);
-          sc[1] = mfma_k32(kf[1][d], kb[1], d == 1, q_hi[d], q_scales, false, sc[1]);
-          sc[0] = mfma_k32(kf[0][d], kb[0], d == 1, q_lo[d], q_scales, true, sc[0]);
-          sc[1] = mfma_k32(kf[1][d], kb[1], d == 1, q_lo[d], q_scales, true, sc[1]);
-        }
+        auto products = [&](auto byte) {
+          constexpr int d = byte / 2;
+          sc[0] = mfma_k32<0, byte>(kf[0][d], kb[0], qs[d], sc[0]);
+          sc[1] = mfma_k32<0, byte>(kf[1][d], kb[1], qs[d], sc[1]);
+          sc[0] = mfma_k32<1, byte>(kf[0][d], kb[0], qs[d], sc[0]);
+          sc[1] = mfma_k32<1, byte>(kf[1][d], kb[1], qs[d], sc[1]);
+          sc[0] = mfma_k32<2, byte>(kf[0][d], kb[0], qs[d], sc[0]);
+          sc[1] = mfma_k32<2, byte>(kf[1][d], kb[1], qs[d], sc[1]);
+          sc[0] = mfma_k32<3, byte>(kf[0][d], kb[0], qs[d], sc[0]);
+          sc[1] = mfma_k32<3, byte>(kf[1][d], kb[1], qs[d], sc[1]);
+        };
+        products(std::integral_constant<int, 0>{});
+        if constexpr (kSteps == 2) products(std::integral_constant<int, 2>{});
       }
       // ---- the next step's tiles; these buffers were last read before the barrier that began
       // this step
