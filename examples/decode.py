@@ -1,18 +1,18 @@
 """A small multi-tenant decoder, from prompts to sampled tokens, on the library's operators.
 
-    python examples/decode.py
+    python examples/decode.py [bf16|fp8|fp4]
 
 Every linear of the model has one base matrix and a 1-bit delta per variant.  Requests of one
 variant share that variant's system prompt, so its keys and values are written once (``prefill``)
 and every request's own tokens follow in pages of its own.  One step of ``decode`` is:
 
 * the batch, grouped by variant (``plan_segments``), through the grouped fused linears;
-* the new keys and values into the paged cache;
+* ``cache_write`` puts the new keys and values into the paged cache, in bf16, e4m3 or 4 bits;
 * ``attend_shared`` in the layers that see everything (each prompt is read once per variant, not
   once per request), ``attend_window`` in the layers with a sliding window and a few first tokens;
 * ``sample`` on the logits.
 
-torch does what is left: embedding, norms, rotary positions, the cache writes.  Weights are random.
+torch does what is left: embedding, norms, rotary positions.  Weights are random.
 """
 from __future__ import annotations
 
@@ -41,6 +41,7 @@ class Config:
     sinks: int = 4
     variants: int = 3
     page: int = 16
+    kv: str = "bf16"         # what the cache holds: bf16, fp8 (e4m3), fp4 (e2m1 and a scale per 32 values)
 
     def linears(self):
         q, kv = self.heads * self.head_dim, self.kv_heads * self.head_dim
@@ -88,6 +89,26 @@ def rotary(x, pos):
     return torch.cat([a * c - b * s, a * s + b * c], dim=-1).bfloat16()
 
 
+class Cache:
+    """One layer's pages, [pages, page, kv_heads, ..], stored head by head; ``scales``: what the cache's
+    calls take beside them.  e4m3 gets 16 times the values, so up to 28: keys are norms of a few, and rotated."""
+
+    def __init__(self, cfg: Config, pages: int, device):
+        def make(width, dtype):
+            shape = (pages, cfg.kv_heads, cfg.page, width)
+            return torch.zeros(shape, dtype=dtype, device=device).transpose(1, 2)
+
+        width, dtype = {"bf16": (cfg.head_dim, torch.bfloat16), "fp8": (cfg.head_dim, torch.float8_e4m3fn),
+                        "fp4": (cfg.head_dim // 2, torch.uint8)}[cfg.kv]
+        self.k, self.v = make(width, dtype), make(width, dtype)
+        self.scales = {}
+        if cfg.kv == "fp8":
+            self.scales = {"k_scale": 1 / 16, "v_scale": 1 / 16}
+        elif cfg.kv == "fp4":
+            self.scales = {"k_block_scales": make(cfg.head_dim // 32, torch.uint8),
+                           "v_block_scales": make(cfg.head_dim // 32, torch.uint8)}
+
+
 class Engine:
     """A batch of requests of several variants and the pages that hold their keys and values."""
 
@@ -118,29 +139,24 @@ class Engine:
         self.prefix, self.table, self.joined, self.first = put(prefix), put(table), put(joined), put(first)
         self.prefix_lens = put(np.array([len(p) for p in self.prompts], np.int32))
         self.lens = torch.zeros(batch, dtype=torch.int32, device=device)
-        shape = (sum(pages_of) + batch * own, cfg.kv_heads, cfg.page, cfg.head_dim)
-        # [pages, page, kv_heads, dim], stored head by head
-        self.cache = [tuple(torch.zeros(shape, dtype=torch.bfloat16, device=device).transpose(1, 2)
-                            for _ in "kv") for _ in range(cfg.layers)]
+        self.cache = [Cache(cfg, sum(pages_of) + batch * own, device) for _ in range(cfg.layers)]
 
     def linears(self, layer, names, x, offs):
         todo = [layer[n] for n in names]
         ys = [torch.empty(x.shape[0], w.shape[0], dtype=torch.bfloat16, device=x.device) for w, _ in todo]
         return bd.matmul_grouped([(x, w, y, vs) for (w, vs), y in zip(todo, ys)], offs, self.segv)
 
-    def forward(self, tokens, pos, table, rows, offs, attend):
-        """Hidden states of ``tokens`` at ``pos``; token i's keys go through table[rows[i]], and
-        attend(layer number, q, k pages, v pages) sees them there."""
+    def forward(self, tokens, pos, table, lens, q_offsets, offs, attend):
+        """Hidden states of ``tokens`` at ``pos``, the last tokens of the sequences that ``table``, ``lens``
+        and ``q_offsets`` describe; their keys go there, and attend(layer number, q, cache) sees them."""
         cfg = self.cfg
-        page = table[rows, pos // cfg.page].long()
         x = self.model.embed[tokens.long()]
         for i, layer in enumerate(self.model.layers):
             q, k, v = (y.unflatten(1, (-1, cfg.head_dim))
                        for y in self.linears(layer, ("q", "k", "v"), norm(x), offs))
-            kc, vc = self.cache[i]
-            kc[page, pos % cfg.page] = rotary(k, pos)
-            vc[page, pos % cfg.page] = v
-            a = attend(i, rotary(q, pos), kc, vc)
+            c = self.cache[i]
+            bd.cache_write(rotary(k, pos), v, c.k, c.v, table, lens, q_offsets, **c.scales)
+            a = attend(i, rotary(q, pos), c)
             x = x + self.linears(layer, ("o",), a.flatten(1), offs)[0]
             gate, up = self.linears(layer, ("gate", "up"), norm(x), offs)
             x = x + self.linears(layer, ("down",), torch.nn.functional.silu(gate) * up, offs)[0]
@@ -151,18 +167,17 @@ class Engine:
         cfg = self.cfg
         n = [len(p) for p in self.prompts]
         offs = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
-        rows = torch.repeat_interleave(torch.arange(len(n)), torch.tensor(n)).to(self.device)
         pos = torch.cat([torch.arange(m) for m in n]).to(self.device)
         q_offsets = torch.from_numpy(offs).to(self.device)
         everything = self.prefix.shape[1] * cfg.page
 
-        def attend(i, q, k, v):
-            return bd.attend_window(q, k, v, self.prefix, self.prefix_lens,
+        def attend(i, q, c):
+            return bd.attend_window(q, c.k, c.v, self.prefix, self.prefix_lens,
                                     cfg.window if i % 2 else everything, cfg.sinks,
-                                    q_offsets=q_offsets, max_q_len=max(n))
+                                    q_offsets=q_offsets, max_q_len=max(n), **c.scales)
 
         tokens = torch.from_numpy(np.concatenate(self.prompts)).to(self.device)
-        return self.forward(tokens, pos, self.prefix, rows, offs, attend)
+        return self.forward(tokens, pos, self.prefix, self.prefix_lens, q_offsets, offs, attend)
 
     def decode(self, tokens):
         """float32 logits after one more token per request (in the order of ``perm``)."""
@@ -171,21 +186,20 @@ class Engine:
         self.lens += 1
         seen = self.first + self.lens
 
-        def attend(i, q, k, v):
+        def attend(i, q, c):
             if i % 2:
-                return bd.attend_window(q, k, v, self.joined, seen, cfg.window, cfg.sinks)
-            return bd.attend_shared(q, k, v, self.table, self.lens, self.prefix, self.prefix_lens,
-                                    self.offs)
+                return bd.attend_window(q, c.k, c.v, self.joined, seen, cfg.window, cfg.sinks, **c.scales)
+            return bd.attend_shared(q, c.k, c.v, self.table, self.lens, self.prefix, self.prefix_lens,
+                                    self.offs, **c.scales)
 
-        rows = torch.arange(len(self.perm), device=self.device)
-        x = self.forward(tokens, pos, self.joined, rows, self.offs, attend)
+        x = self.forward(tokens, pos, self.joined, seen, None, self.offs, attend)
         w, variants = self.model.head
         return bd.matmul(x, w, variants, self.offs, self.segv, out_dtype="f32")
 
 
 def main():
     device = torch.device("cuda:0")
-    cfg = Config()
+    cfg = Config(kv=sys.argv[1] if len(sys.argv) > 1 else "bf16")
     rng = np.random.default_rng(7)
     model = Model(cfg, device)
     variant = rng.integers(0, cfg.variants, 20)

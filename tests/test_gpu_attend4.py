@@ -254,6 +254,52 @@ def test_pages_that_are_no_pages(q_lens, lens, dim):
 
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("q_lens,lens", KINDS)
+def test_absent_keys_read_nothing_of_page_0(q_lens, lens, dim):
+    """Page 0, which belongs to nobody, holds NaN; keys without a page and behind the lists are absent."""
+    rng = np.random.default_rng(25)
+    table, c, q, qf, offs = _setup(rng, q_lens, lens, dim=dim, extra=60)
+    free = list(set(range(c.kf.shape[0])) - set(table[table >= 0].tolist()))[0]
+    table = np.where(table == 0, free, table)
+    table[0, 2], table[1, 1] = -1, 10 ** 6
+    for x in c.byte:
+        x[0] = 255
+    for x in c.codes:
+        x[free] = x[1]
+    c.byte[0][free], c.byte[1][free] = c.byte[0][1], c.byte[1][1]
+    c.upload()
+    out, lse = bd.attend_window(q, c.k, c.v, i32(table), i32(lens), 4000, 2, q_offsets=offs,
+                                max_q_len=max(q_lens), return_lse=True, **c.kw())
+    check(out, lse, window_ref(qf, c, 16, table, lens, q_lens, 4000, 2, (1, 1), dim ** -0.5))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_lens,lens", KINDS)
+def test_keys_and_values_laid_out_differently(q_lens, lens, dim):
+    """Keys head by head, values token by token, in pages and heads of an odd number."""
+    rng = np.random.default_rng(26)
+    table, c, q, qf, offs = _setup(rng, q_lens, lens, heads=9, hk=3, dim=dim, page=7)
+    t = lambda x: x.transpose(1, 2).contiguous().transpose(1, 2)  # noqa: E731
+    u = lambda x: x.contiguous()                                 # noqa: E731
+    out, lse = bd.attend_window(q, t(c.k), u(c.v), i32(table), i32(lens), 1500, 2, q_offsets=offs,
+                                max_q_len=max(q_lens), return_lse=True, k_block_scales=t(c.kb),
+                                v_block_scales=u(c.vb))
+    check(out, lse, window_ref(qf, c, 7, table, lens, q_lens, 1500, 2, (1, 1), dim ** -0.5))
+
+
+@pytest.mark.parametrize("heads,hk,dim", [(40, 1, 128), (64, 1, 64), (96, 2, 128)])
+def test_single_tokens_of_many_heads(heads, hk, dim):
+    """More than 32 query heads a kv head: single tokens by the tile kernel, prefixes by both."""
+    rng = np.random.default_rng(27)
+    lens = [1400, 0, 33]
+    table, c, q, qf, _ = _setup(rng, [1, 1, 1], lens, heads, hk, dim)
+    out, lse = bd.attend_window(q, c.k, c.v, i32(table), i32(lens), 1000, 4, return_lse=True, **c.kw())
+    check(out, lse, window_ref(qf, c, 16, table, lens, [1, 1, 1], 1000, 4, (1, 1), dim ** -0.5))
+    out, lse = bd.attend_shared(q, c.k, c.v, i32(table), i32(lens), None, None, [0, 2, 3], return_lse=True, **c.kw())
+    check(out, lse, window_ref(qf, c, 16, table, lens, [1, 1, 1], 10 ** 6, 0, (1, 1), dim ** -0.5))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_lens,lens", KINDS)
 @pytest.mark.parametrize("window", [37, 4000])
 def test_what_no_query_sees_is_not_used(q_lens, lens, window, dim):
     """Blocks of NaN before the windows, beyond the lengths, in the pages of nobody."""
@@ -416,6 +462,30 @@ def test_graphs_share_a_workspace():
             eager = call(i, torch.empty_like(q))
             torch.cuda.synchronize()
             assert torch.equal(outs[i], eager)
+
+
+def test_graph_of_a_split_chunk():
+    """Parts of a chunk's keys and what joins them, captured, replayed with other queries and lengths."""
+    rng = np.random.default_rng(31)
+    table, c, q, qf, offs = _setup(rng, [70, 30], [2500, 900])
+    t, l = i32(table), i32([2500, 900])
+    out = torch.empty_like(q)
+
+    def call(to):
+        return bd.attend_window(q, c.k, c.v, t, l, 1900, 4, q_offsets=offs, max_q_len=70, out=to, **c.kw())
+
+    call(out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(out)
+    for turn in range(4):
+        q.copy_(torch.randn_like(q))
+        l.copy_(i32([2500 - 300 * turn, 70 + turn]))
+        g.replay()
+        eager = call(torch.empty_like(q))
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
 
 
 def test_repeated_calls_agree_and_other_streams():
