@@ -5,7 +5,11 @@
 // block's power of two):
 //   s_j = c * (q . k_j),  c = scale * k_scale * log2(e)
 //   m = max_j s_j,  l = sum_j 2^(s_j - m),  o = v_scale / l * sum_j 2^(s_j - m) v_j
-// in one pass over the keys, with a running maximum and sum.
+// in one pass over the keys: the running maximum m and sum l are kept in fp32 per row, and the fp32 output
+// sums are rescaled when m grows.  As from the wider caches, scores are computed transposed, S^T = K Q^T, so
+// that each lane has scores of one query row and the weights are the B operand of O^T = V^T P^T as they are.
+// K goes into the scaled matrix instruction in 4 bits (no widening, a quarter of the LDS bytes), V is
+// widened to bf16, exactly: its blocks lie along the dims, not along the keys that the second product sums.
 #include <type_traits>
 
 #include "attend_device.h"
@@ -117,7 +121,19 @@ __device__ __forceinline__ float odd_block(const unsigned char* blocks, int d) {
 // list, each of a workgroup's 4 waves 32 keys of a 128-key step on its own.  A lane's 16 bytes of a K row
 // are one block of 32 dims, as the scaled matrix instruction wants its operand (dim 64: one row in the
 // first two lane groups, another, 16 keys on, in the last two, whose queries are zeros; for the others' turn
-// the halves change places).  V rows are widened to bf16 into 8 KiB of the wave's LDS, and read transposed.
+// the halves change places).  V rows are widened to bf16 into 8 KiB of the wave's LDS, and read transposed,
+// four 16-row tiles ahead of the product.  The work split, and what joins its pieces, are those of the wider
+// caches' row kernel.
+//
+// Bound by reading the cache: 64 sequences x 8 kv heads of up to 8208 keys, dim 128, 480 MB in 102 us, 4.7
+// TB/s (a large copy's 5.2); one sequence's 131072 keys, 143 MB in 35 us, 4.1 TB/s, 4 of them to begin.
+// Vector instructions are busy 50% of the time, matrix instructions 13%, the LDS 37% (bank conflicts 17%).
+// Where the keys come from the caches (64 sequences in 14 segments, 100 MB of readings, 8 MB of them from
+// memory: 33 us) it is the chain of a step within a wave.  Tried and no faster (64 sequences): rows two
+// steps ahead in two sets of registers, queries in LDS, 107 us; two workgroups a compute unit instead of
+// three, 106 us, with rows one or two steps ahead; keys' lists in vector registers and byte loads of the
+// scales, which the compiler widens at once and so waits for, 105 us.  At dim 128 some variants spill: 9
+// registers for several tokens, 19 and 44 with two column blocks, 40 with four.
 // ---------------------------------------------------------------------------------------------
 // The aligned word with the scale bytes of the row at byte o of the scale bytes (dim 64: a row has two, at
 // bits 0 or 16; the word's other half is a neighbour's, or behind the array's end in the same word, and is
@@ -541,7 +557,18 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
 // ---------------------------------------------------------------------------------------------
 // Tile kernel: 256 query rows (tokens x the heads of one kv head) against a key list in 64-key steps.  8
 // waves of 32 rows; K codes and scale bytes in LDS as they are, V widened to bf16 on the way there, each a
-// step ahead in two buffers.
+// step ahead.  Prefixes: work cut into equal runs, and where a segment's rows fill at most half the waves,
+// the others take a second key tile of the same step (256 sequences in 14 segments 118 -> 106 us).  Windows:
+// tile_work below.
+//
+// Bound by matrix and vector instructions, which take turns on a SIMD rather than overlap: of a step's about
+// 5400 cycles the two waves of a SIMD have 2000 of products (16 scaled ones for the scores, 16 of bf16 for the
+// values, a wave) and 2300 of weights (32 exponentials a lane, at a quarter of the rate, are half of that).
+// Dim 128, 64 heads on 8: 4 chunks of up to 2048 tokens behind 4096, window 4096, 689 GFLOP in 720 to 800 us
+// by the machine, 860 to 960 TFLOP/s (a large matrix product reaches 1192).  Tried and slower or no faster (that
+// call, 761 us at the time): the late half of the waves a phase behind, so that products meet weights, 861
+// us; a barrier that leaves the next rows' loads on their way, no change; scores by two e4m3 products or
+// three of e2m3 instead of four, within 2%.
 // ---------------------------------------------------------------------------------------------
 // Byte offset of 16-byte unit u (32 dims) of row r in a K tile: a wave's reads take one unit of 32 rows
 template <int D>

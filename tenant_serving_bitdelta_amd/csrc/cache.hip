@@ -2,16 +2,20 @@
 //
 // Mathematics, per value x of a row, y = x / scale in fp32:
 //   bf16  y rounded;   e4m3  min(max(y, -448), 448) rounded;
-//   4 bits, per 32 consecutive values: 2^e = the smallest power of two with max |y| <= 7 * 2^e (then
-//   every |y| / 2^e is at most half a step of {0, .5, 1, 1.5, 2, 3, 4, 6} away from it; 6.5 or more
-//   would be off by more with the usual choice, the largest power of two below max |y| / 4), code = the
-//   nearest one, ties to even, by the conversion instruction.
+//   4 bits, per 32 consecutive values: 2^e = the smallest power of two with max |y| <= 7 * 2^e, code = y /
+//   2^e rounded to the nearest of {0, .5, 1, 1.5, 2, 3, 4, 6}, ties to the even code, by the conversion
+//   instruction.  No value is then off by more than half a step of that grid (with 2^e the largest power of
+//   two below max |y| / 4, as is common, values near 8 would become 6).
 // The quotient is a product where 1 / scale is exact, else a correctly rounded division.
 //
-// Bound by memory: 4 bytes of bf16 and 2 * 17/32 (4 bits) to 4 stored bytes per pair of a key and a
-// value.  A thread takes 8 values (16 bytes of bf16) of one row at a time, so that a wave's loads and
-// stores are whole lines, and 4 lanes hold a block of 32 (its largest value by two lane moves); each of
-// a workgroup's tokens is looked up once, by one thread.
+// Bound by memory where tokens are many: 4 bytes of bf16 and 2 * 17/32 (4 bits) to 4 stored bytes per pair
+// of a key and a value.  A thread takes 8 values (16 bytes of bf16) of one row at a time, so that a wave's
+// loads and stores are whole lines, and 4 lanes hold a block of 32 (its largest value by two lane moves);
+// each of a workgroup's tokens is looked up once, by one thread, while the rows to write are on their way.
+// Measured, dim 128: 14 prompts of up to 8192 tokens, 8 heads, read from 4 bits, 363 MB in 58 us, 6.2 TB/s;
+// 4.6 thousand tokens of 8 heads written in 4 bits, 24 MB in 10.7 us, and read back in 7.8; 7 thousand of 4
+// heads written in e4m3, 22 MB in 9.2 us; four single tokens 3.5 us.  Of the short calls' times 3 us are the
+// launch and the chain offsets -> length -> table -> place; a workgroup per token took 15 us for the 10.7.
 #include "bd_internal.h"
 #include "cache.h"
 
