@@ -112,7 +112,7 @@ def check(out, lse, ref):
         assert np.array_equal(np.isnan(z[t]), np.isnan(l)), (t, z[t], l)
         live = ~dead & ~np.isnan(l)
         off = np.abs(z[t][live] - l[live])
-    assert np.all(off <= err[live] + 2e-6 + 1e-6 * np.abs(l[live])), (t, z[t], l, err)
+        assert np.all(off <= err[live] + 2e-6 + 1e-6 * np.abs(l[live])), (t, z[t], l, err)
 
 
 def shared_ref(q, c, page, table, lens, ptable, plens, offs, scales, scale):
@@ -531,3 +531,17 @@ def test_refusals_of_the_binding():
     k = torch.zeros((4, 16, 2, 128), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):
         bd.attend_window(q, k, k, *args[3:], **c.kw())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_workers_pass_over_empty_sequences(dim):
+    """(a table so wide that units are split; a workgroup's run then goes over several short units)"""
+    rng = np.random.default_rng(dim)
+    lens = [int(x) for x in rng.integers(1, 700, 300)]
+    for i in (0, 1, 17, 18, 19, 20, 150, 297, 298, 299, *rng.integers(0, 300, 80)):
+        lens[i] = 0
+    lens[64] = 4000
+    table, c, q, qf, _ = _setup(rng, [1] * 300, lens, 4, 2, dim, extra=60)
+    out, lse = bd.attend_window(q, c.k, c.v, i32(table), i32(lens), 5000, return_lse=True, **c.kw())
+    assert bd.attend_window_workspace_bytes(c.k, 4, i32(table), 300, 1, 5000, 0) > 0
+    check(out, lse, window_ref(qf, c, 16, table, lens, [1] * 300, 5000, 0, (1.0, 1.0), dim ** -0.5))
