@@ -767,9 +767,11 @@ def _kv_cache(k_pages, v_pages, k_scale, v_scale, k_block_scales=None, v_block_s
 def _cache_sizes(k_pages):
     """The same for a query of workspace sizes: no scales are looked at."""
     import torch
-    if k_pages.dtype is not torch.uint8:
+    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda or k_pages.dtype is not torch.uint8:
         return _kv_cache(k_pages, k_pages, 1.0, 1.0)
     shape, ks = k_pages.shape, k_pages.stride()
+    if len(shape) != 4:
+        raise ValueError("k_pages must be [pages, page_size, kv_heads, head_dim / 2]")
     p = k_pages.data_ptr()
     return _KvCache(p, p, 2, shape[0], shape[1], shape[2], 2 * shape[3], *[2 * x for x in ks[:3]],
                     *[2 * x for x in ks[:3]], 1.0, 1.0, p, p)
@@ -845,11 +847,11 @@ def attend_shared(q, k_pages, v_pages, table, lens, prefix_table, prefix_lens, s
 
     ``q``: bf16 [batch, heads, head_dim]; ``k_pages`` / ``v_pages``: [pages, page_size, kv_heads,
     head_dim] bf16 or float8_e4m3fn (each stored value times ``k_scale`` / ``v_scale``), any
-    strides but contiguous rows, or 4-bit pages with their block scales (see cache_write); ``table`` int32 [batch, n], ``lens`` int32 [batch],
-    ``prefix_table`` int32 [segments, m] and ``prefix_lens`` int32 [segments] (both None: no
-    prefixes), on the device.  Returns bf16 ``out`` like q, and with ``return_lse`` (or ``lse``
-    given) also the natural log of each row's softmax sum, float32 [batch, heads].  A sequence
-    with no keys gives zeros and -inf."""
+    strides but contiguous rows, or 4-bit pages with their block scales (see cache_write); ``table``
+    int32 [batch, n], ``lens`` int32 [batch], ``prefix_table`` int32 [segments, m] and
+    ``prefix_lens`` int32 [segments] (both None: no prefixes), on the device.  Returns bf16 ``out``
+    like q, and with ``return_lse`` (or ``lse`` given) also the natural log of each row's softmax
+    sum, float32 [batch, heads].  A sequence with no keys gives zeros and -inf."""
     offs, offs_p = _host_i32(seg_offsets)
     cache = _kv_cache(k_pages, v_pages, k_scale, v_scale, k_block_scales, v_block_scales)
     rows, out, lse = _attend_rows(q, cache, out, lse, return_lse, scale, stream)

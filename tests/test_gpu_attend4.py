@@ -545,3 +545,14 @@ def test_workers_pass_over_empty_sequences(dim):
     out, lse = bd.attend_window(q, c.k, c.v, i32(table), i32(lens), 5000, return_lse=True, **c.kw())
     assert bd.attend_window_workspace_bytes(c.k, 4, i32(table), 300, 1, 5000, 0) > 0
     check(out, lse, window_ref(qf, c, 16, table, lens, [1] * 300, 5000, 0, (1.0, 1.0), dim ** -0.5))
+
+
+def test_refusals_of_the_workspace_query():
+    pages = torch.zeros((4, 16, 2, 64), dtype=torch.uint8, device="cuda")
+    table = i32([[0, 1], [2, 3]])
+    assert bd.attend_window_workspace_bytes(pages, 8, table, 2, 1, 50, 0) >= 0
+    for bad, error in ((pages[0], ValueError), (pages.cpu(), TypeError), (None, TypeError)):
+        with pytest.raises(error):
+            bd.attend_window_workspace_bytes(bad, 8, table, 2, 1, 50, 0)
+        with pytest.raises(error):
+            bd.attend_shared_workspace_bytes(bad, 8, table, None, [0, 2])
