@@ -128,7 +128,7 @@ __device__ __forceinline__ float odd_block(const unsigned char* blocks, int d) {
 // Bound by reading the cache: 64 sequences x 8 kv heads of up to 8208 keys, dim 128, 480 MB in 102 us, 4.7
 // TB/s (a large copy's 5.2); one sequence's 131072 keys, 143 MB in 35 us, 4.1 TB/s, 4 of them to begin.
 // Vector instructions are busy 50% of the time, matrix instructions 13%, the LDS 37% (bank conflicts 17%).
-// Where the keys come from the caches (64 sequences in 14 segments, 100 MB of readings, 8 MB of them from
+// Where the keys come from the caches (64 sequences in 14 segments, 100 MB of readings, 43 MB of them from
 // memory: 33 us) it is the chain of a step within a wave.  Tried and no faster (64 sequences): rows two
 // steps ahead in two sets of registers, queries in LDS, 107 us; two workgroups a compute unit instead of
 // three, 106 us, with rows one or two steps ahead; keys' lists in vector registers and byte loads of the
