@@ -286,11 +286,17 @@ __device__ __forceinline__ void join_waves(const AttendArgs& a, unsigned char* v
   const int lane = tid & 63, j = lane & 15, g = lane >> 4;
   lc = half_sum(row_sum(lc));
   __syncthreads();  // the V tiles, or the last block's sums, are no longer read
-  float* const ow = reinterpret_cast<float*>(vlds + wave * kWaveLds);  // [16 columns][D]
+  // [16 columns][D], dims by fours, four n of column j at n ^ j: a column's length is a multiple of all banks
+  auto fours = [](int col, int n) { return col * D + 4 * (n ^ col); };
+  float* const ow = reinterpret_cast<float*>(vlds + wave * kWaveLds);
+  const bool live = 16 * c + j < rows;
+  if (live) {
+    int col = j;  // (opaque: the addresses are worked out here, not before the steps, which lack the registers)
+    asm volatile("" : "+v"(col));
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i)
-    *reinterpret_cast<f32x4*>(ow + j * D + 16 * i + 4 * g) = oc[i];
-  if (g == 0) {
+    for (int i = 0; i < D / 16; ++i) *reinterpret_cast<f32x4*>(ow + fours(col, 4 * i + g)) = oc[i];
+  }
+  if (live && g == 0) {
     ml[wave][j][0] = mc;
     ml[wave][j][1] = lc;
   }
@@ -298,7 +304,9 @@ __device__ __forceinline__ void join_waves(const AttendArgs& a, unsigned char* v
   constexpr int kQuads = 16 * D / 4 / 256;  // f32x4 per thread
 #pragma unroll
   for (int e = 0; e < kQuads; ++e) {
-    const int idx = tid + 256 * e, col = idx / (D / 4), d4 = idx - col * (D / 4);
+    int idx = tid + 256 * e;
+    asm volatile("" : "+v"(idx));
+    const int col = idx / (D / 4), d4 = idx - col * (D / 4);
     const int row = 16 * c + col;
     if (row < rows) {
       float mx = kNegInf;
@@ -312,7 +320,7 @@ __device__ __forceinline__ void join_waves(const AttendArgs& a, unsigned char* v
         const float f = exp2_fast(ml[v][col][0] - mb);
         lt += f * ml[v][col][1];
         ot += f * *reinterpret_cast<const f32x4*>(
-                      reinterpret_cast<const float*>(vlds + v * kWaveLds) + col * D + 4 * d4);
+                      reinterpret_cast<const float*>(vlds + v * kWaveLds) + fours(col, d4));
       }
       if (a.direct) {
         const int t = row / a.group, hh = h * a.group + row - t * a.group;
