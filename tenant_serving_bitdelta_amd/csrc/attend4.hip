@@ -125,15 +125,16 @@ __device__ __forceinline__ float odd_block(const unsigned char* blocks, int d) {
 // four 16-row tiles ahead of the product.  The work split, and what joins its pieces, are those of the wider
 // caches' row kernel.
 //
-// Bound by reading the cache: 64 sequences x 8 kv heads of up to 8208 keys, dim 128, 480 MB in 102 us, 4.7
-// TB/s (a large copy's 5.2); one sequence's 131072 keys, 143 MB in 35 us, 4.1 TB/s, 4 of them to begin.
-// Vector instructions are busy 50% of the time, matrix instructions 13%, the LDS 37% (bank conflicts 17%).
+// Bound by reading the cache: 64 sequences x 8 kv heads of up to 8208 keys, dim 128, 480 MB in 100 us, 4.8
+// TB/s (a large copy's 5.2); one sequence's 131072 keys, 143 MB in 33.5 us, 4.3 TB/s, 4 us of them to begin.
+// Vector instructions are busy 50% of the time, matrix instructions 13%, the LDS 33% (bank conflicts 13%).
 // Where the keys come from the caches (64 sequences in 14 segments, 100 MB of readings, 43 MB of them from
-// memory: 33 us) it is the chain of a step within a wave.  Tried and no faster (64 sequences): rows two
-// steps ahead in two sets of registers, queries in LDS, 107 us; two workgroups a compute unit instead of
-// three, 106 us, with rows one or two steps ahead; keys' lists in vector registers and byte loads of the
-// scales, which the compiler widens at once and so waits for, 105 us.  At dim 128 some variants spill: 9
-// registers for several tokens, 19 and 44 with two column blocks, 40 with four.
+// memory: 31 us) it is the chain of a step within a wave.  Tried and no faster: rows two steps ahead in two
+// sets of registers, queries in LDS; two workgroups a compute unit instead of three, with rows one or two
+// steps ahead; keys' lists in vector registers and byte loads of the scales, which the compiler widens at
+// once and so waits for; a unit's first rows fetched during the last step of the unit before it; up to 8 rows
+// in two columns each, with two of the query's parts and one of a wave's two key tiles, which halves the
+// score products and the exponentials.  At dim 128 four column blocks spill 41 registers.
 // ---------------------------------------------------------------------------------------------
 // The aligned word with the scale bytes of the row at byte o of the scale bytes (dim 64: a row has two, at
 // bits 0 or 16; the word's other half is a neighbour's, or behind the array's end in the same word, and is
@@ -286,7 +287,8 @@ __device__ __forceinline__ void join_waves(const AttendArgs& a, unsigned char* v
   const int lane = tid & 63, j = lane & 15, g = lane >> 4;
   lc = half_sum(row_sum(lc));
   __syncthreads();  // the V tiles, or the last block's sums, are no longer read
-  // [16 columns][D], dims by fours, four n of column j at n ^ j: a column's length is a multiple of all banks
+  // [16 columns][D], dims by fours, four n of column j at n ^ j: a column's length is a multiple of all
+  // banks (256 sequences' own keys, in short units, 51 us instead of 58)
   auto fours = [](int col, int n) { return col * D + 4 * (n ^ col); };
   float* const ow = reinterpret_cast<float*>(vlds + wave * kWaveLds);
   const bool live = 16 * c + j < rows;
@@ -397,7 +399,7 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
         s_begin = (int)(x - x0 - (int64_t)h * s);
       } else {
         // the next unit: there is one, x being before the end of all (looked up anew, 256 sequences' own
-        // keys take 63 us instead of 59)
+        // keys took 63 us instead of 59)
         if (++h == a.kv_heads) {
           h = 0;
           do ++b;
