@@ -474,9 +474,11 @@ typedef enum {
 /*
  * BITDELTA_KV_FP4 (4.25 bits a value): two codes a byte, the lower four bits first, so that a row of
  * head_dim values is head_dim / 2 bytes; the 32 values of a block (values 32 i .. 32 i + 31 of a row)
- * have one scale byte b and stand for code * 2^(b - 127), b = 255 for 32 NaN.  The scale bytes of a
- * row, head_dim / 32 of them, lie in an array that is an image of the pages at a 16th of the size: those
- * of the row at k + o bytes at k_block_scales + o / 16, with the same page, token and head strides.
+ * have one scale byte b and stand for code * 2^(b - 127), b = 255 for 32 NaN.  (2^128 and more, which b =
+ * 253 and 254 can mean and bitdelta_cache_write never writes, is an infinity where it is read back or among
+ * v: its dim of the rows that see it comes out infinite or NaN.)  The scale bytes of a row, head_dim / 32 of
+ * them, lie in an array that is an image of the pages at a 16th of the size: those of the row at k + o bytes
+ * at k_block_scales + o / 16, with the same page, token and head strides.
  */
 typedef struct {
   const void* k; /* [dev] keys, 16-byte aligned (bitdelta_cache_write writes here)              */

@@ -111,9 +111,25 @@ __device__ __forceinline__ f32x16 mfma_k32(const u32x4& k, int k_bytes, const Qu
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 2, BYTE, k_bytes, SEL, q.scales);
 }
 
-// NaN if the block of dim d of a value row is NaN, else 0; blocks: the row's scale bytes
-__device__ __forceinline__ float odd_block(const unsigned char* blocks, int d) {
-  return blocks[d >> 5] == 255 ? __builtin_nanf("") : 0.f;
+// Values that are no finite number once they are bf16: all of a block of NaN (byte 255), and under the largest
+// scales 2^128 and more (4 and 6 * 2^126 of byte 253, 2 and more * 2^127 of byte 254), which the conversion
+// makes infinities.  Their codes' bits among those of v; byte: the block's scale.
+constexpr unsigned kOddByte = 253;  // the first scale with such values
+__device__ __forceinline__ unsigned odd_codes(unsigned v, unsigned byte) {
+  const unsigned ones = 0x11111111u;
+  const unsigned m = byte == 255 ? ones : (byte == 254 ? (v >> 2) & ones : (byte == 253 ? (v >> 2) & (v >> 1) & ones : 0));
+  return 15u * m;
+}
+// Values d .. d + 3 of a value row that are such, else 0; d is a multiple of 4, byte: their block's scale
+__device__ __forceinline__ f32x4 odd_values(const unsigned char* row, unsigned byte, int d) {
+  const unsigned codes = *reinterpret_cast<const uint16_t*>(row + (d >> 1)), odd = odd_codes(codes, byte);
+  f32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float x = byte == 255 ? __builtin_nanf("") : ((codes >> (4 * e + 3)) & 1u ? kNegInf : -kNegInf);
+    r[e] = (odd >> (4 * e)) & 15u ? x : 0.f;
+  }
+  return r;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -217,17 +233,19 @@ struct Row4Loop {
   __device__ __forceinline__ unsigned v_byte(int i, int g) const {
     return __builtin_amdgcn_ubfe(vb[i], vat[i] + 8 * block(g), 8);
   }
-  // keys with a block of NaN among their values, bit (key); those blocks become zeros
+  // keys with values that may be no finite numbers, bit (key); those that are none become zeros
   __device__ __forceinline__ unsigned clear_odd_blocks(int g) {
     unsigned odd = 0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const bool f = v_byte(i, g) == 255;
+      const unsigned byte = v_byte(i, g);
+      const bool f = byte >= kOddByte;
       uint64_t m = __ballot(f);
       if (m) {
         if (f) {
-          vr[i] = u32x4{0, 0, 0, 0};
-          vb[i] = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) vr[i][e] &= ~odd_codes(vr[i][e], byte);
+          if (byte == 255) vb[i] = 0;
         }
         m |= m >> 16;  // lane groups 0, 1 and 2, 3
         if constexpr (D == 128) odd |= (unsigned)((m | (m >> 32)) & 0xFFFFull) << (16 * i);
@@ -547,9 +565,14 @@ __global__ __launch_bounds__(256, NC == 1 ? 3 : (NC == 2 ? 2 : 1)) void attend4_
             const bool seen = sees(kl, w.pos[c], a.window, a.sinks, vp);
 #pragma unroll
             for (int i = 0; i < Loop::kTiles; ++i) {
-              const float odd_one = seen ? odd_block(blocks, 16 * i) : 0.f;
+              const unsigned byte = (unsigned)uniform(blocks[i >> 1]);
+              if (byte < kOddByte) continue;
+              int d = 16 * i + 4 * g;
+              // (opaque: else its part of the lane is kept in a register over the steps, one too many at dim 128)
+              if constexpr (NC == 1) asm volatile("" : "+v"(d));
+              const f32x4 x = odd_values(row, byte, d);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) w.o[c][i][e] = w.o[c][i][e] + odd_one;
+              for (int e = 0; e < 4; ++e) w.o[c][i][e] = w.o[c][i][e] + (seen ? x[e] : 0.f);
             }
           }
         }
@@ -673,9 +696,9 @@ struct Tile4Stage {
     vb = block_word<D>(a.cache.v_blocks, vo >> 4, &vat);
     kb = block_word<D>(a.cache.k_blocks, ko >> 4, &kat);
   }
-  // state: per key, bit 0: it exists; bit 1 (edge steps, where some row does not see some key): a block of
-  // its values is NaN.  Those are stored as zeros, since their product with a zero weight would be NaN, and
-  // added later for the rows that see them.
+  // state: per key, bit 0: it exists; bit 1 (edge steps, where some row does not see some key): some of its
+  // values may be no finite numbers.  Those that are none are stored as zeros, since their product with a zero
+  // weight would be NaN, and added later for the rows that see them.
   __device__ __forceinline__ void store(unsigned char* kt, unsigned* kbt, unsigned char* vt, int* state, bool edge,
                                         int tid) {
     const int r = tid >> 3, part = tid & 7;
@@ -686,10 +709,11 @@ struct Tile4Stage {
       byte = 0;
     }
     if (edge) {
-      const bool f = byte == 255;
+      const bool f = byte >= kOddByte;
       if (f) {
-        v = u32x2{0, 0};
-        byte = 0;
+        v[0] &= ~odd_codes(v[0], byte);
+        v[1] &= ~odd_codes(v[1], byte);
+        if (byte == 255) byte = 0;
       }
       const uint64_t m = __ballot(f) >> (tid & 56);  // of this key's eighths
       if (m & 0xFF) bits |= 2;
@@ -1039,9 +1063,14 @@ __global__ __launch_bounds__(512, 2) void attend4_tile_kernel(const AttendArgs a
             const bool seen = sees(kl, pq, a.window, a.sinks, vp);
 #pragma unroll
             for (int i = 0; i < kOut; ++i) {
-              const float odd_one = seen ? odd_block(blocks, 32 * i) : 0.f;
+              const unsigned byte = (unsigned)uniform(blocks[i]);
+              if (byte < kOddByte) continue;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[i][e] = o[i][e] + odd_one;
+              for (int e4 = 0; e4 < 4; ++e4) {
+                const f32x4 x = odd_values(row_v, byte, 32 * i + 8 * e4 + 4 * hf);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][4 * e4 + e] = o[i][4 * e4 + e] + (seen ? x[e] : 0.f);
+              }
             }
           }
         }
