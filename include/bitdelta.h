@@ -582,7 +582,8 @@ size_t bitdelta_attend_window_workspace_bytes(int64_t tokens, int32_t heads,
  * position lens[b] - 1 (the new tokens counted).  Without q_offsets each sequence has one row, its
  * last token (then tokens = batch).  The token at position p is in slot p % page_size of page
  * table[b][p / page_size].  It has no place where p is below 0 or beyond the table's row, or the entry
- * is no page.
+ * is no page.  (A length beyond the row's capacity is not cut here, as the attentions cut it, which then
+ * count a chunk's rows back from the capacity: the rows beyond have no place, and the others keep theirs.)
  *
  * Limits (else UNSUPPORTED): those of the cache above, BITDELTA_ATTEND_MAX_SEQS sequences, 2^16 kv heads,
  * 2^30 rows (tokens x kv heads).

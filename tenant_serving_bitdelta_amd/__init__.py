@@ -968,7 +968,8 @@ def cache_write(k, v, k_pages, v_pages, table, lens, q_offsets=None, k_scale=1.0
     """New keys and values into their pages, quantised on the way.  Which token a row is goes by the
     tables as attend_window has them: sequence b holds ``lens[b]`` tokens, its new ones among them as the
     last ones, which are rows q_offsets[b] .. q_offsets[b + 1] (int32 [batch + 1] on the device; None: one
-    token per sequence).  Rows whose token has no page in the table are not written.
+    token per sequence).  Rows whose token has no page in the table are not written (a length beyond the
+    table is not cut to what it holds, as the attentions cut it).
 
     ``k`` / ``v``: bf16 [tokens, kv_heads, head_dim], contiguous rows.  ``k_pages`` / ``v_pages``:
     [pages, page_size, kv_heads, head_dim] bf16 or float8_e4m3fn, which get each value divided by
@@ -976,7 +977,8 @@ def cache_write(k, v, k_pages, v_pages, table, lens, q_offsets=None, k_scale=1.0
     2] with ``k_block_scales`` / ``v_block_scales``, uint8 [..., head_dim / 32] of a 16th of the pages'
     strides: each 32 values of a row share a power of two, byte - 127, such that the largest is at most 7
     of them, and are rounded to 0, 0.5, 1, 1.5, 2, 3, 4 or 6 of them (lower four bits first).  Infinities
-    and NaN become NaN, in 4 bits with the 32 values around them.  Returns (k_pages, v_pages)."""
+    and NaN stay what they are in bf16; in float8 they become NaN, in 4 bits their whole block.  Returns
+    (k_pages, v_pages)."""
     cache = _kv_cache(k_pages, v_pages, k_scale, v_scale, k_block_scales, v_block_scales)
     device = k_pages.device
     rows = _kv_rows(k, v, cache, device)
