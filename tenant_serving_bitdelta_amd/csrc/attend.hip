@@ -932,9 +932,9 @@ __global__ __launch_bounds__(512, 2) void attend_tile_kernel(const AttendArgs a)
 // ---------------------------------------------------------------------------------------------
 // Combine: one wave per query row adds the row's partials of both kernels, in a fixed order: lanes of
 // 4 dims each, 64 / (dim / 4) pieces side by side, four loads each in flight.  Bound by finding the
-// pieces (divisions) and the loads' latency: 16384 rows of 3 to 5 pieces 18 us, 64 rows of 96 4 us.  Two
-// rows a wave took 15.6 us for the former, but 6.1 for the latter.  W = 4: a workgroup's waves take one
-// row's pieces between them.
+// pieces (divisions) and the loads' latency: 16384 rows of 3 to 5 pieces 16 to 18 us, 64 rows of 96 10.7, of 64
+// 8.3.  Two rows a wave were 13% faster for the first, but half as much again for few rows of many pieces.
+// W = 4: a workgroup's waves take one row's pieces between them: 64 rows of 96 5.0 to 5.4 us, of 64 4.9.
 // ---------------------------------------------------------------------------------------------
 template <int D, int W>
 __global__ __launch_bounds__(256) void attend_combine_kernel(const AttendArgs a) {

@@ -37,9 +37,9 @@ __device__ __forceinline__ float block_step(unsigned byte) { return __uint_as_fl
 // steps of 1/8 below 2): by blocks of 32 dims, q / 2^e = x0 + 2^-4 x1 + 2^-9 x2 + 2^-14 x3, where 2^e is the
 // smallest power of two with max |q| <= 7.5 * 2^e, and each x is what those before it leave, in its unit,
 // rounded.  x0 leaves at most 2^-2 (2^-4 of values below 2), x1 2^-8, x2 2^-13, x3 2^-18: a bf16 value's 8
-// bits are exact down to 2^-10, and smaller values off by at most 2^-19 of the block's largest: log-sums come
-// out 4e-8 off, as from a bf16 cache (two rows of e4m3, which take the same time, left those over few keys
-// 5e-6 off, three of e2m3 3e-6 in 98% of the time).  A block with an infinity or NaN has scale bytes 255,
+// bits are exact down to 2^-10, and smaller values off by at most 2^-19 of the block's largest: log-sums of
+// normal queries come out 4e-8 off, as from a bf16 cache (two rows of e4m3, which take the same time, left those
+// over few keys 5e-6 off, three of e2m3 3e-6 in 98% of the time).  A block with an infinity or NaN has scale bytes 255,
 // which make its row's scores NaN.
 // ---------------------------------------------------------------------------------------------
 constexpr int kParts = 4;

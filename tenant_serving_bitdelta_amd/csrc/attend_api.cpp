@@ -40,7 +40,10 @@ constexpr int kPartSteps = 4;
 // 12 steps one long list among short ones would be waited for.
 // From 4 bits (64 sequences of up to the given length, 8 kv heads, one workgroup a unit against split and
 // joined): 2000 keys 28 against 37 us, 4000 46 against 50, 6000 66 against 63; 256 of up to 3000 108 against
-// 135.
+// 135.  Up to 32 steps one long list among short ones is waited for, which even batches and short ones in wide
+// tables gain from: 64 of 100 keys 7 against 13 us, of 1000 18 against 27; but one of 4000 among 63 of 100 34
+// against 17, among 63 of 1000 37 against 27, eight of 4000 among 56 of 500 36 against 27; one of 4000 among
+// 255 of 100 37 against 33, among 255 of 700 45 against 57.
 int direct_steps(int64_t units, int32_t dtype) {
   if (units < 512) return 6;
   return dtype == BITDELTA_KV_FP4 ? 32 : 12;
@@ -276,7 +279,9 @@ bitdelta_status run(bd::AttendArgs* a, const Plan& p, const bitdelta_kv_cache& c
       fp4 ? bd::launch_attend4_rows(*a, c.head_dim, p.columns, blocks, st)
           : bd::launch_attend_rows(*a, c.head_dim, fp8, p.columns, blocks, st));
   if (s != BITDELTA_OK || p.kind == Kind::kRows) return s;
-  // units of 32 pieces and more are few (64 rows of 96 pieces 5 us instead of 11)
+  // units of 32 pieces and more are few: 64 rows of 96 pieces 5 us instead of 11.  (The wider caches' would gain
+  // as much, 64 rows of 64 pieces 4.9 against 8.3, but the order of their sums, and with it the last bits of
+  // results they have had before, would be another.)
   const bool many = fp4 && p.row_workers >= 32 * p.row_units;
   return bd::status_of_hip(bd::launch_attend_combine(*a, c.head_dim, many, st));
 }

@@ -16,6 +16,8 @@
 // 4.6 thousand tokens of 8 heads written in 4 bits, 24 MB in 10.7 us, and read back in 7.8; 7 thousand of 4
 // heads written in e4m3, 22 MB in 9.2 us; four single tokens 3.5 us.  Of the short calls' times 3 us are the
 // launch and the chain offsets -> length -> table -> place; a workgroup per token took 15 us for the 10.7.
+// 65536 tokens of 8 heads: written in bf16 537 MB in 108 us (5.0 TB/s), e4m3 403 MB in 87 (4.6), 4 bits 340 MB
+// in 77 (4.4; 89 with a scale that is no power of two), read back in 101 (5.3), 77 (5.2) and 54 us (6.3).
 #include "bd_internal.h"
 #include "cache.h"
 
